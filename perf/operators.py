@@ -1,0 +1,403 @@
+"""The 8-bit expert products and the gradients of the experts' products, as cases to measure.
+
+Each case is one operator at one size.  `run` computes it either in plain torch operations in
+32 bits (`own` false) or through the framework's entry points (`own` true).
+
+Operators ("op" of a case):
+  quantize  rows or 128-row blocks of a matrix to e4m3, one power-of-two scale per 128 columns
+  product   y[r] = sum over blocks b of 128 columns of
+            x_scale[r, b] * w_scale[e, n / 128, b] * (xq[r, b] . wq[e, n, b]), rows grouped by
+            expert e; one group is the dense product
+  ffn       the experts' SwiGLU network over e4m3 weights: x quantized by rows, gate and up
+            products, silu(gate) * up quantized by rows, down product
+  dgrad     dx[r] = dy[r] W[e]             (gradient of y[r] = x[r] W[e]^T by its input)
+  wgrad     dW[e] = sum over e's rows of dy[r]^T x[r]   (... by its weight)
+"""
+import math
+
+import torch
+
+own = False
+
+F32, E8M0 = "f32", "e8m0"
+MAX_E4M3 = 448.0
+BLOCK = 128
+
+
+def listed():
+    return [
+        # a decode step's 256 tokens of a 7168-wide model on their way into the experts: latency
+        {"name": "quantize decode rows", "op": "quantize", "rows": 256, "K": 7168, "block": 1,
+         "dtype": "bf16", "scale": E8M0},
+        # a prefill batch of odd length held in 32 bits
+        {"name": "quantize prefill rows fp32", "op": "quantize", "rows": 8191, "K": 4096, "block": 1,
+         "dtype": "f32", "scale": F32},
+        # one projection of eight experts when the weights are loaded
+        {"name": "quantize weights", "op": "quantize", "rows": 8 * 14336, "K": 4096, "block": 128,
+         "dtype": "bf16", "scale": F32},
+        # a shared (dense) expert's down projection for a few tokens: latency
+        {"name": "product shared expert", "op": "product", "E": 1, "rows": 37, "slack": 0, "N": 7168,
+         "K": 2048, "dtype": "bf16", "scale": F32},
+        # the down projection of 256 experts for a decode step of 256 tokens, 8 experts each
+        {"name": "product decode", "op": "product", "E": 256, "rows": 2048, "slack": 0, "N": 7168,
+         "K": 2048, "dtype": "bf16", "scale": F32},
+        # the down projection of eight large experts for a prefill batch
+        {"name": "product prefill", "op": "product", "E": 8, "rows": 8192, "slack": 0, "N": 4096,
+         "K": 14336, "dtype": "bf16", "scale": E8M0},
+        # the whole expert network of a decode step: every expert's weights are read once
+        {"name": "ffn decode", "op": "ffn", "T": 256, "k": 8, "E": 256, "d": 7168, "F": 2048,
+         "scale": E8M0},
+        # ... and of a prefill batch: bound by the matrix units
+        {"name": "ffn prefill", "op": "ffn", "T": 4096, "k": 2, "E": 8, "d": 4096, "F": 14336,
+         "scale": F32},
+        # a gradient check's size in 32 bits: latency
+        {"name": "dgrad small fp32", "op": "dgrad", "E": 8, "rows": 128, "slack": 5, "N": 256,
+         "K": 128, "dtype": "f32"},
+        # a training batch through the gate projection of eight large experts
+        {"name": "dgrad train", "op": "dgrad", "E": 8, "rows": 8191, "slack": 0, "N": 14336,
+         "K": 4096, "dtype": "bf16"},
+        # weight gradients of one GPU's 32 experts: about a thousand rows each
+        {"name": "wgrad train", "op": "wgrad", "E": 32, "rows": 32767, "slack": 0, "N": 2048,
+         "K": 7168, "dtype": "bf16"},
+        # weight gradients in 32 bits, a few ragged rows for each expert
+        {"name": "wgrad ragged fp32", "op": "wgrad", "E": 8, "rows": 1001, "slack": 23, "N": 1024,
+         "K": 512, "dtype": "f32"},
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def _wide(rng, lo, hi):
+    return 128 * max(1, _log(rng, lo / 128, hi / 128))
+
+
+def draw(rng):
+    op = rng.choice(["quantize", "product", "ffn", "dgrad", "wgrad"])
+    if op == "quantize":
+        block, K = rng.choice([1, 1, 128]), _wide(rng, 128, 16384)
+        rows = _log(rng, 1, (1 << 29) // K)
+        return {"op": op, "rows": max(1, rows // block) * block, "K": K, "block": block,
+                "dtype": rng.choice(["bf16", "bf16", "f32"]), "scale": rng.choice([F32, E8M0])}
+    E = rng.choice([1, 3, 8, 16, 32, 64, 128, 256])
+    if op == "ffn":
+        d, F = _wide(rng, 128, 8192), _wide(rng, 128, 16384)
+        while E * d * F > 1 << 31 and E > 1:
+            E = max(1, E // 2)
+        T = _log(rng, 1, min(4096, max(2, int(3e11 / (d * F)))))
+        return {"op": op, "T": T, "k": min(E, rng.choice([1, 2, 6, 8])), "E": E, "d": d, "F": F,
+                "scale": rng.choice([F32, E8M0])}
+    N, K = _wide(rng, 128, 16384), _wide(rng, 128, 16384)
+    while E * N * K > 1 << 31 and E > 1:
+        E = max(1, E // 2)
+    dtype = rng.choice(["bf16", "bf16", "f32"])
+    # the matrix units do 32-bit products at a sixteenth of the 16-bit rate
+    most = 4e11 if op == "product" or dtype == "bf16" else 4e10
+    rows = _log(rng, 1, min(32768, max(2, int(most / (N * K)))))
+    case = {"op": op, "E": E, "rows": rows, "slack": rng.choice([0, 0, 1, 77]), "N": N, "K": K,
+            "dtype": dtype}
+    if op == "product":
+        case["scale"] = rng.choice([F32, E8M0])
+    return case
+
+
+# ------------------------------------------------------------------------------------ inputs
+def _type(name):
+    return torch.bfloat16 if name == "bf16" else torch.float32
+
+
+def _generator(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _normal(shape, g, dtype, std=1.0):
+    return torch.randn(shape, generator=g, device="cuda", dtype=dtype).mul_(std)
+
+
+def _e4m3(shape, g):
+    """e4m3 values as a quantizer leaves them: normal, the largest of a block near 448."""
+    v = torch.randn(shape, generator=g, device="cuda", dtype=torch.bfloat16)
+    return v.mul_(112).clamp_(-MAX_E4M3, MAX_E4M3).to(torch.float8_e4m3fn)
+
+
+def _scales(shape, g, kind, size):
+    """Scales about `size`: any fp32 values, or powers of two as exponent bytes (bias 127)."""
+    v = torch.rand(shape, generator=g, device="cuda").add_(0.5).mul_(size)
+    if kind == F32:
+        return v
+    return v.log2_().round_().add_(127).to(torch.uint8)
+
+
+def _groups(rows, E, g):
+    """Offsets [E + 1] of `rows` rows dealt to E experts of unequal popularity."""
+    p = (0.5 * torch.randn(E, generator=g, device="cuda")).exp_()
+    e = torch.multinomial(p, rows, replacement=True, generator=g)
+    counts = torch.bincount(e, minlength=E)
+    offsets = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    offsets[1:] = counts.cumsum(0)
+    return offsets, int(counts.max())
+
+
+def prepare(case, seed):
+    g = _generator(seed)
+    s = dict(case)
+    op = case["op"]
+    if op == "quantize":
+        x = _normal((case["rows"], case["K"]), g, _type(case["dtype"]))
+        # columns of unequal size, as activations and weights have them
+        x.mul_(torch.randn(case["K"], generator=g, device="cuda").mul_(0.5).exp_().to(x.dtype))
+        s["x"] = x
+        s["q"] = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device="cuda")
+        shape = (case["rows"] // case["block"], case["K"] // BLOCK)
+        s["x_scale"] = torch.empty(shape, device="cuda",
+                                   dtype=torch.float32 if case["scale"] == F32 else torch.uint8)
+        return s
+    E = case["E"]
+    if op == "ffn":
+        T, k, d, F = case["T"], case["k"], case["d"], case["F"]
+        s["x"] = _normal((T, d), g, torch.bfloat16)
+        score = torch.randn((T, E), generator=g, device="cuda")
+        score.add_(torch.randn(E, generator=g, device="cuda").mul_(0.5))
+        chosen = score.topk(k, dim=1).indices.reshape(-1)
+        order = torch.argsort(chosen, stable=True)
+        s["src_token"] = (order // k).to(torch.int32)
+        counts = torch.bincount(chosen, minlength=E)
+        s["offsets"] = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+        s["offsets"][1:] = counts.cumsum(0)
+        s["most"] = int(counts.max())
+        for name, n, kk in (("w_gate", F, d), ("w_up", F, d), ("w_down", d, F)):
+            s[name] = _e4m3((E, n, kk), g)
+            s[name + "_scale"] = _scales((E, n // BLOCK, kk // BLOCK), g, case["scale"],
+                                         1 / (112 * math.sqrt(kk)))
+        s["y"] = torch.zeros((T * k, d), dtype=torch.bfloat16, device="cuda")
+        return s
+    rows, N, K = case["rows"], case["N"], case["K"]
+    s["R"] = rows + case["slack"]
+    s["offsets"], s["most"] = _groups(rows, E, g)
+    dt = _type(case["dtype"])
+    if op == "product":
+        s["xq"] = _e4m3((s["R"], K), g)
+        s["x_scale"] = _scales((s["R"], K // BLOCK), g, case["scale"], 1 / 112)
+        s["wq"] = _e4m3((E, N, K), g)
+        s["w_scale"] = _scales((E, N // BLOCK, K // BLOCK), g, case["scale"],
+                               1 / (112 * math.sqrt(K)))
+        s["y"] = torch.zeros((s["R"], N), dtype=dt, device="cuda")
+        return s
+    # what lies behind the last expert's rows is not the operator's to read
+    s["dy"] = _normal((s["R"], N), g, dt)
+    s["dy"][rows:] = math.nan
+    if op == "dgrad":
+        s["w"] = _normal((E, N, K), g, dt, 1 / math.sqrt(N))
+        s["dx"] = torch.zeros((s["R"], K), dtype=dt, device="cuda")
+    else:
+        s["x"] = _normal((s["R"], K), g, dt)
+        s["x"][rows:] = math.nan
+        s["dw"] = torch.empty((E, N, K), dtype=dt, device="cuda")
+    return s
+
+
+# ------------------------------------------------------------------------------- plain forms
+def _power(e):
+    """2^e in 32 bits for whole e from -126 to 127, by its bits: a power function may be off."""
+    return ((e.to(torch.int32) + 127) << 23).view(torch.float32)
+
+
+def _plain_scale(scale):
+    return scale if scale.dtype == torch.float32 else _power(scale.to(torch.int32) - 127)
+
+
+def _plain_exponent(most):
+    """The smallest e with most <= 448 * 2^e, at least -126; 0 for an all-zero block."""
+    m, e = torch.frexp(most)  # most = m * 2^e, 0.5 <= m < 1; 448 = 0.875 * 2^9
+    e = torch.where(m > 0.875, e - 8, e - 9).clamp(min=-126)
+    return torch.where(most > 0, e, torch.zeros_like(e))
+
+
+def _plain_quantize(x, block):
+    """q (as fp32 values) [rows, K] and the exponents [rows / block, K / 128]."""
+    rows, K = x.shape
+    v = x.float().view(rows // block, block, K // BLOCK, BLOCK)
+    e = _plain_exponent(v.abs().amax(dim=(1, 3)))
+    v = v * _power(-e)[:, None, :, None]
+    return v.to(torch.float8_e4m3fn).view(rows, K), e
+
+
+def _plain_dequantize(q, scale, block):
+    rows, K = q.shape[-2:]
+    v = q.float().view(-1, rows // block, block, K // BLOCK, BLOCK)
+    v = v * scale.reshape(-1, rows // block, 1, K // BLOCK, 1)
+    return v.view(q.shape)
+
+
+def _pad(x, offsets, most):
+    """Rows of x by expert, [E, most, K], zero where an expert has fewer; the places too."""
+    i = torch.arange(most, device=x.device)
+    place = offsets[:-1, None].long() + i
+    live = place < offsets[1:, None]
+    rows = x[place.clamp(max=x.shape[0] - 1)].float()
+    return torch.where(live[:, :, None], rows, torch.zeros_like(rows)), place[live], live
+
+
+def _plain(s):
+    op = s["op"]
+    if op == "quantize":
+        q, e = _plain_quantize(s["x"], s["block"])
+        return {"q": q, "scale": _power(e) if s["scale"] == F32 else (e + 127).to(torch.uint8)}
+    if op == "product":
+        x, place, live = _pad(_plain_dequantize(s["xq"], _plain_scale(s["x_scale"]), 1),
+                              s["offsets"], s["most"])
+        w = _plain_dequantize(s["wq"], _plain_scale(s["w_scale"]), BLOCK)
+        y = torch.bmm(x, w.transpose(1, 2))
+        s["y"][place] = y[live].to(s["y"].dtype)
+        return s["y"]
+    if op == "ffn":
+        q, e = _plain_quantize(s["x"], 1)
+        x = _plain_dequantize(q, _power(e), 1)
+        x, place, live = _pad(x[s["src_token"].long()], s["offsets"], s["most"])
+        w = _plain_dequantize(s["w_gate"], _plain_scale(s["w_gate_scale"]), BLOCK)
+        gate = torch.bmm(x, w.transpose(1, 2))
+        w = _plain_dequantize(s["w_up"], _plain_scale(s["w_up_scale"]), BLOCK)
+        h = gate * torch.sigmoid(gate) * torch.bmm(x, w.transpose(1, 2))
+        q, e = _plain_quantize(h.view(-1, s["F"]), 1)
+        h = _plain_dequantize(q, _power(e), 1)
+        w = _plain_dequantize(s["w_down"], _plain_scale(s["w_down_scale"]), BLOCK)
+        y = torch.bmm(h.view(s["E"], -1, s["F"]), w.transpose(1, 2))
+        s["y"][place] = y[live].to(s["y"].dtype)
+        return s["y"]
+    dy, place, live = _pad(s["dy"], s["offsets"], s["most"])
+    if op == "dgrad":
+        dx = torch.bmm(dy, s["w"].float())
+        s["dx"][place] = dx[live].to(s["dx"].dtype)
+        return s["dx"]
+    x, _, _ = _pad(s["x"], s["offsets"], s["most"])
+    return torch.bmm(dy.transpose(1, 2), x).to(s["dw"].dtype)
+
+
+# -------------------------------------------------------------------------- the framework's
+def _own(s):
+    import routing_expert_ffn_router_amd as moe
+
+    op = s["op"]
+    kind = moe.MOE_SCALE_F32 if s.get("scale") == F32 else moe.MOE_SCALE_E8M0
+    if op == "quantize":
+        moe.quantize(s["x"], s["block"], kind, s["q"], s["x_scale"])
+        return {"q": s["q"], "scale": s["x_scale"]}
+    if op == "ffn":
+        if "shape" not in s:
+            s["shape"] = moe.shape(s["T"], s["d"], s["E"], s["k"], s["F"])
+            s["workspace"] = torch.empty(moe.fp8_workspace_size(s["shape"], kind),
+                                         dtype=torch.uint8, device="cuda")
+        moe.expert_ffn_fp8(s["shape"], kind, s["x"], s["src_token"], s["offsets"],
+                           (s["w_gate"], s["w_gate_scale"]), (s["w_up"], s["w_up_scale"]),
+                           (s["w_down"], s["w_down_scale"]), s["workspace"], s["y"])
+        return s["y"]
+    if "shape" not in s:
+        dt = moe.MOE_BF16 if s["dtype"] == "bf16" else moe.MOE_F32
+        s["shape"] = moe.group_shape(s["R"], s["E"], s["N"], s["K"], dt, kind)
+        s["workspace"] = torch.empty(moe.group_workspace_size(s["shape"]), dtype=torch.uint8,
+                                     device="cuda")
+    if op == "product":
+        moe.grouped_gemm_fp8(s["shape"], s["xq"], s["x_scale"], s["offsets"], s["wq"],
+                             s["w_scale"], s["workspace"], s["y"])
+        return s["y"]
+    if op == "dgrad":
+        moe.grouped_dgrad(s["shape"], s["dy"], s["offsets"], s["w"], s["workspace"], s["dx"])
+        return s["dx"]
+    moe.grouped_wgrad(s["shape"], s["dy"], s["x"], s["offsets"], s["workspace"], s["dw"])
+    return s["dw"]
+
+
+def run(state):
+    return _own(state) if own else _plain(state)
+
+
+# ------------------------------------------------------------------------------ in 64 bits
+def _exact_power(e):
+    return ((e.to(torch.int64) + 1023) << 52).view(torch.float64)
+
+
+def _exact_values(q, scale, block):
+    """The numbers that e4m3 values and their scales stand for, in 64 bits."""
+    s = scale.double() if scale.dtype == torch.float32 else _exact_power(scale.to(torch.int64) - 127)
+    s = s.repeat_interleave(block, -2).repeat_interleave(BLOCK, -1)
+    return q.to(torch.float32).double() * s
+
+
+def _exact_quantize(x, block):
+    """(e4m3 values, scales) in 64 bits: scale 2^e, the least that brings a block to 448."""
+    rows, K = x.shape
+    most = x.double().abs().view(rows // block, block, K // BLOCK, BLOCK).amax(3).amax(1)
+    part, e = torch.frexp(most / MAX_E4M3)  # part * 2^e, 0.5 <= part < 1
+    e = torch.where(part > 0.5, e, e - 1).clamp(min=-126)
+    scale = _exact_power(torch.where(most > 0, e, torch.zeros_like(e)))
+    v = x.double() / scale.repeat_interleave(block, 0).repeat_interleave(BLOCK, 1)
+    # e4m3: four significant bits, no step below 2^-9
+    step = _exact_power(torch.frexp(v).exponent.clamp(min=-5) - 4)
+    return torch.round(v / step) * step, scale
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    op = case["op"]
+    if op == "quantize":
+        v, scale = _exact_quantize(s["x"], case["block"])
+        return {"q": v, "scale": scale if case["scale"] == F32 else None}
+    at = s["offsets"].tolist()
+    spans = [(e, a, b) for e, (a, b) in enumerate(zip(at, at[1:])) if b > a]
+    if op == "product":
+        y = torch.zeros(s["y"].shape, dtype=torch.float64, device="cuda")
+        for e, a, b in spans:
+            w = _exact_values(s["wq"][e], s["w_scale"][e], BLOCK)
+            y[a:b] = _exact_values(s["xq"][a:b], s["x_scale"][a:b], 1) @ w.t()
+        return y
+    if op == "ffn":
+        v, scale = _exact_quantize(s["x"], 1)
+        x = v * scale.repeat_interleave(BLOCK, 1)
+        y = torch.zeros(s["y"].shape, dtype=torch.float64, device="cuda")
+        for e, a, b in spans:
+            rows = x[s["src_token"][a:b].long()]
+            gate = rows @ _exact_values(s["w_gate"][e], s["w_gate_scale"][e], BLOCK).t()
+            up = rows @ _exact_values(s["w_up"][e], s["w_up_scale"][e], BLOCK).t()
+            v, scale = _exact_quantize(gate / (1 + torch.exp(-gate)) * up, 1)
+            h = v * scale.repeat_interleave(BLOCK, 1)
+            y[a:b] = h @ _exact_values(s["w_down"][e], s["w_down_scale"][e], BLOCK).t()
+        return y
+    if op == "dgrad":
+        dx = torch.zeros(s["dx"].shape, dtype=torch.float64, device="cuda")
+        for e, a, b in spans:
+            dx[a:b] = s["dy"][a:b].double() @ s["w"][e].double()
+        return dx
+    dw = torch.zeros(s["dw"].shape, dtype=torch.float64, device="cuda")
+    for e, a, b in spans:
+        dw[e] = s["dy"][a:b].double().t() @ s["x"][a:b].double()
+    return dw
+
+
+# ------------------------------------------------------------------------------------- work
+def work(case):
+    op = case["op"]
+    size = 2 if case.get("dtype", "bf16") == "bf16" else 4
+    per_scale = 4 if case.get("scale") == F32 else 1
+    if op == "quantize":
+        n = case["rows"] * case["K"]
+        scales = n // case["block"] // BLOCK
+        return {"bytes": n * (size + 1) + scales * per_scale, "flops": 2 * n}
+    E = case["E"]
+    R = case["T"] * case["k"] if op == "ffn" else case["rows"]
+    live = E * (1 - (1 - 1 / E) ** R)  # experts that get a row: the others' weights stay unread
+    if op == "ffn":
+        weights = 3 * live * case["d"] * case["F"]
+        data = case["T"] * case["d"] * 2 + R * (4 + case["d"] * 2)
+        return {"bytes": weights * (1 + per_scale / BLOCK ** 2) + data,
+                "flops": 6 * R * case["d"] * case["F"]}
+    N, K = case["N"], case["K"]
+    flops = 2 * R * N * K
+    if op == "product":
+        return {"bytes": R * K * (1 + per_scale / BLOCK) + R * N * size
+                + live * N * K * (1 + per_scale / BLOCK ** 2), "flops": flops}
+    if op == "dgrad":
+        return {"bytes": (R * (N + K) + live * N * K) * size, "flops": flops}
+    return {"bytes": (R * (N + K) + E * N * K) * size, "flops": flops}
