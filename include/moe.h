@@ -417,6 +417,151 @@ int moe_layer(const moe_shape* shape, const void* x, const void* w_router,
               int32_t* tokens_per_expert, int32_t* drops, int32_t* status,
               hipStream_t stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Expert weights in 8-bit floating point, and the gradients of the experts' products.
+ *
+ * 8-bit values are OCP e4m3 (one byte, largest 448, 0x7f / 0xff NaN, no infinities) with one
+ * scale for each block of 128: an activation row [K] has K / 128 scales, a weight matrix
+ * [N, K] has [N / 128, K / 128] of them, one for each 128 x 128 block.  A value stands for
+ * e4m3 * scale.  Scales are contiguous row-major arrays of one of two types:
+ *   MOE_SCALE_F32   float: any finite value (block scales as checkpoints store them)
+ *   MOE_SCALE_E8M0  one byte v, standing for 2^(v - 127); 255 stands for NaN.  The matrix
+ *                   instruction multiplies these itself.
+ * [EP-checks] "Memory must be counted by phase": expert weights are the largest line of the
+ * memory sheet, and a decode step reads all of them.
+ *
+ * Precision of the 8-bit products: sums are held in fp32, but the 8-bit matrix instruction adds
+ * eight neighbouring products at a time and cuts them off 13 bits below the largest (measured
+ * on MI355X; 1.3e-5 of the result's norm on normal data).  Outputs are therefore bf16, whose
+ * half step is 2^-8 of a value at most, and MOE_F32 is refused.
+ * ------------------------------------------------------------------------------------------ */
+typedef enum { MOE_SCALE_F32 = 0, MOE_SCALE_E8M0 = 1 } moe_scale_type;
+
+/* A tensor of e4m3 values and its scales (device pointers). */
+typedef struct {
+  const void* q;
+  const void* scale;
+} moe_fp8_tensor;
+
+/* A product grouped by expert: rows [expert_offsets[e], expert_offsets[e + 1]) of the row
+ * operands belong to expert e, whose weight is matrix e of [E, N, K].  Groups may be empty and
+ * of any length.  Limits: 0 <= rows < 2^31, 1 <= E <= 1024, N and K multiples of 128 and at
+ * most 2^20, and a grid within 2^32 threads. */
+typedef struct {
+  int64_t rows;       /* row slots of the row operands */
+  int64_t E;          /* experts */
+  int64_t N;          /* output width of the product, x W^T */
+  int64_t K;          /* input width */
+  int32_t dtype;      /* moe_dtype of the operands (gradients) or of the output (8-bit) */
+  int32_t scale_type; /* moe_scale_type of the 8-bit operands; the gradients ignore it */
+} moe_group_shape;
+
+/* Bytes of device workspace the three grouped entry points below need (the tile table); 0 for
+ * an invalid shape.  Host function. */
+size_t moe_group_workspace_size(const moe_group_shape* shape);
+
+/*
+ * moe_quantize -- a matrix to e4m3 with a power-of-two scale for each block of block_rows x 128
+ * values: block_rows 1 for activations, 128 for weights ([E, N, K] as E * N rows).
+ * The scale is 2^e with the least e >= -126 for which the block's largest magnitude is at most
+ * 448 * 2^e (1 for a block of zeros); q = x / 2^e rounded to nearest even.  The division is
+ * exact, so a value is rounded once.  A block that holds an infinity or a NaN becomes all NaN:
+ * q 0x7f throughout and a NaN scale (255 for MOE_SCALE_E8M0).
+ *   x      [rows, K] dtype in; rows a multiple of block_rows, K of 128
+ *   q      [rows, K] e4m3 out
+ *   scale  [rows / block_rows, K / 128] scale_type out
+ * x and q must be 16-byte aligned; rows * K < 2^37.  rows = 0 is valid.
+ */
+int moe_quantize(int64_t rows, int64_t K, int64_t block_rows, int dtype, int scale_type,
+                 const void* x, void* q, void* scale, hipStream_t stream);
+
+/*
+ * moe_grouped_gemm_fp8 -- product of 8-bit operands grouped by expert:
+ *   y[r, n] = sum over blocks b of x_scale[r, b] * w_scale[e, n / 128, b] *
+ *             (sum over the 128 columns c of b of xq[r, c] * wq[e, n, c])
+ * for the rows r of expert e.  Rows >= expert_offsets[E] of y are not written.
+ *   xq, x_scale     [rows, K], [rows, K / 128] in
+ *   expert_offsets  [E+1] int32 in (non-decreasing, expert_offsets[E] <= rows); NULL with
+ *                   E = 1: the dense product, every row belongs to the one matrix
+ *   wq, w_scale     [E, N, K], [E, N / 128, K / 128] in
+ *   workspace       moe_group_workspace_size() bytes, 256-byte aligned
+ *   y               [rows, N] bf16 out
+ * shape->dtype must be MOE_BF16.
+ */
+int moe_grouped_gemm_fp8(const moe_group_shape* shape, const void* xq, const void* x_scale,
+                         const int32_t* expert_offsets, const void* wq, const void* w_scale,
+                         void* workspace, size_t workspace_bytes, void* y, hipStream_t stream);
+
+/*
+ * moe_grouped_dgrad -- gradient of y[r] = x[r] W[e]^T (moe_expert_down, and each product of
+ * moe_expert_gate_up) by its input: dx[r, k] = sum over n of dy[r, n] * w[e, n, k].
+ * Accumulated in fp32, rounded once to dtype.  Rows >= expert_offsets[E] of dx are not written
+ * and those of dy not read.
+ *   dy [rows, N] dtype in; w [E, N, K] dtype in; dx [rows, K] dtype out
+ *   expert_offsets and workspace as in moe_grouped_gemm_fp8
+ */
+int moe_grouped_dgrad(const moe_group_shape* shape, const void* dy,
+                      const int32_t* expert_offsets, const void* w, void* workspace,
+                      size_t workspace_bytes, void* dx, hipStream_t stream);
+
+/*
+ * moe_grouped_wgrad -- the same product's gradient by its weight:
+ *   dw[e, n, k] = sum over the rows r of expert e of dy[r, n] * x[r, k]
+ * accumulated in fp32 in row order, rounded once to dtype.  The matrix of an expert without
+ * rows is written as zeros.  Rows >= expert_offsets[E] of dy and x are not read.
+ *   dy [rows, N] dtype in; x [rows, K] dtype in; dw [E, N, K] dtype out
+ *   expert_offsets and workspace as in moe_grouped_gemm_fp8
+ */
+int moe_grouped_wgrad(const moe_group_shape* shape, const void* dy, const void* x,
+                      const int32_t* expert_offsets, void* workspace, size_t workspace_bytes,
+                      void* dw, hipStream_t stream);
+
+/* Bytes of device workspace for moe_expert_ffn_fp8 and moe_layer_fp8 (the same size serves
+ * both); 0 for an invalid shape or scale type, or a dtype other than MOE_BF16.  Host function. */
+size_t moe_fp8_workspace_size(const moe_shape* shape, int scale_type);
+
+/* Byte offsets of the regions in that workspace, as moe_workspace_layout; MOE_WS_X_PERM holds
+ * the quantized rows of x and, 256-byte aligned behind them, their scales; MOE_WS_H likewise
+ * the quantized hidden rows.  Returns a moe_status.  Host function. */
+int moe_fp8_workspace_layout(const moe_shape* shape, int scale_type, int64_t* offsets);
+
+/*
+ * moe_expert_ffn_fp8 -- moe_expert_ffn with 8-bit weights.  Each row of x is quantized as by
+ * moe_quantize (block_rows 1); gate and up are 8-bit products (moe_grouped_gemm_fp8, held in
+ * fp32); h = silu(gate) * up is quantized by rows in the product's epilogue, without a
+ * rounding before it; y_perm is the 8-bit product of h with w_down, rounded to bf16.
+ * Same sources as moe_expert_ffn.
+ *   x               with src_token: [T, d] bf16, row r of expert e reads x[src_token[r]] (an
+ *                   entry outside [0, T), such as an empty padded slot's -1, reads a row of x
+ *                   all the same: its row of y_perm is unspecified); without (NULL): x_perm
+ *                   [R, d] bf16, R = moe_max_rows
+ *   expert_offsets  [E+1] int32 in (non-decreasing, expert_offsets[E] <= R)
+ *   w_gate, w_up    [E, F, d] with scales [E, F / 128, d / 128]; w_down [E, d, F] with scales
+ *                   [E, d / 128, F / 128], all of scale_type
+ *   workspace       moe_fp8_workspace_size() bytes, 256-byte aligned
+ *   y_perm          [R, d] bf16 out; rows >= expert_offsets[E] are not written
+ * shape->dtype must be MOE_BF16; max(T, R) * d and max(T, R) * F at most 2^37, and with
+ * src_token T * d < 2^31 (MOE_ERR_UNSUPPORTED otherwise).
+ */
+int moe_expert_ffn_fp8(const moe_shape* shape, int scale_type, const void* x,
+                       const int32_t* src_token, const int32_t* expert_offsets,
+                       const moe_fp8_tensor* w_gate, const moe_fp8_tensor* w_up,
+                       const moe_fp8_tensor* w_down, void* workspace, size_t workspace_bytes,
+                       void* y_perm, hipStream_t stream);
+
+/*
+ * moe_layer_fp8 -- moe_layer with 8-bit expert weights: the router reads bf16 x and w_router as
+ * there, the dispatch builds its tables only, and the experts run as moe_expert_ffn_fp8 over the
+ * gathered rows.  Needs T * d < 2^31 (MOE_ERR_UNSUPPORTED otherwise).
+ * Arguments as in moe_layer and moe_expert_ffn_fp8.
+ */
+int moe_layer_fp8(const moe_shape* shape, int scale_type, const void* x, const void* w_router,
+                  const float* b_router, const moe_fp8_tensor* w_gate,
+                  const moe_fp8_tensor* w_up, const moe_fp8_tensor* w_down, void* workspace,
+                  size_t workspace_bytes, void* out, int32_t* routed_counts,
+                  int32_t* tokens_per_expert, int32_t* drops, int32_t* status,
+                  hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

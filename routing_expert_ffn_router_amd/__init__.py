@@ -28,6 +28,9 @@ DISPATCH_SCRATCH_BYTES = 8 << 20  # MOE_DISPATCH_SCRATCH_BYTES
 MOE_F32 = 0
 MOE_BF16 = 1
 
+MOE_SCALE_F32 = 0
+MOE_SCALE_E8M0 = 1
+
 MOE_FLAG_PAD_TO_CAPACITY = 1
 MOE_FLAG_SLOT_MAJOR = 2
 MOE_FLAG_BIAS_SELECTION_ONLY = 4
@@ -50,6 +53,23 @@ class MoeShape(ctypes.Structure):
                 f"capacity={self.capacity}, dtype={'bf16' if self.dtype == 1 else 'f32'}, "
                 f"flags={self.flags}, n_groups={self.n_groups}, "
                 f"topk_groups={self.topk_groups})")
+
+
+class MoeGroupShape(ctypes.Structure):
+    """moe_group_shape: a product grouped by expert (see include/moe.h)."""
+    _fields_ = [("rows", ctypes.c_int64), ("E", ctypes.c_int64), ("N", ctypes.c_int64),
+                ("K", ctypes.c_int64), ("dtype", ctypes.c_int32),
+                ("scale_type", ctypes.c_int32)]
+
+    def __repr__(self):
+        return (f"MoeGroupShape(rows={self.rows}, E={self.E}, N={self.N}, K={self.K}, "
+                f"dtype={'bf16' if self.dtype == 1 else 'f32'}, "
+                f"scale_type={'e8m0' if self.scale_type == 1 else 'f32'})")
+
+
+class MoeFp8Tensor(ctypes.Structure):
+    """moe_fp8_tensor: e4m3 values and their scales (device pointers)."""
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
 
 
 class ExpertStats(ctypes.Structure):
@@ -77,6 +97,8 @@ class MoeError(RuntimeError):
 _lib = None
 _P = ctypes.c_void_p
 _S = ctypes.POINTER(MoeShape)
+_G = ctypes.POINTER(MoeGroupShape)
+_W = ctypes.POINTER(MoeFp8Tensor)
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -119,6 +141,16 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_combine": (i32, [_S, _P, _P, _P, _P, _P]),
         "moe_slot_counts": (i32, [_S, _P, _P, _P, _P, _P]),
         "moe_layer": (i32, [_S, _P, _P, _P, _P, _P, _P, _P, sz, _P, _P, _P, _P, _P, _P]),
+        "moe_group_workspace_size": (sz, [_G]),
+        "moe_quantize": (i32, [i64, i64, i64, i32, i32, _P, _P, _P, _P]),
+        "moe_grouped_gemm_fp8": (i32, [_G, _P, _P, _P, _P, _P, _P, sz, _P, _P]),
+        "moe_grouped_dgrad": (i32, [_G, _P, _P, _P, _P, sz, _P, _P]),
+        "moe_grouped_wgrad": (i32, [_G, _P, _P, _P, _P, sz, _P, _P]),
+        "moe_fp8_workspace_size": (sz, [_S, i32]),
+        "moe_fp8_workspace_layout": (i32, [_S, i32, ctypes.POINTER(i64)]),
+        "moe_expert_ffn_fp8": (i32, [_S, i32, _P, _P, _P, _W, _W, _W, _P, sz, _P, _P]),
+        "moe_layer_fp8": (i32, [_S, i32, _P, _P, _P, _W, _W, _W, _P, sz, _P, _P, _P, _P, _P,
+                                _P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -132,7 +164,7 @@ def header_functions(path: str = HEADER_PATH) -> list:
     """Names of the functions include/moe.h declares."""
     text = open(path).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
-    return sorted(set(re.findall(r"\b(moe_[a-z_]+)\s*\(", text)))
+    return sorted(set(re.findall(r"\b(moe_[a-z0-9_]+)\s*\(", text)))
 
 
 def status_string(status: int) -> str:
@@ -437,6 +469,233 @@ class MoELayer:
         yield "down"
         combine(s, v("y_perm"), v("dest_row"), v("topk_w"), self.out, stream=stream)
         yield "combine"
+
+
+# ------------------------------------------------------- 8-bit products and gradients
+def group_shape(rows: int, E: int, N: int, K: int, dtype: int = MOE_BF16,
+                scale_type: int = MOE_SCALE_F32) -> MoeGroupShape:
+    return MoeGroupShape(rows, E, N, K, dtype, scale_type)
+
+
+def group_workspace_size(g: MoeGroupShape) -> int:
+    return int(load_library().moe_group_workspace_size(ctypes.byref(g)))
+
+
+def fp8_workspace_size(s: MoeShape, scale_type: int = MOE_SCALE_F32) -> int:
+    return int(load_library().moe_fp8_workspace_size(ctypes.byref(s), scale_type))
+
+
+def fp8_workspace_layout(s: MoeShape, scale_type: int = MOE_SCALE_F32) -> dict:
+    offs = (ctypes.c_int64 * len(WS_REGIONS))()
+    _check("moe_fp8_workspace_layout",
+           load_library().moe_fp8_workspace_layout(ctypes.byref(s), scale_type, offs))
+    return {n: int(o) for n, o in zip(WS_REGIONS, offs)}
+
+
+def _act_dtype(dtype: int):
+    import torch
+
+    return torch.bfloat16 if dtype == MOE_BF16 else torch.float32
+
+
+def _arg(t, name: str, dtypes, shape) -> Optional[int]:
+    """The device pointer of a tensor that an entry point reads or writes in whole: contiguous,
+    of one of `dtypes`, exactly `shape`, on the current GPU."""
+    import torch
+
+    if t is None:
+        raise ValueError(f"{name} is missing")
+    if not isinstance(dtypes, tuple):
+        dtypes = (dtypes,)
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} is {t.dtype}, not {' or '.join(str(d) for d in dtypes)}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} is not contiguous")
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current GPU")
+    return t.data_ptr()
+
+
+def _ws_arg(t):
+    import torch
+
+    if t is None:
+        return None, 0
+    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"workspace is on {t.device}, not on the current GPU")
+    if not t.is_contiguous():
+        raise ValueError("workspace is not contiguous")
+    return t.data_ptr(), _nbytes(t)
+
+
+def _e4m3_dtypes() -> tuple:
+    import torch
+
+    return torch.float8_e4m3fn, torch.uint8
+
+
+def _scale_dtypes(scale_type: int) -> tuple:
+    import torch
+
+    if scale_type == MOE_SCALE_E8M0:
+        return torch.uint8, torch.float8_e8m0fnu
+    return (torch.float32,)
+
+
+def _fp8_weight(w, name: str, scale_type: int, E: int, N: int, K: int) -> MoeFp8Tensor:
+    q, scale = w
+    return MoeFp8Tensor(
+        _arg(q, name, _e4m3_dtypes(), (E, N, K)),
+        _arg(scale, f"{name}'s scale", _scale_dtypes(scale_type), (E, N // 128, K // 128)))
+
+
+def _offsets_arg(t, E: int):
+    import torch
+
+    return None if t is None else _arg(t, "expert_offsets", torch.int32, (E + 1,))
+
+
+def quantize(x, block_rows: int, scale_type: int, q, scale, stream=None) -> None:
+    """moe_quantize: x [..., K] (rows are the leading dimensions) to e4m3 q of x's shape and
+    scales of shape [rows / block_rows, K / 128], or of x's leading dimensions with the last one
+    divided by block_rows and K / 128."""
+    import torch
+
+    K = x.shape[-1]
+    rows = x.numel() // K if K else 0
+    ok = x.dim() >= 1 and K % 128 == 0 and K > 0 and block_rows in (1, 128) and \
+        rows % block_rows == 0
+    if ok:
+        flat = (rows // block_rows, K // 128)
+        lead = tuple(x.shape[:-1])
+        nested = lead[:-1] + (lead[-1] // block_rows, K // 128) if lead else flat
+        want = flat if tuple(scale.shape) == flat else nested
+        # nested scales of 128-row blocks: no block may span two matrices
+        if lead and lead[-1] % block_rows:
+            want = flat
+        xp = _arg(x, "x", (torch.bfloat16, torch.float32), x.shape)
+        qp = _arg(q, "q", _e4m3_dtypes(), x.shape)
+        sp = _arg(scale, "scale", _scale_dtypes(scale_type), want)
+    else:  # the library refuses it and says why
+        xp, qp, sp = _ptr(x), _ptr(q), _ptr(scale)
+    _check("moe_quantize", load_library().moe_quantize(
+        rows, K, block_rows, MOE_BF16 if x.dtype == torch.bfloat16 else MOE_F32, scale_type, xp,
+        qp, sp, _stream(stream)))
+
+
+def grouped_gemm_fp8(g: MoeGroupShape, xq, x_scale, expert_offsets, wq, w_scale, workspace, y,
+                     stream=None) -> None:
+    """moe_grouped_gemm_fp8: y[r] = dequantized xq[r] W[e]^T for the rows of each expert."""
+    w = _fp8_weight((wq, w_scale), "wq", g.scale_type, g.E, g.N, g.K)
+    ws, nbytes = _ws_arg(workspace)
+    _check("moe_grouped_gemm_fp8", load_library().moe_grouped_gemm_fp8(
+        ctypes.byref(g), _arg(xq, "xq", _e4m3_dtypes(), (g.rows, g.K)),
+        _arg(x_scale, "x_scale", _scale_dtypes(g.scale_type), (g.rows, g.K // 128)),
+        _offsets_arg(expert_offsets, g.E), w.q, w.scale, ws, nbytes,
+        _arg(y, "y", _act_dtype(g.dtype), (g.rows, g.N)), _stream(stream)))
+
+
+def grouped_dgrad(g: MoeGroupShape, dy, expert_offsets, w, workspace, dx, stream=None) -> None:
+    """moe_grouped_dgrad: dx[r] = dy[r] W[e] for the rows of each expert."""
+    dt = _act_dtype(g.dtype)
+    ws, nbytes = _ws_arg(workspace)
+    _check("moe_grouped_dgrad", load_library().moe_grouped_dgrad(
+        ctypes.byref(g), _arg(dy, "dy", dt, (g.rows, g.N)), _offsets_arg(expert_offsets, g.E),
+        _arg(w, "w", dt, (g.E, g.N, g.K)), ws, nbytes, _arg(dx, "dx", dt, (g.rows, g.K)),
+        _stream(stream)))
+
+
+def grouped_wgrad(g: MoeGroupShape, dy, x, expert_offsets, workspace, dw, stream=None) -> None:
+    """moe_grouped_wgrad: dw[e] = sum over the expert's rows of dy[r]^T x[r]."""
+    dt = _act_dtype(g.dtype)
+    ws, nbytes = _ws_arg(workspace)
+    _check("moe_grouped_wgrad", load_library().moe_grouped_wgrad(
+        ctypes.byref(g), _arg(dy, "dy", dt, (g.rows, g.N)), _arg(x, "x", dt, (g.rows, g.K)),
+        _offsets_arg(expert_offsets, g.E), ws, nbytes, _arg(dw, "dw", dt, (g.E, g.N, g.K)),
+        _stream(stream)))
+
+
+def expert_ffn_fp8(s: MoeShape, scale_type: int, x, src_token, expert_offsets, w_gate, w_up,
+                   w_down, workspace, y_perm, stream=None) -> None:
+    """moe_expert_ffn_fp8; each weight is a pair (e4m3 values, scales)."""
+    import torch
+
+    R = max_rows(s)
+    wg = _fp8_weight(w_gate, "w_gate", scale_type, s.E, s.F, s.d)
+    wu = _fp8_weight(w_up, "w_up", scale_type, s.E, s.F, s.d)
+    wd = _fp8_weight(w_down, "w_down", scale_type, s.E, s.d, s.F)
+    dt = _act_dtype(s.dtype)
+    src = None if src_token is None else _arg(src_token, "src_token", torch.int32, (R,))
+    ws, nbytes = _ws_arg(workspace)
+    _check("moe_expert_ffn_fp8", load_library().moe_expert_ffn_fp8(
+        ctypes.byref(s), scale_type,
+        _arg(x, "x", dt, (R if src is None else s.T, s.d)), src,
+        _offsets_arg(expert_offsets, s.E), ctypes.byref(wg), ctypes.byref(wu), ctypes.byref(wd),
+        ws, nbytes, _arg(y_perm, "y_perm", dt, (R, s.d)), _stream(stream)))
+
+
+def layer_fp8(s: MoeShape, scale_type: int, x, w_router, b_router, w_gate, w_up, w_down,
+              workspace, out, routed_counts=None, tokens_per_expert=None, drops=None,
+              status=None, stream=None) -> None:
+    """moe_layer_fp8; each expert weight is a pair (e4m3 values, scales)."""
+    import torch
+
+    wg = _fp8_weight(w_gate, "w_gate", scale_type, s.E, s.F, s.d)
+    wu = _fp8_weight(w_up, "w_up", scale_type, s.E, s.F, s.d)
+    wd = _fp8_weight(w_down, "w_down", scale_type, s.E, s.d, s.F)
+    dt, i32 = _act_dtype(s.dtype), torch.int32
+
+    def optional(t, name, dtype, n):
+        return None if t is None else _arg(t, name, dtype, (n,))
+
+    ws, nbytes = _ws_arg(workspace)
+    _check("moe_layer_fp8", load_library().moe_layer_fp8(
+        ctypes.byref(s), scale_type, _arg(x, "x", dt, (s.T, s.d)),
+        _arg(w_router, "w_router", dt, (s.E, s.d)),
+        optional(b_router, "b_router", torch.float32, s.E), ctypes.byref(wg), ctypes.byref(wu),
+        ctypes.byref(wd), ws, nbytes, _arg(out, "out", dt, (s.T, s.d)),
+        optional(routed_counts, "routed_counts", i32, s.E),
+        optional(tokens_per_expert, "tokens_per_expert", i32, s.E),
+        optional(drops, "drops", i32, s.k + 2), optional(status, "status", i32, 1),
+        _stream(stream)))
+
+
+class MoELayerFp8:
+    """Convenience owner of the workspace and outputs of moe_layer_fp8 for one shape, with
+    `quantize_weights` for weights that are held in bf16 or fp32."""
+
+    def __init__(self, s: MoeShape, scale_type: int = MOE_SCALE_E8M0, device="cuda"):
+        import torch
+
+        nbytes = fp8_workspace_size(s, scale_type)
+        if nbytes == 0:
+            raise MoeError("moe_fp8_workspace_size", MOE_ERR_UNSUPPORTED)
+        self.shape, self.scale_type = s, scale_type
+        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self.out = torch.empty((s.T, s.d), dtype=torch.bfloat16, device=device)
+        self.routed_counts = torch.empty(s.E, dtype=torch.int32, device=device)
+        self.tokens_per_expert = torch.empty(s.E, dtype=torch.int32, device=device)
+        self.drops = torch.empty(s.k + 2, dtype=torch.int32, device=device)
+        self.status = torch.empty(1, dtype=torch.int32, device=device)
+
+    def quantize_weights(self, w, stream=None) -> tuple:
+        """(e4m3 values, scales) of stacked weights [E, N, K], one scale per 128 x 128 block."""
+        import torch
+
+        E, N, K = w.shape
+        q = torch.empty((E, N, K), dtype=torch.float8_e4m3fn, device=w.device)
+        scale = torch.empty((E, N // 128, K // 128), device=w.device,
+                            dtype=_scale_dtypes(self.scale_type)[0])
+        quantize(w, 128, self.scale_type, q, scale, stream)
+        return q, scale
+
+    def __call__(self, x, w_router, b_router, w_gate, w_up, w_down, stream=None):
+        layer_fp8(self.shape, self.scale_type, x, w_router, b_router, w_gate, w_up, w_down,
+                  self.workspace, self.out, self.routed_counts, self.tokens_per_expert,
+                  self.drops, self.status, stream)
+        return self.out
 
 
 # ------------------------------------------------------------------------------ calibration

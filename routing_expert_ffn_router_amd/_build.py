@@ -20,7 +20,7 @@ LIB = os.path.join(PKG, "libmoe.so")
 STAMP = os.path.join(OBJ, "libmoe.sha256")
 
 SOURCES = ["route.hip", "dispatch.hip", "expert_ffn.hip", "combine.hip", "noalloc.hip",
-           "moe_abi.cpp", "stats.cpp"]
+           "quantize.hip", "fp8_gemm.hip", "grad_gemm.hip", "moe_abi.cpp", "stats.cpp"]
 # the MFMA-rate calibration for the measurement harness, in a library of its own
 CALIB_SOURCES = ["calib.hip"]
 CALIB_LIB = os.path.join(PKG, "libmoe_calib.so")

@@ -46,31 +46,23 @@
 //     of shapes with many tokens and experts.
 #include <algorithm>
 #include <type_traits>
-#include <utility>
 
-#include "common.h"
+#include "gemm_common.h"
 #include "kernels.h"
 
 namespace moe {
 
-// silu(g) = g / (1 + e^-g) with the hardware reciprocal (about 1 ulp) instead of a correctly
-// rounded division: the SwiGLU epilogue evaluates it for every output of the gate/up GEMM,
-// and the division's ten instructions made that epilogue several percent of a tile.  For
-// g < -88 the reciprocal of +inf gives -0.0 where the exact value is below 1e-36.
-__device__ inline float silu_f32(float g) {
-  return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g));
-}
-
 // Tile table for one row-tile height BM: table[0] = number of m-tiles over all experts;
 // entry i (i < table[0]) is (expert, first row) at table[1 + 2i], table[2 + 2i].  Experts
-// are numbered in index order and their tiles in row order.
+// are numbered in index order and their tiles in row order.  Rows past `rows` get no tile.
 __global__ void __launch_bounds__(1024)
-tile_table_kernel(const int32_t* __restrict__ offsets, int E, int bm, int m_max,
+tile_table_kernel(const int32_t* __restrict__ offsets, int E, int rows, int bm, int m_max,
                   int32_t* __restrict__ table) {
   __shared__ int smem[17];
   const int e = threadIdx.x;
-  const int row0 = e < E ? offsets[e] : 0;
-  const int c = e < E ? offsets[e + 1] - row0 : 0;
+  // offsets == nullptr: one expert holding every row
+  const int row0 = e < E && offsets ? min(max(offsets[e], 0), rows) : 0;
+  const int c = e < E ? max((offsets ? min(offsets[e + 1], rows) : rows) - row0, 0) : 0;
   const int tiles = (c + bm - 1) / bm;
   int total;
   const int pre = block_exclusive_scan(tiles, smem, &total);
@@ -109,8 +101,6 @@ tile_table_kernel(const int32_t* __restrict__ offsets, int E, int bm, int m_max,
 // NT/2 tiles of gate rows and the NT/2 tiles of up rows of the same output columns, so
 // the gate and up accumulators of one output element sit in the same lane.
 // ---------------------------------------------------------------------------------------
-typedef __attribute__((address_space(3))) char lds_char;
-
 // ROWB: bytes of each row per stage (64 or 128); STAGES: LDS stages (2, 3 or 4);
 // BM_ activation rows and BNW_ weight rows per block; the 8 waves split it WM_ x WN_.
 // DSEL_: which waves issue the direct loads: 0 = all eight; 1 = waves 4-7, one per SIMD
@@ -197,42 +187,6 @@ using RouterTile = PrefillTileT<128, 3, 64, 128, 2, 4>;
 // every tile start wait for a full HBM round trip; at 72 KB of LDS two blocks share a CU
 // and one streams while the other starts (decode layer -1.5 % against 64 x 256).
 using DecodeDownTile = PrefillTileT<128, 3, 64, 128, 2, 4>;
-
-// A wave-uniform 64-bit address, moved to scalar registers.
-__device__ inline uint64_t uniform_u64(const void* p) {
-  const uint64_t a = reinterpret_cast<uint64_t>(p);
-  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
-  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
-  return ((uint64_t)hi << 32) | lo;
-}
-// Raw buffer resource for byte offsets below 2^31 from a uniform base address.  Selecting
-// between bases (scalar) rather than between descriptors keeps the descriptor in scalar
-// registers; a descriptor the compiler cannot prove uniform turns every buffer load into a
-// serialised per-lane loop.
-__device__ inline __amdgpu_buffer_rsrc_t buffer_rsrc(uint64_t base) {
-  constexpr int kFlags = 0x00020000;  // raw buffer, 32-bit data format (gfx9 family)
-  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), 0, 0x7fffffff,
-                                           kFlags);
-}
-
-template <int N>
-using IntC = std::integral_constant<int, N>;
-// f(IntC<0>{}), ..., f(IntC<L-1>{}), with compile-time indices
-template <class F, int... Is>
-__device__ inline void unroll_steps_impl(F&& f, std::integer_sequence<int, Is...>) {
-  (f(IntC<Is>{}), ...);
-}
-template <int L, class F>
-__device__ inline void unroll_steps(F&& f) {
-  unroll_steps_impl(f, std::make_integer_sequence<int, L>{});
-}
-
-// wait until at most N direct loads of this wave are outstanding, then block barrier
-template <int N>
-__device__ inline void wait_vm_barrier() {
-  static_assert(N >= 0 && N < 64, "vmcnt immediate");
-  asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
-}
 
 template <class T, bool SWIGLU, class P, class OutT, int kLdsAlloc>
 __device__ __attribute__((always_inline)) inline void prefill_gemm_body(
@@ -696,22 +650,6 @@ __device__ inline TailSplit tail_split_of(int m_tiles, int n_tiles, int s_max) {
   }
   return p;
 }
-// (m-tile, n-tile) of dense tile number i: groups of m_tiles x group_n tiles, n fastest
-// within a group; the last group holds the n_tiles mod group_n remaining n-tiles.
-__device__ inline void dense_tile(int i, int m_tiles, int n_tiles, int group_n, int* mt,
-                                  int* nt) {
-  const int per_group = m_tiles * group_n, full = n_tiles / group_n;
-  if (i < full * per_group) {
-    const int grp = i / per_group, rem = i - grp * per_group;
-    *mt = rem / group_n;
-    *nt = grp * group_n + rem % group_n;
-  } else {
-    const int rem = i - full * per_group, gw = n_tiles - full * group_n;
-    *mt = rem / gw;
-    *nt = full * group_n + rem % gw;
-  }
-}
-
 // One block per (m-tile, n-tile), or, with the tail split, per whole tile or per piece of a
 // tail tile.  Blocks are dealt round-robin to the 8 XCDs; the logical tile index is
 // remapped so each XCD walks a contiguous range of logical tiles, n fastest within
@@ -869,6 +807,12 @@ tail_sum_kernel(const float* __restrict__ acc, const int32_t* __restrict__ offse
 // ---------------------------------------------------------------------------------------
 // launch configurations
 // ---------------------------------------------------------------------------------------
+hipError_t launch_tile_table(const int32_t* offsets, int64_t E, int64_t rows, int bm,
+                             int64_t m_max, int32_t* table, hipStream_t s) {
+  tile_table_kernel<<<1, 1024, 0, s>>>(offsets, (int)E, (int)rows, bm, (int)m_max, table);
+  return hipGetLastError();
+}
+
 // Row-tile heights: decode-sized experts (mean <= 32 rows) stream weights with 64-row tiles;
 // prefill-sized ones use 256- or 320-row tiles.
 FfnPlan ffn_plan(int64_t T, int64_t E, int64_t k, int64_t C, int64_t R, bool pad, int64_t d,
@@ -979,8 +923,7 @@ hipError_t launch_prefill(const T* A, const int32_t* a_rows, const T* B0, const 
 
 hipError_t launch_table(const FfnArgs& a, const FfnPlan& p, hipStream_t s) {
   if (p.m_max <= 0) return hipSuccess;
-  tile_table_kernel<<<1, 1024, 0, s>>>(a.offsets, (int)a.E, p.bm, (int)p.m_max, a.sched);
-  return hipGetLastError();
+  return launch_tile_table(a.offsets, a.E, a.R, p.bm, p.m_max, a.sched, s);
 }
 
 template <class T>

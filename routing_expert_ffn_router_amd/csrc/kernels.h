@@ -124,6 +124,57 @@ hipError_t launch_router_gemm(int dtype, const void* x, const void* w, const flo
 // call on the same stream built it from the same offsets.
 hipError_t launch_expert_ffn(const FfnArgs& a, int which, hipStream_t s);
 
+// ---------------------------------------------------------------------------------------
+// 8-bit products and gradients
+// ---------------------------------------------------------------------------------------
+hipError_t launch_quantize(int64_t rows, int64_t K, int64_t block_rows, int dtype,
+                           int scale_type, const void* x, void* q, void* scale, hipStream_t s);
+
+// Tile table of row height bm over the experts' rows: table[0] = tiles, then (expert, first
+// row) pairs, at most m_max of them.  Offsets are clamped to [0, rows].
+hipError_t launch_tile_table(const int32_t* offsets, int64_t E, int64_t rows, int bm,
+                             int64_t m_max, int32_t* table, hipStream_t s);
+
+// Row tiling of a grouped product over R row slots of E experts.
+struct GroupPlan {
+  bool small;     // at most 32 rows per expert on average: the weight-streaming kernel
+  int bm;         // row-tile height
+  int64_t m_max;  // bound on the row tiles over all experts
+};
+GroupPlan fp8_plan(int64_t R, int64_t E);
+GroupPlan dgrad_plan(int64_t R, int64_t E, int elt);
+inline int64_t group_table_ints(const GroupPlan& p) { return 1 + 2 * p.m_max; }
+
+// One 8-bit grouped product.  With b1 (the up weights; b0 then the gate weights): the output is
+// silu(gate) * up, quantized by rows into hq [R, N] and h_scale; else y [R, N] bf16.
+struct Fp8Args {
+  const void* xq;           // [x_rows, K]
+  const void* x_scale;      // [x_rows, K / 128]
+  const int32_t* src_rows;  // nullable: row r reads xq row src_rows[r], clamped to x_rows
+  int64_t x_rows;
+  const void* b0;
+  const void* b0_scale;
+  const void* b1;
+  const void* b1_scale;
+  int64_t R, E, N, K;
+  int scale_type;
+  const int32_t* offsets;  // [E+1]
+  const int32_t* table;    // launch_tile_table of fp8_plan(R, E)
+  void* y;
+  void* hq;
+  void* h_scale;
+};
+hipError_t launch_fp8_gemm(const Fp8Args& a, hipStream_t s);
+
+// dtype 0 fp32, 1 bf16.  dgrad reads the table of dgrad_plan; wgrad needs only the offsets.
+hipError_t launch_dgrad(int dtype, const void* dy, const int32_t* offsets,
+                        const int32_t* table, const void* w, void* dx, int64_t R, int64_t E,
+                        int64_t N, int64_t K, hipStream_t s);
+hipError_t launch_wgrad(int dtype, const void* dy, const void* x, const int32_t* offsets,
+                        void* dw, int64_t R, int64_t E, int64_t N, int64_t K, hipStream_t s);
+// Upper bound on the blocks (512 threads each) of the grouped launches above.
+int64_t group_max_blocks(int64_t R, int64_t E, int64_t N, int64_t K, int elt);
+
 // S8
 hipError_t launch_combine(int dtype, const void* y_perm, const int32_t* dest_row,
                           const float* topk_w, void* out, int64_t T, int64_t d, int64_t k,

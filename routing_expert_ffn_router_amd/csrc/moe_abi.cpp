@@ -145,13 +145,14 @@ int check_dispatch_args(const moe_shape* s, const int32_t* topk_idx, const void*
 
 // The dispatch launches, with the scratch tables tile_hist / tile_base ([ntiles, E] int32
 // each) from the workspace or from the static array.
-// With table set, the dispatch also writes the grouped GEMMs' tile table of the layer's
-// plan there (moe_layer).
+// With table set, the dispatch also writes the grouped GEMMs' tile table there, of row height
+// table_bm with at most table_m_max tiles (moe_layer, moe_layer_fp8).
 int dispatch_launch(const moe_shape* s, const int32_t* topk_idx, const void* x,
                     int32_t* tile_hist, int32_t* tile_base, int32_t* routed_counts,
                     int32_t* tokens_per_expert, int32_t* expert_offsets, int32_t* src_token,
                     int32_t* src_slot, int32_t* dest_row, int32_t* drops, void* x_perm,
-                    hipStream_t st, int32_t* table = nullptr) {
+                    hipStream_t st, int32_t* table = nullptr, int table_bm = 0,
+                    int64_t table_m_max = 0) {
   moe::DispatchArgs a;
   a.topk_idx = topk_idx;
   a.x = x;
@@ -174,13 +175,9 @@ int dispatch_launch(const moe_shape* s, const int32_t* topk_idx, const void* x,
   a.dest_row = dest_row;
   a.drops = drops;
   a.x_perm = x_perm;
-  if (table) {
-    const moe::FfnPlan plan = moe::ffn_plan(s->T, s->E, s->k, a.C, a.R, a.pad, s->d, s->F,
-                                            a.elt_bytes);
-    a.table = table;
-    a.table_bm = plan.bm;
-    a.table_m_max = plan.m_max;
-  }
+  a.table = table;
+  a.table_bm = table_bm;
+  a.table_m_max = table_m_max;
   return hip_status(moe::launch_dispatch(a, st));
 }
 
@@ -474,9 +471,12 @@ int moe_layer(const moe_shape* s, const void* x, const void* w_router, const flo
   rc = check_dispatch_args(s, idx, x, routed, kept, offsets, src, dest, dr, x_copy);
   if (rc != MOE_OK) return rc;
   // the dispatch also writes the grouped GEMMs' tile table from the offsets it computes
+  const moe::FfnPlan plan = moe::ffn_plan(s->T, s->E, s->k, eff_capacity(s), max_rows(s),
+                                          padded(s), s->d, s->F, elt_bytes(s->dtype));
   rc = dispatch_launch(s, idx, x, region<int32_t>(ws, L, MOE_WS_TILE_HIST),
                        region<int32_t>(ws, L, MOE_WS_TILE_BASE), routed, kept, offsets, src,
-                       nullptr, dest, dr, x_copy, st, region<int32_t>(ws, L, MOE_WS_SCHED));
+                       nullptr, dest, dr, x_copy, st, region<int32_t>(ws, L, MOE_WS_SCHED),
+                       plan.bm, plan.m_max);
   if (rc != MOE_OK) return rc;
   void* h = region<void>(ws, L, MOE_WS_H);
   rc = expert_ffn_impl(s, 1, gathered ? nullptr : x_perm, gathered ? x : nullptr,
@@ -485,6 +485,327 @@ int moe_layer(const moe_shape* s, const void* x, const void* w_router, const flo
   if (rc != MOE_OK) return rc;
   rc = expert_ffn_impl(s, 2, nullptr, nullptr, nullptr, h, offsets, nullptr, nullptr, w_down,
                        ws, ws_bytes, y_perm, st, /*table_ready=*/true);
+  if (rc != MOE_OK) return rc;
+  return moe_combine(s, y_perm, dest, gates, out, st);
+}
+
+}  // extern "C"
+
+// ------------------------------------------------------------------------------------------
+// 8-bit products and the gradients of the experts' products
+// ------------------------------------------------------------------------------------------
+namespace {
+
+constexpr int64_t kMaxBlocks = (int64_t)1 << 23;  // 512 threads each: within 2^32 threads
+
+int scale_bytes(int scale_type) { return scale_type == MOE_SCALE_E8M0 ? 1 : 4; }
+
+bool known_scale(int scale_type) {
+  return scale_type == MOE_SCALE_F32 || scale_type == MOE_SCALE_E8M0;
+}
+
+// a * b <= limit for positive a, b
+bool product_within(int64_t a, int64_t b, int64_t limit) { return a <= limit / b; }
+
+int check_group(const moe_group_shape* g) {
+  if (!g) return MOE_ERR_INVALID_ARG;
+  if (g->rows < 0 || g->E <= 0 || g->N <= 0 || g->K <= 0) return MOE_ERR_INVALID_ARG;
+  if (g->dtype != MOE_F32 && g->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (!known_scale(g->scale_type)) return MOE_ERR_UNSUPPORTED;
+  if (g->E > kMaxE || g->rows >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
+  if (g->N % 128 != 0 || g->K % 128 != 0) return MOE_ERR_UNSUPPORTED;
+  if (g->N > ((int64_t)1 << 20) || g->K > ((int64_t)1 << 20)) return MOE_ERR_UNSUPPORTED;
+  if (moe::group_max_blocks(g->rows, g->E, g->N, g->K, elt_bytes(g->dtype)) >= kMaxBlocks)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+int64_t group_table_bytes(int64_t R, int64_t E, int elt) {
+  const int64_t a = moe::group_table_ints(moe::fp8_plan(R, E));
+  const int64_t b = moe::group_table_ints(moe::dgrad_plan(R, E, elt));
+  return align_up((a > b ? a : b) * 4);
+}
+
+// Checks shared by the grouped entry points; the operands are checked by the caller.
+int check_group_call(const moe_group_shape* g, const int32_t* offsets, const void* ws,
+                     size_t ws_bytes) {
+  const int rc = check_group(g);
+  if (rc != MOE_OK) return rc;
+  if (!offsets && g->E != 1) return MOE_ERR_INVALID_ARG;
+  if (!ws || (int64_t)ws_bytes < group_table_bytes(g->rows, g->E, elt_bytes(g->dtype)))
+    return MOE_ERR_WORKSPACE;
+  if (((uintptr_t)ws & (kAlign - 1)) != 0) return MOE_ERR_ALIGNMENT;
+  return MOE_OK;
+}
+
+bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
+
+int check_fp8(const moe_fp8_tensor* w, int scale_type) {
+  if (!w || !w->q || !w->scale) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(w->q)) return MOE_ERR_ALIGNMENT;
+  if (scale_type == MOE_SCALE_F32 && !aligned4(w->scale)) return MOE_ERR_ALIGNMENT;
+  return MOE_OK;
+}
+
+// Bytes of q and, 256-byte aligned behind it, the scales of [rows, K] activations.
+int64_t fp8_rows_bytes(int64_t rows, int64_t K, int scale_type) {
+  return align_up(rows * K) + rows * (K / 128) * scale_bytes(scale_type);
+}
+
+int check_fp8_shape(const moe_shape* s, int scale_type) {
+  const int rc = check_shape(s);
+  if (rc != MOE_OK) return rc;
+  if (s->dtype != MOE_BF16 || !known_scale(scale_type)) return MOE_ERR_UNSUPPORTED;
+  const int64_t R = max_rows(s), x_rows = s->T > R ? s->T : R;
+  if (x_rows > 0 && (!product_within(x_rows, s->d, (int64_t)1 << 37) ||
+                     !product_within(x_rows, s->F, (int64_t)1 << 37)))
+    return MOE_ERR_UNSUPPORTED;
+  // both products' grids (either orientation)
+  if (moe::group_max_blocks(R, s->E, s->F, s->d, 2) >= kMaxBlocks) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+// The regions of moe_layer with the row buffers in 8 bits and no split reductions.
+Layout fp8_layout(const moe_shape* s, int scale_type) {
+  Layout L = make_layout(s);
+  const int64_t R = max_rows(s);
+  L.size[MOE_WS_SCHED] = moe::group_table_ints(moe::fp8_plan(R, s->E)) * 4;
+  L.size[MOE_WS_X_PERM] = fp8_rows_bytes(s->T > R ? s->T : R, s->d, scale_type);
+  L.size[MOE_WS_H] = fp8_rows_bytes(R, s->F, scale_type);
+  L.size[MOE_WS_DOWN_ACC] = 0;
+  int64_t o = 0;
+  for (int i = 0; i < MOE_WS_COUNT; ++i) {
+    L.off[i] = o;
+    o += align_up(L.size[i]);
+  }
+  L.total = o;
+  return L;
+}
+
+int check_fp8_workspace(const moe_shape* s, int scale_type, const void* ws, size_t bytes,
+                        Layout* L) {
+  *L = fp8_layout(s, scale_type);
+  if (!ws || (int64_t)bytes < L->total) return MOE_ERR_WORKSPACE;
+  if (((uintptr_t)ws & (kAlign - 1)) != 0) return MOE_ERR_ALIGNMENT;
+  return MOE_OK;
+}
+
+int check_fp8_weights(const moe_fp8_tensor* w_gate, const moe_fp8_tensor* w_up,
+                      const moe_fp8_tensor* w_down, int scale_type) {
+  int rc = check_fp8(w_gate, scale_type);
+  if (rc == MOE_OK) rc = check_fp8(w_up, scale_type);
+  if (rc == MOE_OK) rc = check_fp8(w_down, scale_type);
+  return rc;
+}
+
+// The expert launches over checked arguments: x quantized, gate/up, down.  With table_ready the
+// workspace holds the tile table of these offsets.
+int fp8_experts(const moe_shape* s, int scale_type, const void* x, const int32_t* src_token,
+                const int32_t* offsets, const moe_fp8_tensor* w_gate,
+                const moe_fp8_tensor* w_up, const moe_fp8_tensor* w_down, void* ws,
+                const Layout& L, void* y_perm, hipStream_t st, bool table_ready) {
+  const int64_t R = max_rows(s), x_rows = src_token ? s->T : R;
+  const int64_t cap = s->T > R ? s->T : R;  // rows the x region is laid out for
+  char* xq = region<char>(ws, L, MOE_WS_X_PERM);
+  char* hq = region<char>(ws, L, MOE_WS_H);
+  int32_t* table = region<int32_t>(ws, L, MOE_WS_SCHED);
+  hipError_t e = moe::launch_quantize(x_rows, s->d, 1, s->dtype, scale_type, x, xq,
+                                      xq + align_up(cap * s->d), st);
+  if (e != hipSuccess) return MOE_ERR_HIP;
+  if (!table_ready) {
+    const moe::GroupPlan p = moe::fp8_plan(R, s->E);
+    if ((e = moe::launch_tile_table(offsets, s->E, R, p.bm, p.m_max, table, st)) != hipSuccess)
+      return MOE_ERR_HIP;
+  }
+  moe::Fp8Args a = {};
+  a.xq = xq;
+  a.x_scale = xq + align_up(cap * s->d);
+  a.src_rows = src_token;
+  a.x_rows = x_rows;
+  a.b0 = w_gate->q;
+  a.b0_scale = w_gate->scale;
+  a.b1 = w_up->q;
+  a.b1_scale = w_up->scale;
+  a.R = R;
+  a.E = s->E;
+  a.N = s->F;
+  a.K = s->d;
+  a.scale_type = scale_type;
+  a.offsets = offsets;
+  a.table = table;
+  a.hq = hq;
+  a.h_scale = hq + align_up(R * s->F);
+  if ((e = moe::launch_fp8_gemm(a, st)) != hipSuccess) return MOE_ERR_HIP;
+  a.xq = hq;
+  a.x_scale = hq + align_up(R * s->F);
+  a.src_rows = nullptr;
+  a.x_rows = R;
+  a.b0 = w_down->q;
+  a.b0_scale = w_down->scale;
+  a.b1 = a.b1_scale = nullptr;
+  a.N = s->d;
+  a.K = s->F;
+  a.y = y_perm;
+  a.hq = a.h_scale = nullptr;
+  return hip_status(moe::launch_fp8_gemm(a, st));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_group_workspace_size(const moe_group_shape* g) {
+  if (check_group(g) != MOE_OK) return 0;
+  return (size_t)group_table_bytes(g->rows, g->E, elt_bytes(g->dtype));
+}
+
+int moe_quantize(int64_t rows, int64_t K, int64_t block_rows, int dtype, int scale_type,
+                 const void* x, void* q, void* scale, hipStream_t st) {
+  if (rows < 0 || K <= 0 || (block_rows != 1 && block_rows != 128)) return MOE_ERR_INVALID_ARG;
+  if (rows % block_rows != 0) return MOE_ERR_INVALID_ARG;
+  if (dtype != MOE_F32 && dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (!known_scale(scale_type)) return MOE_ERR_UNSUPPORTED;
+  // 2^37 values: a grid within 2^32 threads
+  if (K % 128 != 0 || !product_within(rows > 0 ? rows : 1, K, ((int64_t)1 << 37) - 1))
+    return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!x || !q || !scale) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(q)) return MOE_ERR_ALIGNMENT;
+  if (scale_type == MOE_SCALE_F32 && !aligned4(scale)) return MOE_ERR_ALIGNMENT;
+  return hip_status(
+      moe::launch_quantize(rows, K, block_rows, dtype, scale_type, x, q, scale, st));
+}
+
+int moe_grouped_gemm_fp8(const moe_group_shape* g, const void* xq, const void* x_scale,
+                         const int32_t* expert_offsets, const void* wq, const void* w_scale,
+                         void* ws, size_t ws_bytes, void* y, hipStream_t st) {
+  int rc = check_group_call(g, expert_offsets, ws, ws_bytes);
+  if (rc != MOE_OK) return rc;
+  if (g->dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+  if (g->rows == 0) return MOE_OK;
+  const moe_fp8_tensor x = {xq, x_scale}, w = {wq, w_scale};
+  if ((rc = check_fp8(&x, g->scale_type)) != MOE_OK) return rc;
+  if ((rc = check_fp8(&w, g->scale_type)) != MOE_OK) return rc;
+  if (!y) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(y)) return MOE_ERR_ALIGNMENT;
+  const moe::GroupPlan p = moe::fp8_plan(g->rows, g->E);
+  int32_t* table = static_cast<int32_t*>(ws);
+  if (moe::launch_tile_table(expert_offsets, g->E, g->rows, p.bm, p.m_max, table, st) !=
+      hipSuccess)
+    return MOE_ERR_HIP;
+  moe::Fp8Args a = {};
+  a.xq = xq;
+  a.x_scale = x_scale;
+  a.x_rows = g->rows;
+  a.b0 = wq;
+  a.b0_scale = w_scale;
+  a.R = g->rows;
+  a.E = g->E;
+  a.N = g->N;
+  a.K = g->K;
+  a.scale_type = g->scale_type;
+  a.offsets = expert_offsets;
+  a.table = table;
+  a.y = y;
+  return hip_status(moe::launch_fp8_gemm(a, st));
+}
+
+int moe_grouped_dgrad(const moe_group_shape* g, const void* dy, const int32_t* expert_offsets,
+                      const void* w, void* ws, size_t ws_bytes, void* dx, hipStream_t st) {
+  const int rc = check_group_call(g, expert_offsets, ws, ws_bytes);
+  if (rc != MOE_OK) return rc;
+  if (g->rows == 0) return MOE_OK;
+  if (!dy || !w || !dx) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(dy) || !aligned16(w) || !aligned16(dx)) return MOE_ERR_ALIGNMENT;
+  const moe::GroupPlan p = moe::dgrad_plan(g->rows, g->E, elt_bytes(g->dtype));
+  int32_t* table = static_cast<int32_t*>(ws);
+  if (moe::launch_tile_table(expert_offsets, g->E, g->rows, p.bm, p.m_max, table, st) !=
+      hipSuccess)
+    return MOE_ERR_HIP;
+  return hip_status(moe::launch_dgrad(g->dtype, dy, expert_offsets, table, w, dx, g->rows, g->E,
+                                      g->N, g->K, st));
+}
+
+int moe_grouped_wgrad(const moe_group_shape* g, const void* dy, const void* x,
+                      const int32_t* expert_offsets, void* ws, size_t ws_bytes, void* dw,
+                      hipStream_t st) {
+  const int rc = check_group_call(g, expert_offsets, ws, ws_bytes);
+  if (rc != MOE_OK) return rc;
+  // without rows every matrix is zeros: dy and x may be null
+  if (!dw || (g->rows > 0 && (!dy || !x))) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(dy) || !aligned16(x) || !aligned16(dw)) return MOE_ERR_ALIGNMENT;
+  return hip_status(moe::launch_wgrad(g->dtype, dy, x, expert_offsets, dw, g->rows, g->E, g->N,
+                                      g->K, st));
+}
+
+size_t moe_fp8_workspace_size(const moe_shape* s, int scale_type) {
+  if (check_fp8_shape(s, scale_type) != MOE_OK) return 0;
+  return (size_t)fp8_layout(s, scale_type).total;
+}
+
+int moe_fp8_workspace_layout(const moe_shape* s, int scale_type, int64_t* offsets) {
+  const int rc = check_fp8_shape(s, scale_type);
+  if (rc != MOE_OK) return rc;
+  if (!offsets) return MOE_ERR_INVALID_ARG;
+  const Layout L = fp8_layout(s, scale_type);
+  for (int i = 0; i < MOE_WS_COUNT; ++i) offsets[i] = L.off[i];
+  return MOE_OK;
+}
+
+int moe_expert_ffn_fp8(const moe_shape* s, int scale_type, const void* x,
+                       const int32_t* src_token, const int32_t* expert_offsets,
+                       const moe_fp8_tensor* w_gate, const moe_fp8_tensor* w_up,
+                       const moe_fp8_tensor* w_down, void* ws, size_t ws_bytes, void* y_perm,
+                       hipStream_t st) {
+  int rc = check_fp8_shape(s, scale_type);
+  if (rc != MOE_OK) return rc;
+  if (s->T == 0) return MOE_OK;
+  if (!x || !expert_offsets || !y_perm) return MOE_ERR_INVALID_ARG;
+  if ((rc = check_fp8_weights(w_gate, w_up, w_down, scale_type)) != MOE_OK) return rc;
+  if (!aligned16(x) || !aligned16(y_perm)) return MOE_ERR_ALIGNMENT;
+  if (src_token && s->T * s->d >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
+  Layout L;
+  if ((rc = check_fp8_workspace(s, scale_type, ws, ws_bytes, &L)) != MOE_OK) return rc;
+  return fp8_experts(s, scale_type, x, src_token, expert_offsets, w_gate, w_up, w_down, ws, L,
+                     y_perm, st, /*table_ready=*/false);
+}
+
+int moe_layer_fp8(const moe_shape* s, int scale_type, const void* x, const void* w_router,
+                  const float* b_router, const moe_fp8_tensor* w_gate,
+                  const moe_fp8_tensor* w_up, const moe_fp8_tensor* w_down, void* ws,
+                  size_t ws_bytes, void* out, int32_t* routed_counts,
+                  int32_t* tokens_per_expert, int32_t* drops, int32_t* status, hipStream_t st) {
+  int rc = check_fp8_shape(s, scale_type);
+  if (rc != MOE_OK) return rc;
+  if (!w_router) return MOE_ERR_INVALID_ARG;
+  if ((rc = check_fp8_weights(w_gate, w_up, w_down, scale_type)) != MOE_OK) return rc;
+  if (s->T > 0 && (!x || !out)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w_router) || !aligned16(out)) return MOE_ERR_ALIGNMENT;
+  if (s->T * s->d >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
+  Layout L;
+  if ((rc = check_fp8_workspace(s, scale_type, ws, ws_bytes, &L)) != MOE_OK) return rc;
+  float* logits = region<float>(ws, L, MOE_WS_LOGITS);
+  int32_t* idx = region<int32_t>(ws, L, MOE_WS_TOPK_IDX);
+  float* gates = region<float>(ws, L, MOE_WS_TOPK_W);
+  int32_t* routed = routed_counts ? routed_counts : region<int32_t>(ws, L, MOE_WS_ROUTED);
+  int32_t* kept = tokens_per_expert ? tokens_per_expert : region<int32_t>(ws, L, MOE_WS_KEPT);
+  int32_t* offsets = region<int32_t>(ws, L, MOE_WS_OFFSETS);
+  int32_t* src = region<int32_t>(ws, L, MOE_WS_SRC_TOKEN);
+  int32_t* dest = region<int32_t>(ws, L, MOE_WS_DEST_ROW);
+  int32_t* dr = drops ? drops : region<int32_t>(ws, L, MOE_WS_DROPS);
+  int32_t* stt = status ? status : region<int32_t>(ws, L, MOE_WS_STATUS);
+  void* y_perm = region<void>(ws, L, MOE_WS_Y_PERM);
+  rc = route_impl(s, x, w_router, b_router, logits, 0, idx, gates, stt, st);
+  if (rc != MOE_OK) return rc;
+  // tables only, the experts' tile table among them: the gate/up product gathers the rows
+  const moe::GroupPlan p = moe::fp8_plan(max_rows(s), s->E);
+  rc = dispatch_launch(s, idx, nullptr, region<int32_t>(ws, L, MOE_WS_TILE_HIST),
+                       region<int32_t>(ws, L, MOE_WS_TILE_BASE), routed, kept, offsets, src,
+                       nullptr, dest, dr, nullptr, st, region<int32_t>(ws, L, MOE_WS_SCHED), p.bm,
+                       p.m_max);
+  if (rc != MOE_OK || s->T == 0) return rc;
+  rc = fp8_experts(s, scale_type, x, src, offsets, w_gate, w_up, w_down, ws, L, y_perm, st,
+                   /*table_ready=*/true);
   if (rc != MOE_OK) return rc;
   return moe_combine(s, y_perm, dest, gates, out, st);
 }
