@@ -492,174 +492,184 @@ def fp8_workspace_layout(s: MoeShape, scale_type: int = MOE_SCALE_F32) -> dict:
     return {n: int(o) for n, o in zip(WS_REGIONS, offs)}
 
 
-def _act_dtype(dtype: int):
-    import torch
+class _Types:
+    """torch's types as the checks below compare them, looked up once."""
 
-    return torch.bfloat16 if dtype == MOE_BF16 else torch.float32
+    def __init__(self):
+        import torch
+
+        self.act = {MOE_BF16: (torch.bfloat16,), MOE_F32: (torch.float32,)}
+        self.acts = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
+        self.f32, self.i32 = (torch.float32,), (torch.int32,)
+        self.e4m3 = (torch.float8_e4m3fn, torch.uint8)
+        self.scale = {MOE_SCALE_F32: self.f32,
+                      MOE_SCALE_E8M0: (torch.uint8, torch.float8_e8m0fnu)}
+        self.device = torch.cuda.current_device
 
 
-def _arg(t, name: str, dtypes, shape) -> Optional[int]:
+_types = None
+
+
+def _begin():
+    """(the types, the current GPU) at the start of a checked call."""
+    global _types
+    if _types is None:
+        _types = _Types()
+    return _types, _types.device()
+
+
+def _arg(t, name: str, dtypes: tuple, shape: tuple, gpu: int) -> int:
     """The device pointer of a tensor that an entry point reads or writes in whole: contiguous,
     of one of `dtypes`, exactly `shape`, on the current GPU."""
-    import torch
-
+    if (t is not None and t.dtype in dtypes and t.shape == shape and t.is_contiguous()
+            and t.get_device() == gpu):
+        return t.data_ptr()
     if t is None:
         raise ValueError(f"{name} is missing")
-    if not isinstance(dtypes, tuple):
-        dtypes = (dtypes,)
     if t.dtype not in dtypes:
         raise ValueError(f"{name} is {t.dtype}, not {' or '.join(str(d) for d in dtypes)}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} is not contiguous")
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, not on the current GPU")
-    return t.data_ptr()
+    raise ValueError(f"{name} is on {t.device}, not on the current GPU")
 
 
-def _ws_arg(t):
-    import torch
+def _optional(t, name: str, dtypes: tuple, shape: tuple, gpu: int) -> Optional[int]:
+    return None if t is None else _arg(t, name, dtypes, shape, gpu)
 
+
+def _workspace_arg(t, gpu: int) -> tuple:
+    """(device pointer, bytes) of a workspace; the library checks its size."""
     if t is None:
         return None, 0
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
+    if t.get_device() != gpu:
         raise ValueError(f"workspace is on {t.device}, not on the current GPU")
     if not t.is_contiguous():
         raise ValueError("workspace is not contiguous")
     return t.data_ptr(), _nbytes(t)
 
 
-def _e4m3_dtypes() -> tuple:
-    import torch
-
-    return torch.float8_e4m3fn, torch.uint8
-
-
-def _scale_dtypes(scale_type: int) -> tuple:
-    import torch
-
-    if scale_type == MOE_SCALE_E8M0:
-        return torch.uint8, torch.float8_e8m0fnu
-    return (torch.float32,)
+def _scale_types(ty: _Types, scale_type: int) -> tuple:
+    if scale_type not in ty.scale:
+        raise ValueError(f"unknown scale type {scale_type}")
+    return ty.scale[scale_type]
 
 
-def _fp8_weight(w, name: str, scale_type: int, E: int, N: int, K: int) -> MoeFp8Tensor:
+def _fp8_weight(w, name: str, ty: _Types, scale_type: int, E: int, N: int, K: int,
+                gpu: int) -> MoeFp8Tensor:
     q, scale = w
-    return MoeFp8Tensor(
-        _arg(q, name, _e4m3_dtypes(), (E, N, K)),
-        _arg(scale, f"{name}'s scale", _scale_dtypes(scale_type), (E, N // 128, K // 128)))
-
-
-def _offsets_arg(t, E: int):
-    import torch
-
-    return None if t is None else _arg(t, "expert_offsets", torch.int32, (E + 1,))
+    return MoeFp8Tensor(_arg(q, name, ty.e4m3, (E, N, K), gpu),
+                        _arg(scale, f"{name}'s scale", _scale_types(ty, scale_type),
+                             (E, N // 128, K // 128), gpu))
 
 
 def quantize(x, block_rows: int, scale_type: int, q, scale, stream=None) -> None:
-    """moe_quantize: x [..., K] (rows are the leading dimensions) to e4m3 q of x's shape and
-    scales of shape [rows / block_rows, K / 128], or of x's leading dimensions with the last one
-    divided by block_rows and K / 128."""
-    import torch
-
-    K = x.shape[-1]
+    """moe_quantize: x [..., N, K] to e4m3 q of the same shape.  Scales are [..., N, K / 128] for
+    block_rows 1 and [..., N / 128, K / 128] for 128, a matrix's scales after another's as its
+    rows are; a list [rows / block_rows, K / 128] of them is taken as well."""
+    ty, gpu = _begin()
+    shape = x.shape
+    if len(shape) < 2 or block_rows not in (1, 128) or shape[-1] % 128 or shape[-2] % block_rows:
+        raise ValueError(f"x of shape {tuple(shape)} has no {block_rows} x 128 blocks")
+    K = shape[-1]
     rows = x.numel() // K if K else 0
-    ok = x.dim() >= 1 and K % 128 == 0 and K > 0 and block_rows in (1, 128) and \
-        rows % block_rows == 0
-    if ok:
-        flat = (rows // block_rows, K // 128)
-        lead = tuple(x.shape[:-1])
-        nested = lead[:-1] + (lead[-1] // block_rows, K // 128) if lead else flat
-        want = flat if tuple(scale.shape) == flat else nested
-        # nested scales of 128-row blocks: no block may span two matrices
-        if lead and lead[-1] % block_rows:
-            want = flat
-        xp = _arg(x, "x", (torch.bfloat16, torch.float32), x.shape)
-        qp = _arg(q, "q", _e4m3_dtypes(), x.shape)
-        sp = _arg(scale, "scale", _scale_dtypes(scale_type), want)
-    else:  # the library refuses it and says why
-        xp, qp, sp = _ptr(x), _ptr(q), _ptr(scale)
+    want = (*shape[:-2], shape[-2] // block_rows, K // 128)
+    if len(shape) > 2 and scale.dim() == 2:
+        want = (rows // block_rows, K // 128)
     _check("moe_quantize", load_library().moe_quantize(
-        rows, K, block_rows, MOE_BF16 if x.dtype == torch.bfloat16 else MOE_F32, scale_type, xp,
-        qp, sp, _stream(stream)))
+        rows, K, block_rows, ty.acts.get(x.dtype, -1), scale_type,
+        _arg(x, "x", tuple(ty.acts), shape, gpu), _arg(q, "q", ty.e4m3, shape, gpu),
+        _arg(scale, "scale", _scale_types(ty, scale_type), want, gpu), _stream(stream)))
 
 
 def grouped_gemm_fp8(g: MoeGroupShape, xq, x_scale, expert_offsets, wq, w_scale, workspace, y,
                      stream=None) -> None:
-    """moe_grouped_gemm_fp8: y[r] = dequantized xq[r] W[e]^T for the rows of each expert."""
-    w = _fp8_weight((wq, w_scale), "wq", g.scale_type, g.E, g.N, g.K)
-    ws, nbytes = _ws_arg(workspace)
+    """moe_grouped_gemm_fp8: y[r] = (xq x_scale)[r] (wq w_scale)[e]^T for the rows of each
+    expert."""
+    ty, gpu = _begin()
+    R, E, N, K = g.rows, g.E, g.N, g.K
+    st = _scale_types(ty, g.scale_type)
+    ws, nbytes = _workspace_arg(workspace, gpu)
     _check("moe_grouped_gemm_fp8", load_library().moe_grouped_gemm_fp8(
-        ctypes.byref(g), _arg(xq, "xq", _e4m3_dtypes(), (g.rows, g.K)),
-        _arg(x_scale, "x_scale", _scale_dtypes(g.scale_type), (g.rows, g.K // 128)),
-        _offsets_arg(expert_offsets, g.E), w.q, w.scale, ws, nbytes,
-        _arg(y, "y", _act_dtype(g.dtype), (g.rows, g.N)), _stream(stream)))
+        ctypes.byref(g), _arg(xq, "xq", ty.e4m3, (R, K), gpu),
+        _arg(x_scale, "x_scale", st, (R, K // 128), gpu),
+        _optional(expert_offsets, "expert_offsets", ty.i32, (E + 1,), gpu),
+        _arg(wq, "wq", ty.e4m3, (E, N, K), gpu),
+        _arg(w_scale, "w_scale", st, (E, N // 128, K // 128), gpu), ws, nbytes,
+        _arg(y, "y", ty.act[MOE_BF16], (R, N), gpu), _stream(stream)))
+
+
+def _group_act(ty: _Types, g: MoeGroupShape) -> tuple:
+    if g.dtype not in ty.act:
+        raise ValueError(f"unknown dtype {g.dtype}")
+    return ty.act[g.dtype]
 
 
 def grouped_dgrad(g: MoeGroupShape, dy, expert_offsets, w, workspace, dx, stream=None) -> None:
     """moe_grouped_dgrad: dx[r] = dy[r] W[e] for the rows of each expert."""
-    dt = _act_dtype(g.dtype)
-    ws, nbytes = _ws_arg(workspace)
+    ty, gpu = _begin()
+    R, E, N, K = g.rows, g.E, g.N, g.K
+    dt = _group_act(ty, g)
+    ws, nbytes = _workspace_arg(workspace, gpu)
     _check("moe_grouped_dgrad", load_library().moe_grouped_dgrad(
-        ctypes.byref(g), _arg(dy, "dy", dt, (g.rows, g.N)), _offsets_arg(expert_offsets, g.E),
-        _arg(w, "w", dt, (g.E, g.N, g.K)), ws, nbytes, _arg(dx, "dx", dt, (g.rows, g.K)),
+        ctypes.byref(g), _arg(dy, "dy", dt, (R, N), gpu),
+        _optional(expert_offsets, "expert_offsets", ty.i32, (E + 1,), gpu),
+        _arg(w, "w", dt, (E, N, K), gpu), ws, nbytes, _arg(dx, "dx", dt, (R, K), gpu),
         _stream(stream)))
 
 
 def grouped_wgrad(g: MoeGroupShape, dy, x, expert_offsets, workspace, dw, stream=None) -> None:
     """moe_grouped_wgrad: dw[e] = sum over the expert's rows of dy[r]^T x[r]."""
-    dt = _act_dtype(g.dtype)
-    ws, nbytes = _ws_arg(workspace)
+    ty, gpu = _begin()
+    R, E, N, K = g.rows, g.E, g.N, g.K
+    dt = _group_act(ty, g)
+    ws, nbytes = _workspace_arg(workspace, gpu)
     _check("moe_grouped_wgrad", load_library().moe_grouped_wgrad(
-        ctypes.byref(g), _arg(dy, "dy", dt, (g.rows, g.N)), _arg(x, "x", dt, (g.rows, g.K)),
-        _offsets_arg(expert_offsets, g.E), ws, nbytes, _arg(dw, "dw", dt, (g.E, g.N, g.K)),
-        _stream(stream)))
+        ctypes.byref(g), _arg(dy, "dy", dt, (R, N), gpu), _arg(x, "x", dt, (R, K), gpu),
+        _optional(expert_offsets, "expert_offsets", ty.i32, (E + 1,), gpu), ws, nbytes,
+        _arg(dw, "dw", dt, (E, N, K), gpu), _stream(stream)))
 
 
 def expert_ffn_fp8(s: MoeShape, scale_type: int, x, src_token, expert_offsets, w_gate, w_up,
                    w_down, workspace, y_perm, stream=None) -> None:
     """moe_expert_ffn_fp8; each weight is a pair (e4m3 values, scales)."""
-    import torch
-
-    R = max_rows(s)
-    wg = _fp8_weight(w_gate, "w_gate", scale_type, s.E, s.F, s.d)
-    wu = _fp8_weight(w_up, "w_up", scale_type, s.E, s.F, s.d)
-    wd = _fp8_weight(w_down, "w_down", scale_type, s.E, s.d, s.F)
-    dt = _act_dtype(s.dtype)
-    src = None if src_token is None else _arg(src_token, "src_token", torch.int32, (R,))
-    ws, nbytes = _ws_arg(workspace)
+    ty, gpu = _begin()
+    R, T, E, d, F = max_rows(s), s.T, s.E, s.d, s.F
+    bf16 = ty.act[MOE_BF16]
+    wg = _fp8_weight(w_gate, "w_gate", ty, scale_type, E, F, d, gpu)
+    wu = _fp8_weight(w_up, "w_up", ty, scale_type, E, F, d, gpu)
+    wd = _fp8_weight(w_down, "w_down", ty, scale_type, E, d, F, gpu)
+    ws, nbytes = _workspace_arg(workspace, gpu)
     _check("moe_expert_ffn_fp8", load_library().moe_expert_ffn_fp8(
         ctypes.byref(s), scale_type,
-        _arg(x, "x", dt, (R if src is None else s.T, s.d)), src,
-        _offsets_arg(expert_offsets, s.E), ctypes.byref(wg), ctypes.byref(wu), ctypes.byref(wd),
-        ws, nbytes, _arg(y_perm, "y_perm", dt, (R, s.d)), _stream(stream)))
+        _arg(x, "x", bf16, (R if src_token is None else T, d), gpu),
+        _optional(src_token, "src_token", ty.i32, (R,), gpu),
+        _arg(expert_offsets, "expert_offsets", ty.i32, (E + 1,), gpu), ctypes.byref(wg),
+        ctypes.byref(wu), ctypes.byref(wd), ws, nbytes,
+        _arg(y_perm, "y_perm", bf16, (R, d), gpu), _stream(stream)))
 
 
 def layer_fp8(s: MoeShape, scale_type: int, x, w_router, b_router, w_gate, w_up, w_down,
               workspace, out, routed_counts=None, tokens_per_expert=None, drops=None,
               status=None, stream=None) -> None:
     """moe_layer_fp8; each expert weight is a pair (e4m3 values, scales)."""
-    import torch
-
-    wg = _fp8_weight(w_gate, "w_gate", scale_type, s.E, s.F, s.d)
-    wu = _fp8_weight(w_up, "w_up", scale_type, s.E, s.F, s.d)
-    wd = _fp8_weight(w_down, "w_down", scale_type, s.E, s.d, s.F)
-    dt, i32 = _act_dtype(s.dtype), torch.int32
-
-    def optional(t, name, dtype, n):
-        return None if t is None else _arg(t, name, dtype, (n,))
-
-    ws, nbytes = _ws_arg(workspace)
+    ty, gpu = _begin()
+    T, E, d, F = s.T, s.E, s.d, s.F
+    bf16 = ty.act[MOE_BF16]
+    wg = _fp8_weight(w_gate, "w_gate", ty, scale_type, E, F, d, gpu)
+    wu = _fp8_weight(w_up, "w_up", ty, scale_type, E, F, d, gpu)
+    wd = _fp8_weight(w_down, "w_down", ty, scale_type, E, d, F, gpu)
+    ws, nbytes = _workspace_arg(workspace, gpu)
     _check("moe_layer_fp8", load_library().moe_layer_fp8(
-        ctypes.byref(s), scale_type, _arg(x, "x", dt, (s.T, s.d)),
-        _arg(w_router, "w_router", dt, (s.E, s.d)),
-        optional(b_router, "b_router", torch.float32, s.E), ctypes.byref(wg), ctypes.byref(wu),
-        ctypes.byref(wd), ws, nbytes, _arg(out, "out", dt, (s.T, s.d)),
-        optional(routed_counts, "routed_counts", i32, s.E),
-        optional(tokens_per_expert, "tokens_per_expert", i32, s.E),
-        optional(drops, "drops", i32, s.k + 2), optional(status, "status", i32, 1),
-        _stream(stream)))
+        ctypes.byref(s), scale_type, _arg(x, "x", bf16, (T, d), gpu),
+        _arg(w_router, "w_router", bf16, (E, d), gpu),
+        _optional(b_router, "b_router", ty.f32, (E,), gpu), ctypes.byref(wg), ctypes.byref(wu),
+        ctypes.byref(wd), ws, nbytes, _arg(out, "out", bf16, (T, d), gpu),
+        _optional(routed_counts, "routed_counts", ty.i32, (E,), gpu),
+        _optional(tokens_per_expert, "tokens_per_expert", ty.i32, (E,), gpu),
+        _optional(drops, "drops", ty.i32, (s.k + 2,), gpu),
+        _optional(status, "status", ty.i32, (1,), gpu), _stream(stream)))
 
 
 class MoELayerFp8:
@@ -687,7 +697,8 @@ class MoELayerFp8:
         E, N, K = w.shape
         q = torch.empty((E, N, K), dtype=torch.float8_e4m3fn, device=w.device)
         scale = torch.empty((E, N // 128, K // 128), device=w.device,
-                            dtype=_scale_dtypes(self.scale_type)[0])
+                            dtype=torch.uint8 if self.scale_type == MOE_SCALE_E8M0
+                            else torch.float32)
         quantize(w, 128, self.scale_type, q, scale, stream)
         return q, scale
 

@@ -14,9 +14,8 @@
 // = lane / 16).  The weight fragment goes first: a lane then holds one row's four consecutive
 // output columns, and the row's scale is one value per lane.
 //
-// Two kernels.  Few rows per expert (at most 32 on average; decode): every weight is read once
-// and bounds the time, so waves load weight fragments straight into registers, a ring of steps
-// ahead, and nothing is shared through LDS.  More rows: weights and rows go through LDS.
+// Weights and rows go through LDS in tiles of 64, 128 or 256 rows by 256 weight rows; a product
+// with too few tiles for the CUs splits its reduction over the waves of a block instead.
 #include <algorithm>
 
 #include "fp8_common.h"
@@ -36,9 +35,9 @@ struct Fp8Kern {
   const void* b0s;
   const uint8_t* b1;
   const void* b1s;
-  int R, N, K;
+  int R, E, N, K;
   const int32_t* offsets;  // nullable: one expert holds all R rows
-  const int32_t* table;
+  const int32_t* table;    // nullable with few experts (group_tile)
   bf16* y;
   uint8_t* hq;
   void* hs;
@@ -72,204 +71,132 @@ __device__ inline void add_scaled(f32x4& acc, const f32x4& p, float s) {
   for (int q = 0; q < 4; ++q) acc[q] = fmaf(p[q], s, acc[q]);
 }
 
-// Row tile and n-tile of this block: the tiles are dealt to the 8 XCDs (blocks go round them in
-// turn) in contiguous shares of the tiles there are, so that a share's tiles keep their rows
-// and weights in one L2.  False: no tile.
-__device__ inline bool fp8_tile(const Fp8Kern& a, int* mt, int* nt) {
-  const int m_tiles = a.table[0], total = m_tiles * a.n_tiles;
-  const int xcd = blockIdx.x & 7, j = blockIdx.x >> 3, per = (total + 7) / 8;
-  const int i = xcd * per + j;
-  if (j >= per || i >= total) return false;
-  dense_tile(i, m_tiles, a.n_tiles, a.group_n, mt, nt);
-  return true;
-}
-
 // Row of xq for row r of the grouped rows.
 __device__ inline int x_row(const Fp8Kern& a, int r) {
   return a.src ? min(max(a.src[r], 0), a.x_rows - 1) : r;
 }
 
 // ---------------------------------------------------------------------------------------
-// few rows per expert
+// few tiles
 // ---------------------------------------------------------------------------------------
-// Eight waves; WK of them share a column tile and take every WK-th step of the reduction (their
-// sums are added through LDS in wave order), 8 / WK column tiles of 16 per block.  LIVE:
-// 16-row tiles that hold rows.  D: steps in flight.
-template <bool SWIGLU, bool E8M0, int WK, int LIVE, int D>
-__device__ inline void skinny_body(const Fp8Kern& a, int e, int m_begin, int rows, int nt,
-                                   float* smem) {
-  constexpr int NW = SWIGLU ? 2 : 1, WN = 8 / WK;
-  const int lane = lane_id(), wave = threadIdx.x / kWave;
+// A product whose column tiles are too few for the 256 CUs (a shared expert and a few tokens) is
+// bound by latency: 16 columns per block, every wave of the eight takes each eighth step of the
+// reduction with its weight and row fragments loaded straight into registers, D steps ahead, and
+// the sums are added through LDS in wave order.  LIVE: 16-row tiles that hold rows.
+constexpr int kSplitRows = 64, kSplitWaves = 8;
+
+template <bool E8M0, int LIVE, int D>
+__device__ inline void split_body(const Fp8Kern& a, const RowTile& rt, int rows, int nt,
+                                  f32x4* part) {
+  constexpr int ES = E8M0 ? 1 : 4;
+  const int lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int c = lane & 15, g = lane >> 4;
-  const int wn = wave % WN, wk = wave / WN;
-  const int n0 = (nt * WN + wn) * 16;
-  const int KB = a.K / kScaleBlock;
-  const uint8_t* wp[NW];
-  const void* wsp[NW];
-  int64_t wsi;
-  {
-    const int64_t row = (int64_t)e * a.N + n0 + c;
-    wp[0] = a.b0 + row * a.K + g * 16;
-    wsp[0] = a.b0s;
-    if constexpr (SWIGLU) {
-      wp[1] = a.b1 + row * a.K + g * 16;
-      wsp[1] = a.b1s;
-    }
-    wsi = ((int64_t)e * (a.N / kScaleBlock) + __builtin_amdgcn_readfirstlane(n0 / kScaleBlock)) *
-          KB;
-  }
-  const uint8_t* xp[LIVE];
-  int64_t xsi[LIVE];
+  const int n0 = nt * 16, KB = a.K / kScaleBlock;
+  const auto rw = buffer_rsrc(uniform_u64(a.b0 + ((int64_t)rt.e * a.N + n0) * a.K));
+  const auto rx = buffer_rsrc(uniform_u64(a.xq + (int64_t)rt.begin * a.K));
+  const auto rws = buffer_rsrc(uniform_u64(
+      static_cast<const char*>(a.b0s) +
+      ((int64_t)rt.e * (a.N / kScaleBlock) + n0 / kScaleBlock) * KB * ES));
+  const auto rxs =
+      buffer_rsrc(uniform_u64(static_cast<const char*>(a.xs) + (int64_t)rt.begin * KB * ES));
+  const uint32_t vw = (uint32_t)c * (uint32_t)a.K + g * 16;
+  uint32_t vx[LIVE], vs[LIVE];
 #pragma unroll
   for (int i = 0; i < LIVE; ++i) {
-    const int64_t row = x_row(a, m_begin + min(i * 16 + c, rows - 1));
-    xp[i] = a.xq + row * a.K + g * 16;
-    xsi[i] = row * KB;
+    const uint32_t row = min(i * 16 + c, rows - 1);
+    vx[i] = row * (uint32_t)a.K + g * 16;
+    vs[i] = row * (uint32_t)(KB * ES);
   }
   struct Step {
-    u32x4 w[NW][2], x[LIVE][2];
-    uint32_t ws[NW], xs[LIVE];
+    u32x4 w[2], x[LIVE][2];
+    uint32_t ws, xs[LIVE];
+  };
+  auto scale_at = [&](const __amdgpu_buffer_rsrc_t& r, uint32_t voff, int kb) -> uint32_t {
+    if constexpr (E8M0)
+      return __builtin_amdgcn_raw_buffer_load_b8(r, voff, kb, 0);
+    else
+      return __builtin_amdgcn_raw_buffer_load_b32(r, voff, kb * 4, 0);
   };
   auto load = [&](Step& s, int t) {
-    const int kb = min(wk + t * WK, KB - 1);  // past the end: the last step again, not used
-    const int64_t off = (int64_t)kb * kScaleBlock;
+    const int kb = min(wave + t * kSplitWaves, KB - 1);  // past the end: not used
 #pragma unroll
-    for (int j = 0; j < NW; ++j) {
+    for (int h = 0; h < 2; ++h)
+      s.w[h] = __builtin_amdgcn_raw_buffer_load_b128(rw, vw, kb * kScaleBlock + h * 64, 2);
+#pragma unroll
+    for (int i = 0; i < LIVE; ++i)
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        s.w[j][h] = __builtin_nontemporal_load(
-            reinterpret_cast<const u32x4*>(wp[j] + off + h * 64));
-      s.ws[j] = load_scale<E8M0>(wsp[j], wsi + kb);
-    }
+        s.x[i][h] = __builtin_amdgcn_raw_buffer_load_b128(rx, vx[i], kb * kScaleBlock + h * 64, 0);
+    s.ws = scale_at(rws, 0, kb);
+#pragma unroll
+    for (int i = 0; i < LIVE; ++i) s.xs[i] = scale_at(rxs, vs[i], kb);
+  };
+  f32x4 acc[LIVE];
+#pragma unroll
+  for (int i = 0; i < LIVE; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](const Step& s) {
+    const i32x8 w = join(s.w[0], s.w[1]);
 #pragma unroll
     for (int i = 0; i < LIVE; ++i) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        s.x[i][h] = *reinterpret_cast<const u32x4*>(xp[i] + off + h * 64);
-      s.xs[i] = load_scale<E8M0>(a.xs, xsi[i] + kb);
+      const i32x8 x = join(s.x[i][0], s.x[i][1]);
+      if constexpr (E8M0)
+        mma_e8m0(acc[i], w, x, s.ws, s.xs[i]);
+      else
+        add_scaled(acc[i], mma_zero(w, x), __uint_as_float(s.ws) * __uint_as_float(s.xs[i]));
     }
   };
-  f32x4 acc[NW][LIVE];
-#pragma unroll
-  for (int j = 0; j < NW; ++j)
-#pragma unroll
-    for (int i = 0; i < LIVE; ++i) acc[j][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto multiply = [&](const Step& s) {
-#pragma unroll
-    for (int j = 0; j < NW; ++j) {
-      const i32x8 w = join(s.w[j][0], s.w[j][1]);
-#pragma unroll
-      for (int i = 0; i < LIVE; ++i) {
-        const i32x8 x = join(s.x[i][0], s.x[i][1]);
-        if constexpr (E8M0)
-          mma_e8m0(acc[j][i], w, x, s.ws[j], s.xs[i]);
-        else
-          add_scaled(acc[j][i], mma_zero(w, x),
-                     __uint_as_float(s.ws[j]) * __uint_as_float(s.xs[i]));
-      }
-    }
-  };
-  const int steps = (KB - wk + WK - 1) / WK;  // may be 0 for a wave past a short reduction
+  const int steps = (KB - wave + kSplitWaves - 1) / kSplitWaves;  // 0 past a short reduction
   Step ring[D];
 #pragma unroll
   for (int d = 0; d < D; ++d) load(ring[d], d);
-  int t = 0;
-  for (; t + D <= steps; t += D) {
+  for (int t = 0; t < steps; t += D) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
-      multiply(ring[d]);
-      load(ring[d], t + d + D);
+      // keep the order: the loads of a slot right behind its last use, D steps ahead
+      __builtin_amdgcn_sched_barrier(0);
+      if (t + d < steps) {
+        multiply(ring[d]);
+        load(ring[d], t + d + D);
+      }
     }
   }
 #pragma unroll
-  for (int d = 0; d < D - 1; ++d)
-    if (t + d < steps) multiply(ring[d]);
-
-  if constexpr (SWIGLU) {
-    // the block's 128 columns are one scale block of h: the row's largest magnitude over the
-    // four lanes that hold its columns in this wave, then over the eight waves through LDS
-    uint32_t* wave_max = reinterpret_cast<uint32_t*>(smem);  // [LIVE * 16][8]
-    float h[LIVE][4];
+  for (int i = 0; i < LIVE; ++i) part[(wave * LIVE + i) * kWave + lane] = acc[i];
+  __syncthreads();
+  if (wave < LIVE) {
+    f32x4 v = part[wave * kWave + lane];
 #pragma unroll
-    for (int i = 0; i < LIVE; ++i) {
-      uint32_t m = 0;
+    for (int w = 1; w < kSplitWaves; ++w) {
+      const f32x4 u = part[(w * LIVE + wave) * kWave + lane];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        h[i][q] = silu_f32(acc[0][i][q]) * acc[1][i][q];
-        m = max(m, abs_bits(h[i][q]));
-      }
-      m = max(m, (uint32_t)__shfl_xor((int)m, 16, kWave));
-      m = max(m, (uint32_t)__shfl_xor((int)m, 32, kWave));
-      if (g == 0) wave_max[(i * 16 + c) * 8 + wave] = m;
+      for (int q = 0; q < 4; ++q) v[q] += u[q];
     }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < LIVE; ++i) {
-      if (i * 16 + c >= rows) continue;
-      uint32_t m = 0;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) m = max(m, wave_max[(i * 16 + c) * 8 + w]);
-      const bool finite = m < kInfBits;
-      const int ex = finite ? scale_exponent(m) : 0;
-      const float r = inv_scale(ex);
-      const int64_t row = m_begin + i * 16 + c;
-      *reinterpret_cast<uint32_t*>(a.hq + row * a.N + n0 + 4 * g) =
-          finite ? pack_e4m3(h[i][0] * r, h[i][1] * r, h[i][2] * r, h[i][3] * r) : kNan4;
-      if (wave == 0 && g == 0)
-        store_scale(a.hs, row * (a.N / kScaleBlock) + nt, E8M0 ? kScaleE8M0 : kScaleF32, ex,
-                    finite);
-    }
-  } else {
     typedef bf16 bf16x4 __attribute__((ext_vector_type(4)));
-    auto store = [&](int i, const f32x4& v) {
-      if (i * 16 + c < rows)
-        *reinterpret_cast<bf16x4*>(a.y + (int64_t)(m_begin + i * 16 + c) * a.N + n0 + 4 * g) =
-            bf16x4{(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]};
-    };
-    if constexpr (WK == 1) {
-#pragma unroll
-      for (int i = 0; i < LIVE; ++i) store(i, acc[0][i]);
-    } else {
-      f32x4* part = reinterpret_cast<f32x4*>(smem);  // [wk][wn][LIVE][64]
-#pragma unroll
-      for (int i = 0; i < LIVE; ++i) part[((wk * WN + wn) * LIVE + i) * kWave + lane] = acc[0][i];
-      __syncthreads();
-      for (int i = wk; i < LIVE; i += WK) {
-        f32x4 v = part[(wn * LIVE + i) * kWave + lane];
-#pragma unroll
-        for (int w = 1; w < WK; ++w) {
-          const f32x4 u = part[((w * WN + wn) * LIVE + i) * kWave + lane];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] += u[q];
-        }
-        store(i, v);
-      }
-    }
+    if (wave * 16 + c < rows)
+      *reinterpret_cast<bf16x4*>(a.y + (int64_t)(rt.begin + wave * 16 + c) * a.N + n0 + 4 * g) =
+          bf16x4{(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]};
   }
 }
 
-constexpr int kSkinnyRows = 64;
-
-template <bool SWIGLU, bool E8M0, int WK>
-__global__ void __launch_bounds__(512) skinny_kernel(const Fp8Kern a) {
-  __shared__ __attribute__((aligned(16))) float smem[WK > 1 ? 8 * 4 * kWave * 4 : kSkinnyRows * 8];
-  int mt, nt;
-  if (!fp8_tile(a, &mt, &nt)) return;
-  const int e = a.table[1 + 2 * mt], m_begin = a.table[2 + 2 * mt];
-  const int m_end = a.offsets ? min(a.offsets[e + 1], a.R) : a.R;
-  const int rows = min(m_end - m_begin, kSkinnyRows);
+template <bool E8M0>
+__global__ void __launch_bounds__(512) split_kernel(const Fp8Kern a) {
+  __shared__ f32x4 part[kSplitWaves * (kSplitRows / 16) * kWave];
+  RowTile rt;
+  int nt;
+  if (!group_tile(a.offsets, a.table, a.E, a.R, kSplitRows, a.n_tiles, a.group_n, &rt, &nt))
+    return;
+  const int rows = min(rt.end - rt.begin, kSplitRows);
   if (rows <= 16)
-    skinny_body<SWIGLU, E8M0, WK, 1, 4>(a, e, m_begin, rows, nt, smem);
+    split_body<E8M0, 1, 4>(a, rt, rows, nt, part);
   else if (rows <= 32)
-    skinny_body<SWIGLU, E8M0, WK, 2, 4>(a, e, m_begin, rows, nt, smem);
-  else if (rows <= 48)
-    skinny_body<SWIGLU, E8M0, WK, 3, 3>(a, e, m_begin, rows, nt, smem);
+    split_body<E8M0, 2, 3>(a, rt, rows, nt, part);
   else
-    skinny_body<SWIGLU, E8M0, WK, 4, 3>(a, e, m_begin, rows, nt, smem);
+    split_body<E8M0, 4, 2>(a, rt, rows, nt, part);
 }
 
 // ---------------------------------------------------------------------------------------
-// many rows per expert
+// tiles through LDS
 // ---------------------------------------------------------------------------------------
 // BM rows x 256 weight rows (with SwiGLU 128 gate and the 128 up rows of the same columns),
 // eight waves as 2 x 4, each 16-row tiles MT = BM / 32 by four 16-column tiles.  A stage of the
@@ -307,28 +234,30 @@ __device__ __attribute__((always_inline)) inline void fp8_body(
   const int rows = m_end - m_begin, KB = a.K / kScaleBlock;
   const bool issuer = wave >= 4;
 
-  // direct loads: one covers eight rows of 128 bytes; issuing wave d fills blocks 4 i + d
+  // Direct loads: one covers eight rows of 128 bytes; issuing wave d fills blocks 4 i + d.  The
+  // rows of blocks i and i + 1 are 32 apart, which leaves the lane's piece the same: one lane
+  // offset and a scalar for each i (weights; those past N, the upper half of a last column tile,
+  // read the lower half again).  Activation rows are gathered or clamped: an offset each.
+  // Few rows per expert: each weight line is read by one tile, and the non-temporal hint keeps
+  // it from displacing the activation rows (decode experts 1853 -> 1735 us).
   constexpr int nA = BM / 32, nB = 8;
+  constexpr bool kStreamW = BM <= 64;
   const int dslot = wave & 3;
   const int64_t w_row0 = (int64_t)e * a.N + nt * BN;
   const uint64_t base_a = uniform_u64(a.src ? a.xq : a.xq + (int64_t)m_begin * a.K);
-  const uint64_t base_b[2] = {uniform_u64(a.b0 + w_row0 * a.K),
-                              SWIGLU ? uniform_u64(a.b1 + w_row0 * a.K) : 0};
-  uint32_t va[nA], vb[nB];
-  auto piece = [&](int r) { return (uint32_t)(((lane & 7) ^ ((r >> 1) & 7)) * 16); };
+  const uint64_t base_b = uniform_u64(a.b0 + w_row0 * a.K);
+  const uint64_t base_b2 = SWIGLU ? uniform_u64(a.b1 + w_row0 * a.K)
+                                  : base_b + (nt * BN + 128 < a.N ? (uint64_t)128 * a.K : 0);
+  uint32_t va[nA];
+  const int dr = dslot * 8 + lane / 8;
+  const uint32_t piece = ((lane & 7) ^ ((dr >> 1) & 7)) * 16;
+  const uint32_t vb = (uint32_t)dr * (uint32_t)a.K + piece;
 #pragma unroll
   for (int i = 0; i < nA; ++i) {
-    const int r = (i * 4 + dslot) * 8 + lane / 8;
-    const int row = min(r, rows - 1);
-    va[i] = (uint32_t)(a.src ? x_row(a, m_begin + row) : row) * (uint32_t)a.K + piece(r);
+    const int row = min(i * 32 + dr, rows - 1);
+    va[i] = (uint32_t)(a.src ? x_row(a, m_begin + row) : row) * (uint32_t)a.K + piece;
   }
-#pragma unroll
-  for (int i = 0; i < nB; ++i) {
-    const int r = (i * 4 + dslot) * 8 + lane / 8;
-    const int row = SWIGLU ? r & 127 : min(r, a.N - 1 - nt * BN);
-    vb[i] = (uint32_t)row * (uint32_t)a.K + piece(r);
-  }
-  auto dma = [&](int kb, lds_char* abuf, lds_char* bbuf) {
+  auto dma_a = [&](int kb, lds_char* abuf) {
     if (!issuer) return;
     const uint32_t koff = (uint32_t)min(kb, KB - 1) * kScaleBlock;
 #pragma unroll
@@ -336,31 +265,49 @@ __device__ __attribute__((always_inline)) inline void fp8_body(
       __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_rsrc(base_a),
                                                abuf + (i * 4 + dslot) * 1024, 16, va[i], koff,
                                                0, 0);
+  };
+  auto dma_b = [&](int kb, lds_char* bbuf) {
+    if (!issuer) return;
+    const uint32_t koff = (uint32_t)min(kb, KB - 1) * kScaleBlock;
 #pragma unroll
     for (int i = 0; i < nB; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_rsrc(base_b[SWIGLU && i >= 4 ? 1 : 0]),
-                                               bbuf + (i * 4 + dslot) * 1024, 16, vb[i], koff,
-                                               0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_rsrc(i < 4 ? base_b : base_b2),
+                                               bbuf + (i * 4 + dslot) * 1024, 16, vb,
+                                               koff + (uint32_t)(i & 3) * 32u * (uint32_t)a.K, 0,
+                                               kStreamW ? 2 : 0);
   };
 
   // scales: thread t < BM brings row t's, one step ahead in registers, one in LDS
-  const bool scaler = tid < BM;
-  const int64_t wsi0 = ((int64_t)e * (a.N / 128) + nt * (BN / 128)) * KB;
+  constexpr int ES = E8M0 ? 1 : 4;  // bytes of a scale
   // the second block of weights: the up matrix, or the next 128 columns (the last column tile
   // of an odd count repeats its first)
-  const int64_t wsi1 = SWIGLU || (nt * 2 + 1) * 128 >= a.N ? wsi0 : wsi0 + KB;
-  const int64_t xsi =
-      scaler ? (int64_t)x_row(a, m_begin + min(tid, rows - 1)) * KB : 0;
+  const int64_t wsi = ((int64_t)e * (a.N / 128) + nt * (BN / 128)) * KB;
+  const uint64_t base_ws0 = uniform_u64(static_cast<const char*>(a.b0s) + wsi * ES);
+  const uint64_t base_ws1 =
+      SWIGLU ? uniform_u64(static_cast<const char*>(a.b1s) + wsi * ES)
+             : base_ws0 + (nt * BN + 128 < a.N ? (uint64_t)KB * ES : 0);
+  // (rows of a tile, or all gathered rows, lie within 2^31 bytes of scales)
+  const uint64_t base_xs =
+      uniform_u64(static_cast<const char*>(a.xs) + (a.src ? 0 : (int64_t)m_begin * KB * ES));
+  const int s_rel = min(tid, rows - 1);
+  const uint32_t vxs = (uint32_t)(a.src ? x_row(a, m_begin + s_rel) : s_rel) *
+                       (uint32_t)(KB * ES);
   uint32_t xs = 0, ws0 = 0, ws1 = 0;
+  auto scale_at = [&](uint64_t base, uint32_t voff, int k) -> uint32_t {
+    if constexpr (E8M0)
+      return __builtin_amdgcn_raw_buffer_load_b8(buffer_rsrc(base), voff, k, 0);
+    else
+      return __builtin_amdgcn_raw_buffer_load_b32(buffer_rsrc(base), voff, k * 4, 0);
+  };
   auto scale_load = [&](int kb) {
-    if (!scaler) return;
+    if (wave >= BM / 64) return;
     const int k = min(kb, KB - 1);
-    xs = load_scale<E8M0>(a.xs, xsi + k);
-    ws0 = load_scale<E8M0>(a.b0s, wsi0 + k);
-    ws1 = load_scale<E8M0>(SWIGLU ? a.b1s : a.b0s, wsi1 + k);
+    xs = scale_at(base_xs, vxs, k);
+    ws0 = scale_at(base_ws0, 0, k);
+    ws1 = scale_at(base_ws1, 0, k);
   };
   auto scale_put = [&](lds_u32* s) {
-    if (!scaler) return;
+    if (wave >= BM / 64) return;
     if constexpr (E8M0) {
       s[tid] = xs;
       if (tid == 0) {
@@ -381,45 +328,86 @@ __device__ __attribute__((always_inline)) inline void fp8_body(
 
   // 16-row tiles of this wave's band that hold rows
   const int band_rows = rows - wm * MT * 16;
-  const int live = band_rows <= 0 ? 0 : min(MT, (band_rows + 15) / 16);
+  const int live = band_rows <= 0 ? 0 : min(MT, (band_rows + 15) / 16);  // uniform
   const int swz = (c >> 1) & 7;
-  const int a_frag = (wm * MT * 16 + c) * 128, slot0 = (g ^ swz) * 16, slot1 = ((g + 4) ^ swz) * 16;
-  // weight rows of column tile j: with SwiGLU two gate tiles, then the up tiles of the same
-  // columns
-  auto b_row = [&](int j) {
-    return SWIGLU ? (j / 2) * 128 + wn * 32 + (j % 2) * 16 : wn * 64 + j * 16;
-  };
-  auto frag = [&](const lds_char* p) {
-    const u32x4 lo = *reinterpret_cast<const lds_u32x4*>(p + slot0);
-    const u32x4 hi = *reinterpret_cast<const lds_u32x4*>(p + slot1);
+  // a fragment's two pieces: byte offsets of the lane's row, row tiles and column tiles a
+  // constant apart; with SwiGLU a wave's column tiles are two gate tiles and the up tiles of the
+  // same columns
+  const int slot0 = (g ^ swz) * 16, slot1 = ((g + 4) ^ swz) * 16;
+  const int af0 = (wm * MT * 16 + c) * 128 + slot0, af1 = af0 - slot0 + slot1;
+  const int bf0 = (wn * (SWIGLU ? 32 : 64) + c) * 128 + slot0, bf1 = bf0 - slot0 + slot1;
+  auto frag = [&](const lds_char* buf, int o0, int o1, int rows_on) {
+    const u32x4 lo = *reinterpret_cast<const lds_u32x4*>(buf + o0 + rows_on * 128);
+    const u32x4 hi = *reinterpret_cast<const lds_u32x4*>(buf + o1 + rows_on * 128);
     return join(lo, hi);
   };
+  auto b_rows_on = [](int j) { return SWIGLU ? (j / 2) * 128 + (j % 2) * 16 : j * 16; };
   const int s_row = wm * MT * 16 + c;
-  auto compute = [&](const lds_char* abuf, const lds_char* bbuf, const lds_u32* s) {
-    i32x8 fb[NT];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) fb[j] = frag(bbuf + (b_row(j) + c) * 128);
-    uint32_t w0 = 0, w1 = 0;
-    if constexpr (E8M0) {
-      w0 = s[BM + (SWIGLU ? 0 : wn >> 1)];
-      w1 = SWIGLU ? s[BM + 1] : w0;
-    }
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      if (i >= live) break;
-      const i32x8 fa = frag(abuf + a_frag + i * 16 * 128);
+  // Multiply one stage.  The row fragments stream through a ring of three, each read two row
+  // tiles ahead of its MFMAs; the reads are spread between the MFMAs.  LIVE: the band's
+  // 16-row tiles that hold rows (compile-time; k_loop picks the copy).  fp32 scales: a row
+  // tile's four products are added to its sums behind the next tile's MFMAs.
+  auto compute = [&](const lds_char* abuf, const lds_char* bbuf, const lds_u32* s, auto live, auto mid) {
+    constexpr int LIVE = decltype(live)::value, RING = 3;
+    if constexpr (LIVE == 0) mid();
+    if constexpr (LIVE > 0) {
+      i32x8 fa[RING], fb[NT];
+      // (fp32 scales outlive their fragment by one row tile)
+      float sa[RING + 1], sb[RING + 1];
+      uint32_t sx[RING];
+      auto ld_a = [&](int i) {
+        fa[i % RING] = frag(abuf, af0, af1, i * 16);
+        if constexpr (E8M0) {
+          sx[i % RING] = s[s_row + i * 16];
+        } else {
+          sa[i % (RING + 1)] = __uint_as_float(s[(SWIGLU ? 0 : (wn >> 1) * BM) + s_row + i * 16]);
+          if constexpr (SWIGLU) sb[i % (RING + 1)] = __uint_as_float(s[BM + s_row + i * 16]);
+        }
+      };
+      uint32_t w0 = 0, w1 = 0;
       if constexpr (E8M0) {
-        const uint32_t sx = s[s_row + i * 16];
+        w0 = s[BM + (SWIGLU ? 0 : wn >> 1)];
+        w1 = SWIGLU ? s[BM + 1] : w0;
+      }
+      ld_a(0);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) mma_e8m0(acc[i][j], fb[j], fa, j < 2 ? w0 : w1, sx);
-      } else {
-        const float sa = __uint_as_float(s[(SWIGLU ? 0 : (wn >> 1) * BM) + s_row + i * 16]);
-        const float sb = SWIGLU ? __uint_as_float(s[BM + s_row + i * 16]) : sa;
-        f32x4 p[NT];
+      for (int j = 0; j < NT; ++j) fb[j] = frag(bbuf, bf0, bf1, b_rows_on(j));
+      if constexpr (LIVE > 1) ld_a(1);
+      mid();
+      constexpr int kAReads = SWIGLU && !E8M0 ? 4 : 3;  // LDS reads of one ld_a
+      f32x4 p[2][NT];
+      unroll_steps<LIVE>([&](auto I) {
+        constexpr int i = decltype(I)::value;
+        if constexpr (i + 2 < LIVE) ld_a(i + 2);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) p[j] = mma_zero(fb[j], fa);
+        for (int j = 0; j < NT; ++j) {
+          if constexpr (E8M0)
+            mma_e8m0(acc[i][j], fb[j], fa[i % RING], j < 2 ? w0 : w1, sx[i % RING]);
+          else
+            p[i & 1][j] = mma_zero(fb[j], fa[i % RING]);
+        }
+        if constexpr (!E8M0 && i > 0) {
 #pragma unroll
-        for (int j = 0; j < NT; ++j) add_scaled(acc[i][j], p[j], j < 2 ? sa : sb);
+          for (int j = 0; j < NT; ++j)
+            add_scaled(acc[i - 1][j], p[(i - 1) & 1][j],
+                       SWIGLU && j >= 2 ? sb[(i - 1) % (RING + 1)]
+                                        : sa[(i - 1) % (RING + 1)]);
+        }
+        // this tile's MFMAs, the reads and the previous tile's additions between them
+        constexpr int R = i + 2 < LIVE ? kAReads : 0;
+        unroll_steps<NT>([&](auto J) {
+          constexpr int j = decltype(J)::value;
+          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+          if constexpr (R > j) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          if constexpr (!E8M0 && i > 0) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+        });
+      });
+      if constexpr (!E8M0) {
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          add_scaled(acc[LIVE - 1][j], p[(LIVE - 1) & 1][j],
+                     SWIGLU && j >= 2 ? sb[(LIVE - 1) % (RING + 1)]
+                                        : sa[(LIVE - 1) % (RING + 1)]);
       }
     }
   };
@@ -438,23 +426,35 @@ __device__ __attribute__((always_inline)) inline void fp8_body(
   scale_load(0);
   scale_put(s0);
   scale_load(1);
-  unroll_steps<S - 1>([&](auto I) { dma(decltype(I)::value, buf_a(I), buf_b(I)); });
+  unroll_steps<S>([&](auto I) {
+    dma_b(decltype(I)::value, buf_b(I));
+    if constexpr (decltype(I)::value < S - 1) dma_a(decltype(I)::value, buf_a(I));
+  });
   constexpr int L = S % 2 == 0 ? S : 2 * S;  // the rings repeat
   if (issuer) __builtin_amdgcn_s_setprio(3);
-  auto step = [&](int k, auto I) {
+  auto step = [&](int k, auto I, auto live) {
     if (k >= KB) return;
     constexpr int i = decltype(I)::value;
     // a wave either issues direct loads or brings scales: the count leaves the direct loads
     // of the S - 2 later stages in flight
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * (nA + nB))
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * (nA + nB) + nB)
                  : "memory");
-    dma(k + S - 1, buf_a(IntC<i + S - 1>{}), buf_b(IntC<i + S - 1>{}));
+    dma_a(k + S - 1, buf_a(IntC<i + S - 1>{}));
     scale_put(i % 2 ? s0 : s1);
     scale_load(k + 2);
-    compute(buf_a(I), buf_b(I), i % 2 ? s1 : s0);
+    compute(buf_a(I), buf_b(I), i % 2 ? s1 : s0, live, [&] {
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      dma_b(k + S, buf_b(I));
+    });
   };
-  for (int k = 0; k < KB; k += L)
-    unroll_steps<L>([&](auto I) { step(k + decltype(I)::value, I); });
+  // one copy of the loop per count of live row tiles, so that nothing is tested between MFMAs
+  auto k_loop = [&](auto live) {
+    for (int k = 0; k < KB; k += L)
+      unroll_steps<L>([&](auto I) { step(k + decltype(I)::value, I, live); });
+  };
+  unroll_steps<MT + 1>([&](auto V) {
+    if (live == decltype(V)::value) k_loop(V);
+  });
   // drain the loads issued past the last stage before the LDS is used again
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
@@ -547,18 +547,17 @@ __device__ inline void fp8_run(const Fp8Kern& a, int e, int m_begin, int m_end, 
 template <int BM, bool SWIGLU, bool E8M0>
 __global__ void __launch_bounds__(512) fp8_kernel(const Fp8Kern a) {
   extern __shared__ __attribute__((aligned(1024))) char smem_dyn[];
-  int mt, nt;
-  if (!fp8_tile(a, &mt, &nt)) return;
-  const int e = a.table[1 + 2 * mt], m_begin = a.table[2 + 2 * mt];
-  const int m_end = a.offsets ? min(a.offsets[e + 1], a.R) : a.R;
+  RowTile rt;
+  int nt;
+  if (!group_tile(a.offsets, a.table, a.E, a.R, BM, a.n_tiles, a.group_n, &rt, &nt)) return;
   lds_char* base = (lds_char*)smem_dyn;
   if constexpr (BM > 128) {
-    if (m_end - m_begin > 128) {
-      fp8_run<BM, SWIGLU, E8M0>(a, e, m_begin, m_end, nt, base);
+    if (rt.end - rt.begin > 128) {
+      fp8_run<BM, SWIGLU, E8M0>(a, rt.e, rt.begin, rt.end, nt, base);
       return;
     }
   }
-  fp8_run<128, SWIGLU, E8M0>(a, e, m_begin, m_end, nt, base);
+  fp8_run<std::min(BM, 128), SWIGLU, E8M0>(a, rt.e, rt.begin, rt.end, nt, base);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -566,18 +565,20 @@ __global__ void __launch_bounds__(512) fp8_kernel(const Fp8Kern a) {
 // ---------------------------------------------------------------------------------------
 GroupPlan fp8_plan(int64_t R, int64_t E) {
   GroupPlan p;
-  p.small = R <= 32 * E;
-  p.bm = p.small ? kSkinnyRows : R <= 128 * E ? 128 : 256;
+  p.bm = R <= 32 * E ? 64 : R <= 128 * E ? 128 : 256;
   p.m_max = (R + E * (p.bm - 1)) / p.bm;
   return p;
 }
 
-template <bool SWIGLU, bool E8M0, int WK>
-static hipError_t run_skinny(Fp8Kern k, int64_t m_max, hipStream_t s) {
-  k.n_tiles = k.N / (128 / WK);
-  k.group_n = k.n_tiles;
-  skinny_kernel<SWIGLU, E8M0, WK>
-      <<<(unsigned)((m_max * k.n_tiles + 7) / 8 * 8), 512, 0, s>>>(k);
+// Bound on the blocks that hold a tile, of m_max x n_tiles, rounded up to the 8 XCDs' shares.
+static unsigned grid_of(int64_t m_max, int64_t n_tiles) {
+  return (unsigned)((m_max * n_tiles + 7) / 8 * 8);
+}
+
+template <bool E8M0>
+static hipError_t run_split(Fp8Kern k, int64_t m_max, hipStream_t s) {
+  k.n_tiles = k.group_n = k.N / 16;
+  split_kernel<E8M0><<<grid_of(m_max, k.n_tiles), 512, 0, s>>>(k);
   return hipGetLastError();
 }
 
@@ -585,28 +586,27 @@ template <int BM, bool SWIGLU, bool E8M0>
 static hipError_t run_tiles(Fp8Kern k, int64_t m_max, hipStream_t s) {
   constexpr int BN = SWIGLU ? 128 : 256;
   k.n_tiles = (k.N + BN - 1) / BN;
-  k.group_n = std::min(k.n_tiles, 8);
-  constexpr int lds = std::max(Fp8Tile<BM>::kLds, Fp8Tile<128>::kLds);
+  // few rows: the activations are what tiles share, so an expert's column tiles run together
+  // (decode experts 1735 -> 1726 us)
+  k.group_n = BM <= 64 ? k.n_tiles : std::min(k.n_tiles, 8);
+  constexpr int lds = std::max(Fp8Tile<BM>::kLds, Fp8Tile<std::min(BM, 128)>::kLds);
   hipError_t e = hipFuncSetAttribute((const void*)fp8_kernel<BM, SWIGLU, E8M0>,
                                      hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;
   fp8_kernel<BM, SWIGLU, E8M0>
-      <<<(unsigned)((m_max * k.n_tiles + 7) / 8 * 8), 512, lds, s>>>(k);
+      <<<grid_of(m_max, k.n_tiles), 512, lds, s>>>(k);
   return hipGetLastError();
 }
 
 template <bool SWIGLU, bool E8M0>
 static hipError_t run_fp8(const Fp8Kern& k, const GroupPlan& p, hipStream_t s) {
-  if (p.small) {
-    if constexpr (!SWIGLU) {
-      // a block of 128 columns for each row tile would leave most CUs idle: split the reduction
-      // over the block's waves and take fewer columns
-      const int64_t blocks = p.m_max * (k.N / 128);
-      if (blocks < 256) return run_skinny<SWIGLU, E8M0, 8>(k, p.m_max, s);
-      if (blocks < 1024) return run_skinny<SWIGLU, E8M0, 2>(k, p.m_max, s);
-    }
-    return run_skinny<SWIGLU, E8M0, 1>(k, p.m_max, s);
+  if constexpr (!SWIGLU) {
+    // at most 64 rows per expert on average and fewer 128-column tiles than CUs
+    const int64_t m64 = (k.R + (int64_t)k.E * (kSplitRows - 1)) / kSplitRows;
+    if (!k.table && k.R <= kSplitRows * k.E && m64 * (k.N / 128) < 256)
+      return run_split<E8M0>(k, m64, s);
   }
+  if (p.bm == 64) return run_tiles<64, SWIGLU, E8M0>(k, p.m_max, s);
   if (p.bm == 128) return run_tiles<128, SWIGLU, E8M0>(k, p.m_max, s);
   return run_tiles<256, SWIGLU, E8M0>(k, p.m_max, s);
 }
@@ -624,6 +624,7 @@ hipError_t launch_fp8_gemm(const Fp8Args& a, hipStream_t s) {
   k.b1 = (const uint8_t*)a.b1;
   k.b1s = a.b1_scale;
   k.R = (int)a.R;
+  k.E = (int)a.E;
   k.N = (int)a.N;
   k.K = (int)a.K;
   k.offsets = a.offsets;

@@ -6,6 +6,7 @@
 #include <utility>
 
 #include "common.h"
+#include "kernels.h"
 
 namespace moe {
 
@@ -69,6 +70,54 @@ __device__ inline void dense_tile(int i, int m_tiles, int n_tiles, int group_n, 
     *mt = rem / gw;
     *nt = full * group_n + rem % gw;
   }
+}
+
+// Tiles of rows grouped by expert.  With at most kScanExperts experts a wave finds its row tile
+// from the offsets themselves, one expert per lane, which saves the launch that writes the tile
+// table (about 2 us of its own and a gap before it); more experts take the table.
+static_assert(kScanExperts <= kWave, "one expert per lane");
+
+struct RowTile {
+  int e, begin, end;  // expert, first row, end of the expert's rows
+};
+
+// Block -> (row tile, column tile): the tiles are dealt to the 8 XCDs (blocks go round them in
+// turn) in contiguous shares of the tiles there are, so that a share's tiles keep their rows and
+// weights in one L2.  table: launch_tile_table's, or null (E <= kScanExperts).  offsets null: one
+// expert holds all R rows.  Offsets are clamped to [0, R].  False: no tile for this block.
+__device__ inline bool group_tile(const int32_t* offsets, const int32_t* table, int E, int R,
+                                  int bm, int n_tiles, int group_n, RowTile* rt, int* nt) {
+  int m_tiles, row0 = 0, tiles = 0, inc = 0;
+  if (table) {
+    m_tiles = table[0];
+  } else {
+    const int l = lane_id();
+    int row1 = 0;
+    if (l < E) {
+      row0 = offsets ? min(max(offsets[l], 0), R) : 0;
+      row1 = offsets ? min(offsets[l + 1], R) : R;
+    }
+    tiles = (max(row1 - row0, 0) + bm - 1) / bm;
+    inc = wave_inclusive_scan(tiles);
+    m_tiles = __builtin_amdgcn_readlane(inc, kWave - 1);
+  }
+  const int total = m_tiles * n_tiles;
+  const int xcd = blockIdx.x & 7, j = blockIdx.x >> 3, per = (total + 7) / 8;
+  const int i = xcd * per + j;
+  if (j >= per || i >= total) return false;
+  int mt;
+  dense_tile(i, m_tiles, n_tiles, group_n, &mt, nt);
+  if (table) {
+    rt->e = table[1 + 2 * mt];
+    rt->begin = table[2 + 2 * mt];
+  } else {
+    rt->e = __builtin_ctzll(__ballot(mt < inc));
+    rt->begin = __builtin_amdgcn_readlane(row0, rt->e) +
+                (mt - (__builtin_amdgcn_readlane(inc, rt->e) -
+                       __builtin_amdgcn_readlane(tiles, rt->e))) * bm;
+  }
+  rt->end = offsets ? min(offsets[rt->e + 1], R) : R;
+  return true;
 }
 
 }  // namespace moe

@@ -247,19 +247,14 @@ template <class T, class G>
 __global__ void __launch_bounds__(512)
 dgrad_kernel(const T* __restrict__ dy, const int32_t* __restrict__ offsets,
              const int32_t* __restrict__ table, const T* __restrict__ w, T* __restrict__ dx,
-             int R, int N, int K, int n_tiles, int group_n) {
+             int R, int E, int N, int K, int n_tiles, int group_n) {
   extern __shared__ __attribute__((aligned(1024))) char smem_dyn[];
-  const int m_tiles = table[0], total = m_tiles * n_tiles;
-  const int xcd = blockIdx.x & 7, j = blockIdx.x >> 3, per = (total + 7) / 8;
-  const int t = xcd * per + j;
-  if (j >= per || t >= total) return;
-  int mt, nt;
-  dense_tile(t, m_tiles, n_tiles, group_n, &mt, &nt);
-  const int e = table[1 + 2 * mt], m_begin = table[2 + 2 * mt];
-  const int m_end = offsets ? min(offsets[e + 1], R) : R;
+  RowTile rt;
+  int nt;
+  if (!group_tile(offsets, table, E, R, G::BM, n_tiles, group_n, &rt, &nt)) return;
   const int col0 = nt * G::BN;
-  grad_run<T, G>(dy + (int64_t)m_begin * N, N, min(m_end - m_begin, G::BM),
-                 w + (int64_t)e * N * K + col0, K, dx + (int64_t)m_begin * K + col0, K, N, 0,
+  grad_run<T, G>(dy + (int64_t)rt.begin * N, N, min(rt.end - rt.begin, G::BM),
+                 w + (int64_t)rt.e * N * K + col0, K, dx + (int64_t)rt.begin * K + col0, K, N, 0,
                  K - col0, (lds_char*)smem_dyn);
 }
 
@@ -290,7 +285,6 @@ wgrad_kernel(const T* __restrict__ dy, const T* __restrict__ x,
 GroupPlan dgrad_plan(int64_t R, int64_t E, int elt) {
   GroupPlan p;
   p.bm = elt == 4 || R <= 128 * E ? 128 : 256;
-  p.small = false;
   p.m_max = (R + E * (p.bm - 1)) / p.bm;
   return p;
 }
@@ -311,13 +305,13 @@ static hipError_t allow_lds(K kernel, int bytes) {
 
 template <class T, class G>
 static hipError_t run_dgrad(const T* dy, const int32_t* offsets, const int32_t* table,
-                            const T* w, T* dx, const GroupPlan& p, int64_t R, int64_t N,
-                            int64_t K, hipStream_t s) {
+                            const T* w, T* dx, const GroupPlan& p, int64_t R, int64_t E,
+                            int64_t N, int64_t K, hipStream_t s) {
   const int n_tiles = (int)((K + G::BN - 1) / G::BN);
   hipError_t e = allow_lds(dgrad_kernel<T, G>, G::kLds);
   if (e != hipSuccess) return e;
   dgrad_kernel<T, G><<<(unsigned)((p.m_max * n_tiles + 7) / 8 * 8), 512, G::kLds, s>>>(
-      dy, offsets, table, w, dx, (int)R, (int)N, (int)K, n_tiles, std::min(n_tiles, 8));
+      dy, offsets, table, w, dx, (int)R, (int)E, (int)N, (int)K, n_tiles, std::min(n_tiles, 8));
   return hipGetLastError();
 }
 
@@ -328,12 +322,12 @@ hipError_t launch_dgrad(int dtype, const void* dy, const int32_t* offsets,
   const GroupPlan p = dgrad_plan(R, E, dtype == 1 ? 2 : 4);
   if (dtype != 1)
     return run_dgrad<float, GradTile<float, 128, 128, false>>(
-        (const float*)dy, offsets, table, (const float*)w, (float*)dx, p, R, N, K, s);
+        (const float*)dy, offsets, table, (const float*)w, (float*)dx, p, R, E, N, K, s);
   if (p.bm == 128)
     return run_dgrad<bf16, GradTile<bf16, 128, 256, false>>(
-        (const bf16*)dy, offsets, table, (const bf16*)w, (bf16*)dx, p, R, N, K, s);
+        (const bf16*)dy, offsets, table, (const bf16*)w, (bf16*)dx, p, R, E, N, K, s);
   return run_dgrad<bf16, GradTile<bf16, 256, 256, false>>(
-      (const bf16*)dy, offsets, table, (const bf16*)w, (bf16*)dx, p, R, N, K, s);
+      (const bf16*)dy, offsets, table, (const bf16*)w, (bf16*)dx, p, R, E, N, K, s);
 }
 
 template <class T, class G>

@@ -137,13 +137,16 @@ hipError_t launch_tile_table(const int32_t* offsets, int64_t E, int64_t rows, in
 
 // Row tiling of a grouped product over R row slots of E experts.
 struct GroupPlan {
-  bool small;     // at most 32 rows per expert on average: the weight-streaming kernel
   int bm;         // row-tile height
   int64_t m_max;  // bound on the row tiles over all experts
 };
 GroupPlan fp8_plan(int64_t R, int64_t E);
 GroupPlan dgrad_plan(int64_t R, int64_t E, int elt);
 inline int64_t group_table_ints(const GroupPlan& p) { return 1 + 2 * p.m_max; }
+// Whether the grouped launches read a tile table: with few experts the blocks find their tiles
+// from the offsets (group_tile) and take a null table.
+constexpr int kScanExperts = 64;
+inline bool group_needs_table(int64_t E) { return E > kScanExperts; }
 
 // One 8-bit grouped product.  With b1 (the up weights; b0 then the gate weights): the output is
 // silu(gate) * up, quantized by rows into hq [R, N] and h_scale; else y [R, N] bf16.
@@ -159,14 +162,15 @@ struct Fp8Args {
   int64_t R, E, N, K;
   int scale_type;
   const int32_t* offsets;  // [E+1]
-  const int32_t* table;    // launch_tile_table of fp8_plan(R, E)
+  const int32_t* table;    // launch_tile_table of fp8_plan(R, E), or null (group_needs_table)
   void* y;
   void* hq;
   void* h_scale;
 };
 hipError_t launch_fp8_gemm(const Fp8Args& a, hipStream_t s);
 
-// dtype 0 fp32, 1 bf16.  dgrad reads the table of dgrad_plan; wgrad needs only the offsets.
+// dtype 0 fp32, 1 bf16.  dgrad reads the table of dgrad_plan (or null: group_needs_table); wgrad
+// needs only the offsets.
 hipError_t launch_dgrad(int dtype, const void* dy, const int32_t* offsets,
                         const int32_t* table, const void* w, void* dx, int64_t R, int64_t E,
                         int64_t N, int64_t K, hipStream_t s);

@@ -538,6 +538,15 @@ int check_group_call(const moe_group_shape* g, const int32_t* offsets, const voi
   return MOE_OK;
 }
 
+// The tile table of plan p in the workspace, where the launches read one; null otherwise.
+int group_table(const moe_group_shape* g, const moe::GroupPlan& p, const int32_t* offsets,
+                void* ws, int32_t** table, hipStream_t st) {
+  *table = moe::group_needs_table(g->E) ? static_cast<int32_t*>(ws) : nullptr;
+  if (!*table) return MOE_OK;
+  return hip_status(
+      moe::launch_tile_table(offsets, g->E, g->rows, p.bm, p.m_max, *table, st));
+}
+
 bool aligned4(const void* p) { return ((uintptr_t)p & 3u) == 0; }
 
 int check_fp8(const moe_fp8_tensor* w, int scale_type) {
@@ -608,11 +617,13 @@ int fp8_experts(const moe_shape* s, int scale_type, const void* x, const int32_t
   const int64_t cap = s->T > R ? s->T : R;  // rows the x region is laid out for
   char* xq = region<char>(ws, L, MOE_WS_X_PERM);
   char* hq = region<char>(ws, L, MOE_WS_H);
-  int32_t* table = region<int32_t>(ws, L, MOE_WS_SCHED);
+  int32_t* table = moe::group_needs_table(s->E) || table_ready
+                       ? region<int32_t>(ws, L, MOE_WS_SCHED)
+                       : nullptr;
   hipError_t e = moe::launch_quantize(x_rows, s->d, 1, s->dtype, scale_type, x, xq,
                                       xq + align_up(cap * s->d), st);
   if (e != hipSuccess) return MOE_ERR_HIP;
-  if (!table_ready) {
+  if (table && !table_ready) {
     const moe::GroupPlan p = moe::fp8_plan(R, s->E);
     if ((e = moe::launch_tile_table(offsets, s->E, R, p.bm, p.m_max, table, st)) != hipSuccess)
       return MOE_ERR_HIP;
@@ -688,11 +699,10 @@ int moe_grouped_gemm_fp8(const moe_group_shape* g, const void* xq, const void* x
   if ((rc = check_fp8(&w, g->scale_type)) != MOE_OK) return rc;
   if (!y) return MOE_ERR_INVALID_ARG;
   if (!aligned16(y)) return MOE_ERR_ALIGNMENT;
-  const moe::GroupPlan p = moe::fp8_plan(g->rows, g->E);
-  int32_t* table = static_cast<int32_t*>(ws);
-  if (moe::launch_tile_table(expert_offsets, g->E, g->rows, p.bm, p.m_max, table, st) !=
-      hipSuccess)
-    return MOE_ERR_HIP;
+  int32_t* table = nullptr;
+  if ((rc = group_table(g, moe::fp8_plan(g->rows, g->E), expert_offsets, ws, &table, st)) !=
+      MOE_OK)
+    return rc;
   moe::Fp8Args a = {};
   a.xq = xq;
   a.x_scale = x_scale;
@@ -712,16 +722,15 @@ int moe_grouped_gemm_fp8(const moe_group_shape* g, const void* xq, const void* x
 
 int moe_grouped_dgrad(const moe_group_shape* g, const void* dy, const int32_t* expert_offsets,
                       const void* w, void* ws, size_t ws_bytes, void* dx, hipStream_t st) {
-  const int rc = check_group_call(g, expert_offsets, ws, ws_bytes);
+  int rc = check_group_call(g, expert_offsets, ws, ws_bytes);
   if (rc != MOE_OK) return rc;
   if (g->rows == 0) return MOE_OK;
   if (!dy || !w || !dx) return MOE_ERR_INVALID_ARG;
   if (!aligned16(dy) || !aligned16(w) || !aligned16(dx)) return MOE_ERR_ALIGNMENT;
-  const moe::GroupPlan p = moe::dgrad_plan(g->rows, g->E, elt_bytes(g->dtype));
-  int32_t* table = static_cast<int32_t*>(ws);
-  if (moe::launch_tile_table(expert_offsets, g->E, g->rows, p.bm, p.m_max, table, st) !=
-      hipSuccess)
-    return MOE_ERR_HIP;
+  int32_t* table = nullptr;
+  if ((rc = group_table(g, moe::dgrad_plan(g->rows, g->E, elt_bytes(g->dtype)), expert_offsets, ws, &table, st)) !=
+      MOE_OK)
+    return rc;
   return hip_status(moe::launch_dgrad(g->dtype, dy, expert_offsets, table, w, dx, g->rows, g->E,
                                       g->N, g->K, st));
 }
