@@ -80,19 +80,20 @@ __device__ inline int x_row(const Fp8Kern& a, int r) {
 // few tiles
 // ---------------------------------------------------------------------------------------
 // A product whose column tiles are too few for the 256 CUs (a shared expert and a few tokens) is
-// bound by latency: 16 columns per block, every wave of the eight takes each eighth step of the
-// reduction with its weight and row fragments loaded straight into registers, D steps ahead, and
-// the sums are added through LDS in wave order.  LIVE: 16-row tiles that hold rows.
+// bound by latency: 16 NT columns per block, every wave of the eight takes each eighth step of
+// the reduction with its weight and row fragments loaded straight into registers, D steps ahead,
+// and the sums are added through LDS in wave order.  Each block reads all of its rows, so more rows
+// take more columns per block.  LIVE: 16-row tiles that hold rows.
 constexpr int kSplitRows = 64, kSplitWaves = 8;
 
-template <bool E8M0, int LIVE, int D>
+template <bool E8M0, int NT, int LIVE, int D>
 __device__ inline void split_body(const Fp8Kern& a, const RowTile& rt, int rows, int nt,
                                   f32x4* part) {
   constexpr int ES = E8M0 ? 1 : 4;
   const int lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int c = lane & 15, g = lane >> 4;
-  const int n0 = nt * 16, KB = a.K / kScaleBlock;
+  const int n0 = nt * 16 * NT, KB = a.K / kScaleBlock;
   const auto rw = buffer_rsrc(uniform_u64(a.b0 + ((int64_t)rt.e * a.N + n0) * a.K));
   const auto rx = buffer_rsrc(uniform_u64(a.xq + (int64_t)rt.begin * a.K));
   const auto rws = buffer_rsrc(uniform_u64(
@@ -100,7 +101,9 @@ __device__ inline void split_body(const Fp8Kern& a, const RowTile& rt, int rows,
       ((int64_t)rt.e * (a.N / kScaleBlock) + n0 / kScaleBlock) * KB * ES));
   const auto rxs =
       buffer_rsrc(uniform_u64(static_cast<const char*>(a.xs) + (int64_t)rt.begin * KB * ES));
-  const uint32_t vw = (uint32_t)c * (uint32_t)a.K + g * 16;
+  uint32_t vw[NT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) vw[j] = (uint32_t)(j * 16 + c) * (uint32_t)a.K + g * 16;
   uint32_t vx[LIVE], vs[LIVE];
 #pragma unroll
   for (int i = 0; i < LIVE; ++i) {
@@ -109,7 +112,7 @@ __device__ inline void split_body(const Fp8Kern& a, const RowTile& rt, int rows,
     vs[i] = row * (uint32_t)(KB * ES);
   }
   struct Step {
-    u32x4 w[2], x[LIVE][2];
+    u32x4 w[NT][2], x[LIVE][2];
     uint32_t ws, xs[LIVE];
   };
   auto scale_at = [&](const __amdgpu_buffer_rsrc_t& r, uint32_t voff, int kb) -> uint32_t {
@@ -119,10 +122,13 @@ __device__ inline void split_body(const Fp8Kern& a, const RowTile& rt, int rows,
       return __builtin_amdgcn_raw_buffer_load_b32(r, voff, kb * 4, 0);
   };
   auto load = [&](Step& s, int t) {
-    const int kb = min(wave + t * kSplitWaves, KB - 1);  // past the end: not used
+    const int kb = wave + t * kSplitWaves;
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      s.w[h] = __builtin_amdgcn_raw_buffer_load_b128(rw, vw, kb * kScaleBlock + h * 64, 2);
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        s.w[j][h] =
+            __builtin_amdgcn_raw_buffer_load_b128(rw, vw[j], kb * kScaleBlock + h * 64, 2);
 #pragma unroll
     for (int i = 0; i < LIVE; ++i)
 #pragma unroll
@@ -132,67 +138,75 @@ __device__ inline void split_body(const Fp8Kern& a, const RowTile& rt, int rows,
 #pragma unroll
     for (int i = 0; i < LIVE; ++i) s.xs[i] = scale_at(rxs, vs[i], kb);
   };
-  f32x4 acc[LIVE];
+  f32x4 acc[LIVE][NT];
 #pragma unroll
-  for (int i = 0; i < LIVE; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < LIVE; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
   auto multiply = [&](const Step& s) {
-    const i32x8 w = join(s.w[0], s.w[1]);
 #pragma unroll
     for (int i = 0; i < LIVE; ++i) {
       const i32x8 x = join(s.x[i][0], s.x[i][1]);
-      if constexpr (E8M0)
-        mma_e8m0(acc[i], w, x, s.ws, s.xs[i]);
-      else
-        add_scaled(acc[i], mma_zero(w, x), __uint_as_float(s.ws) * __uint_as_float(s.xs[i]));
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const i32x8 w = join(s.w[j][0], s.w[j][1]);
+        if constexpr (E8M0)
+          mma_e8m0(acc[i][j], w, x, s.ws, s.xs[i]);
+        else
+          add_scaled(acc[i][j], mma_zero(w, x),
+                     __uint_as_float(s.ws) * __uint_as_float(s.xs[i]));
+      }
     }
   };
   const int steps = (KB - wave + kSplitWaves - 1) / kSplitWaves;  // 0 past a short reduction
   Step ring[D];
 #pragma unroll
-  for (int d = 0; d < D; ++d) load(ring[d], d);
+  for (int d = 0; d < D; ++d)
+    if (d < steps) load(ring[d], d);
   for (int t = 0; t < steps; t += D) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {
       // keep the order: the loads of a slot right behind its last use, D steps ahead
       __builtin_amdgcn_sched_barrier(0);
-      if (t + d < steps) {
-        multiply(ring[d]);
-        load(ring[d], t + d + D);
-      }
+      if (t + d < steps) multiply(ring[d]);
+      if (t + d + D < steps) load(ring[d], t + d + D);
     }
   }
+  constexpr int TILES = LIVE * NT;
 #pragma unroll
-  for (int i = 0; i < LIVE; ++i) part[(wave * LIVE + i) * kWave + lane] = acc[i];
+  for (int i = 0; i < TILES; ++i) part[(wave * TILES + i) * kWave + lane] = acc[i / NT][i % NT];
   __syncthreads();
-  if (wave < LIVE) {
+  if (wave < TILES) {
+    const int i = wave / NT, j = wave % NT;
     f32x4 v = part[wave * kWave + lane];
 #pragma unroll
     for (int w = 1; w < kSplitWaves; ++w) {
-      const f32x4 u = part[(w * LIVE + wave) * kWave + lane];
+      const f32x4 u = part[(w * TILES + wave) * kWave + lane];
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] += u[q];
     }
     typedef bf16 bf16x4 __attribute__((ext_vector_type(4)));
-    if (wave * 16 + c < rows)
-      *reinterpret_cast<bf16x4*>(a.y + (int64_t)(rt.begin + wave * 16 + c) * a.N + n0 + 4 * g) =
+    if (i * 16 + c < rows)
+      *reinterpret_cast<bf16x4*>(a.y + (int64_t)(rt.begin + i * 16 + c) * a.N + n0 + j * 16 +
+                                 4 * g) =
           bf16x4{(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]};
   }
 }
 
-template <bool E8M0>
+template <bool E8M0, int NT>
 __global__ void __launch_bounds__(512) split_kernel(const Fp8Kern a) {
-  __shared__ f32x4 part[kSplitWaves * (kSplitRows / 16) * kWave];
+  __shared__ f32x4 part[kSplitWaves * (kSplitRows / 16) * NT * kWave];
   RowTile rt;
   int nt;
   if (!group_tile(a.offsets, a.table, a.E, a.R, kSplitRows, a.n_tiles, a.group_n, &rt, &nt))
     return;
   const int rows = min(rt.end - rt.begin, kSplitRows);
   if (rows <= 16)
-    split_body<E8M0, 1, 4>(a, rt, rows, nt, part);
+    split_body<E8M0, NT, 1, 4>(a, rt, rows, nt, part);
   else if (rows <= 32)
-    split_body<E8M0, 2, 3>(a, rt, rows, nt, part);
+    split_body<E8M0, NT, 2, 3>(a, rt, rows, nt, part);
   else
-    split_body<E8M0, 4, 2>(a, rt, rows, nt, part);
+    split_body<E8M0, NT, 4, NT == 1 ? 3 : 2>(a, rt, rows, nt, part);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -575,10 +589,10 @@ static unsigned grid_of(int64_t m_max, int64_t n_tiles) {
   return (unsigned)((m_max * n_tiles + 7) / 8 * 8);
 }
 
-template <bool E8M0>
+template <bool E8M0, int NT>
 static hipError_t run_split(Fp8Kern k, int64_t m_max, hipStream_t s) {
-  k.n_tiles = k.group_n = k.N / 16;
-  split_kernel<E8M0><<<grid_of(m_max, k.n_tiles), 512, 0, s>>>(k);
+  k.n_tiles = k.group_n = k.N / (16 * NT);
+  split_kernel<E8M0, NT><<<grid_of(m_max, k.n_tiles), 512, 0, s>>>(k);
   return hipGetLastError();
 }
 
@@ -604,7 +618,8 @@ static hipError_t run_fp8(const Fp8Kern& k, const GroupPlan& p, hipStream_t s) {
     // at most 64 rows per expert on average and fewer 128-column tiles than CUs
     const int64_t m64 = (k.R + (int64_t)k.E * (kSplitRows - 1)) / kSplitRows;
     if (!k.table && k.R <= kSplitRows * k.E && m64 * (k.N / 128) < 256)
-      return run_split<E8M0>(k, m64, s);
+      return k.R <= 16 * k.E || m64 * (k.N / 32) < 192 ? run_split<E8M0, 1>(k, m64, s)
+                                                       : run_split<E8M0, 2>(k, m64, s);
   }
   if (p.bm == 64) return run_tiles<64, SWIGLU, E8M0>(k, p.m_max, s);
   if (p.bm == 128) return run_tiles<128, SWIGLU, E8M0>(k, p.m_max, s);

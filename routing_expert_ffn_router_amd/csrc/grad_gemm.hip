@@ -28,22 +28,24 @@ typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
 typedef __attribute__((address_space(3))) uint32_t lds_u32;
 
-// Output tile BM x BN, 8 waves as WM x WN.  BP: reduction values per stage.
-// A "normal" operand is staged as BM rows of BP values (128 bytes), a "turned" one as BP rows of
-// BM (or BN) values.
-template <class T, int BM_, int BN_, bool A_TURNED_>
+// Output tile BM x BN, 8 waves as 2 x 4, each MT x NT MFMA tiles of 16 x 16.  BP: reduction values
+// per stage, two MFMA steps.  A "normal" operand is staged as BM rows of BP values (128 bytes), a
+// "turned" one as BP rows of BM (or BN) values.
+template <class T, int BM_, int BN_, bool A_TURNED_, int STAGES_>
 struct GradTile {
   static constexpr int BM = BM_, BN = BN_, WM = 2, WN = 4;
   static constexpr bool kATurned = A_TURNED_;
   static constexpr int kElt = sizeof(T);
-  static constexpr int BP = 128 / kElt;        // 64 bf16, 32 fp32
-  static constexpr int kStep = 64 / kElt;      // p per MFMA step: 32 bf16, 16 fp32
+  static constexpr int BP = 128 / kElt;  // 64 bf16, 32 fp32
   static constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
   static constexpr int kABytes = BM * BP * kElt, kBBytes = BN * BP * kElt;
-  static constexpr int kStages = 2;
+  static constexpr int kStages = STAGES_;
   static constexpr int kLds = kStages * (kABytes + kBBytes);
-  static constexpr int kALoads = kABytes / 8192, kBLoads = kBBytes / 8192;  // per wave
-  static_assert(kLds <= 160 * 1024 && kABytes % 8192 == 0 && kBBytes % 8192 == 0, "tile");
+  // direct loads of 1024 bytes per stage and issuing wave (waves 4-7)
+  static constexpr int kALoads = kABytes / 4096, kBLoads = kBBytes / 4096;
+  // a turned row is 512 bytes: one load covers two of them
+  static_assert(BN * kElt == 512 && (!A_TURNED_ || BM * kElt == 512), "turned rows");
+  static_assert(kStages >= 2 && kStages <= 4 && kLds <= 160 * 1024, "LDS of one CU");
 };
 
 // Slot of 16-byte piece q of row p in a turned operand's stage.  bf16: a wave's transposing reads
@@ -55,74 +57,85 @@ __device__ inline int turned_slot(int p, int q) {
   return q ^ (((p >> 2) & 3) << 2);
 }
 
-// A buffer resource over [base, base + bytes): loads past its end give zeros.
+// A buffer resource over [base, base + bytes): loads past its end give zeros.  (Loads lie within
+// 2^31 bytes of the base, so an end beyond that needs no exact value.)
 __device__ inline __amdgpu_buffer_rsrc_t bounded_rsrc(uint64_t base, int64_t bytes) {
   const int n = (int)min(max(bytes, (int64_t)0), (int64_t)0x7fffffff);
   return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), 0, n, 0x00020000);
 }
 
-// One tile.  A: normal operand rows a_row0.. (clamped to a_rows of them) of pitch a_pitch
-// elements, or turned operand columns a_col0..; B: turned columns b_col0...  p runs over [0, P)
-// of rows whose first is A / B themselves.
+// One tile.  A: a normal operand's first row, of a_rows rows of pitch a_pitch elements (rows past
+// them load as zeros), or a turned operand's first column, of a_rows columns; B: a turned operand's
+// first column, of b_cols.  The reduction runs over [0, P): a normal row's values, a turned
+// operand's rows.  C: the tile's first output; rows past a_rows and columns past b_cols are not
+// stored.
 template <class T, class G>
 __device__ __attribute__((always_inline)) inline void grad_body(
     const T* __restrict__ A, int64_t a_pitch, int a_rows, const T* __restrict__ B,
-    int64_t b_pitch, T* __restrict__ C, int64_t c_pitch, int64_t P, int64_t a_cols,
-    int64_t b_cols, lds_char* __restrict__ a0, lds_char* __restrict__ a1,
-    lds_char* __restrict__ b0, lds_char* __restrict__ b1) {
-  constexpr int E = sizeof(T), MT = G::MT, NT = G::NT;
+    int64_t b_pitch, T* __restrict__ C, int64_t c_pitch, int64_t P, int b_cols,
+    lds_char* __restrict__ a0, lds_char* __restrict__ a1, lds_char* __restrict__ a2,
+    lds_char* __restrict__ a3, lds_char* __restrict__ b0, lds_char* __restrict__ b1,
+    lds_char* __restrict__ b2, lds_char* __restrict__ b3) {
+  constexpr int E = sizeof(T), MT = G::MT, NT = G::NT, S = G::kStages;
   const int tid = threadIdx.x, lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int wm = wave / G::WN, wn = wave % G::WN;
+  const int wm = wave >> 2, wn = wave & 3;
   const int c = lane & 15, g = lane >> 4;
+  const bool issuer = wave >= 4;
+  const int dslot = wave & 3;
 
-  // direct loads: load i of wave w fills the 1024 bytes i * 8 + w of the stage, lane L the 16
-  // bytes L of them
-  uint32_t va[G::kALoads], vb[G::kBLoads];
-  auto turned_off = [&](int i, int row_bytes, int64_t pitch) {
-    const int at = (i * 8 + wave) * 64 + lane, pieces = row_bytes / 16;
-    const int p = at / pieces, slot = at % pieces;
-    return (uint32_t)(p * pitch * E) + (uint32_t)turned_slot<T>(p, slot) * 16;  // an involution
+  // Direct loads: load i of issuing wave d fills the 1024 bytes 4 i + d of the stage, lane L the 16
+  // bytes L of them.  Turned: rows 8 i + 2 d + (L / 32), whose slot permutation depends on i by
+  // its lowest bit only; a lane's offset for even and odd i and a scalar for the rows.  Columns
+  // past the operand's (the upper half of a last tile) read the lower half again.
+  auto turned_lane = [&](int odd, int64_t pitch, int cols) {
+    const int p = 8 * odd + 2 * dslot + lane / 32;
+    int byte = turned_slot<T>(p, lane % 32) * 16;  // the permutation undoes itself
+    if (byte >= cols * E) byte -= 128 * E;
+    return (uint32_t)((2 * dslot + lane / 32) * pitch * E) + (uint32_t)byte;
   };
-#pragma unroll
-  for (int i = 0; i < G::kALoads; ++i) {
-    if constexpr (G::kATurned) {
-      va[i] = turned_off(i, G::BM * E, a_pitch);
-    } else {
-      const int r = (i * 8 + wave) * 8 + lane / 8;
-      const int q = (lane & 7) ^ ((r >> 1) & 7);
-      va[i] = (uint32_t)min(r, a_rows - 1) * (uint32_t)(a_pitch * E) + q * 16;
-    }
+  uint32_t va[2], vb[2];
+  if constexpr (G::kATurned) {
+    va[0] = turned_lane(0, a_pitch, a_rows);
+    va[1] = turned_lane(1, a_pitch, a_rows);
+  } else {  // rows 32 i + 8 d + L / 8
+    const int r = dslot * 8 + lane / 8;
+    va[0] = va[1] =
+        (uint32_t)r * (uint32_t)(a_pitch * E) + (uint32_t)(((lane & 7) ^ ((r >> 1) & 7)) * 16);
   }
-#pragma unroll
-  for (int i = 0; i < G::kBLoads; ++i) vb[i] = turned_off(i, G::BN * E, b_pitch);
+  vb[0] = turned_lane(0, b_pitch, b_cols);
+  vb[1] = turned_lane(1, b_pitch, b_cols);
   const uint64_t base_a = uniform_u64(A), base_b = uniform_u64(B);
   const int steps = (int)((P + G::BP - 1) / G::BP);
-  auto dma = [&](int k, lds_char* abuf, lds_char* bbuf) {
-    if (k >= steps) return;
-    const int64_t p0 = (int64_t)k * G::BP;
-    // bytes from the stage's first value to the operand's end: rows p0 .. P - 1 of pitch, the
-    // last of them only the columns that exist
-    const int64_t bb = ((P - p0 - 1) * b_pitch + b_cols) * E;
-    const auto rb = bounded_rsrc(base_b + p0 * b_pitch * E, bb);
+  const uint32_t a_row = (uint32_t)(a_pitch * E), b_row = (uint32_t)(b_pitch * E);
+  // Stages past the last re-read it into a buffer nobody reads again, so that every step issues
+  // as many loads and the waits count a constant.
+  auto dma_a = [&](int k, lds_char* buf) {
+    if (!issuer) return;
+    const int64_t p0 = (int64_t)min(k, steps - 1) * G::BP;
     if constexpr (G::kATurned) {
-      const int64_t ab = ((P - p0 - 1) * a_pitch + a_cols) * E;
-      const auto ra = bounded_rsrc(base_a + p0 * a_pitch * E, ab);
+      const auto r = bounded_rsrc(base_a + p0 * a_row, (P - p0 - 1) * a_row + a_rows * E);
 #pragma unroll
       for (int i = 0; i < G::kALoads; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, abuf + (i * 8 + wave) * 1024, 16, va[i], 0,
-                                                 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, buf + (i * 4 + dslot) * 1024, 16, va[i & 1],
+                                                 (uint32_t)i * 8u * a_row, 0, 0);
     } else {
-      const auto ra = buffer_rsrc(base_a + p0 * E);
+      const auto r = bounded_rsrc(base_a, (int64_t)a_rows * a_row);
 #pragma unroll
       for (int i = 0; i < G::kALoads; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, abuf + (i * 8 + wave) * 1024, 16, va[i], 0,
-                                                 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, buf + (i * 4 + dslot) * 1024, 16, va[0],
+                                                 (uint32_t)p0 * E + (uint32_t)i * 32u * a_row, 0,
+                                                 0);
     }
+  };
+  auto dma_b = [&](int k, lds_char* buf) {
+    if (!issuer) return;
+    const int64_t p0 = (int64_t)min(k, steps - 1) * G::BP;
+    const auto r = bounded_rsrc(base_b + p0 * b_row, (P - p0 - 1) * b_row + b_cols * E);
 #pragma unroll
     for (int i = 0; i < G::kBLoads; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, bbuf + (i * 8 + wave) * 1024, 16, vb[i], 0, 0,
-                                               0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r, buf + (i * 4 + dslot) * 1024, 16, vb[i & 1],
+                                               (uint32_t)i * 8u * b_row, 0, 0);
   };
 
   f32x4 acc[MT][NT];
@@ -131,70 +144,143 @@ __device__ __attribute__((always_inline)) inline void grad_body(
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-  // Fragment of 16 columns col0.. of a turned operand for MFMA step ks: lane (c, g) gets column
-  // c's values p = 8 g .. 8 g + 7 (bf16) or 4 g .. 4 g + 3 (fp32) of the step, as a normal
-  // operand's 16-byte piece g holds them.
-  auto turned_frag = [&](const lds_char* buf, int row_bytes, int ks, int col0) -> u32x4 {
+  // Fragment of 16 columns of a turned operand for MFMA step ks of the stage: lane (c, g) gets
+  // column c's values p = 8 g .. 8 g + 7 (bf16) or 4 g .. 4 g + 3 (fp32) of the step, as a normal
+  // operand's 16-byte piece g holds them.  turned_at: the lane's byte for 16-column tile t; the
+  // rows that follow it are constants apart, since the permutation depends on the lane only.
+  auto turned_at = [&](int t) {
     if constexpr (E == 2) {
-      u32x4 v;
+      const int p = 8 * g + c / 4, byte = t * 32 + (c % 4) * 8;
+      return p * 512 + (turned_slot<T>(p, byte >> 4) << 4) + (byte & 15);
+    } else {
+      const int p = 4 * g, byte = t * 64 + c * 4;
+      return p * 512 + (turned_slot<T>(p, byte >> 4) << 4) + (byte & 15);
+    }
+  };
+  auto turned_frag = [&](const lds_char* buf, int at, int ks) -> u32x4 {
+    u32x4 v;
+    if constexpr (E == 2) {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const int p = ks * 32 + 8 * g + 4 * h + c / 4;
-        const int byte = col0 * 2 + (c % 4) * 8;
         const s16x4 t = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (lds_s16x4*)(buf + p * row_bytes + (turned_slot<T>(p, byte >> 4) << 4) + (byte & 15)));
+            (lds_s16x4*)(buf + at + (ks * 32 + 4 * h) * 512));
         typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
         const u32x2 w = __builtin_bit_cast(u32x2, t);
         v[2 * h] = w[0];
         v[2 * h + 1] = w[1];
       }
-      return v;
     } else {
-      u32x4 v;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int p = ks * 16 + 4 * g + i;
-        const int byte = (col0 + c) * 4;
-        v[i] = *reinterpret_cast<const lds_u32*>(buf + p * row_bytes +
-                                                 (turned_slot<T>(p, byte >> 4) << 4) + (byte & 15));
-      }
-      return v;
+      for (int i = 0; i < 4; ++i)
+        v[i] = *reinterpret_cast<const lds_u32*>(buf + at + (ks * 16 + i) * 512);
     }
+    return v;
   };
-  auto a_frag = [&](const lds_char* buf, int ks, int i) -> u32x4 {
-    const int r = (wm * MT + i) * 16;
-    if constexpr (G::kATurned) {
-      return turned_frag(buf, G::BM * E, ks, r);
-    } else {
-      return *reinterpret_cast<const lds_u32x4*>(buf + (r + c) * 128 +
-                                                 (((ks * 4 + g) ^ ((c >> 1) & 7)) << 4));
-    }
-  };
-  auto compute = [&](const lds_char* abuf, const lds_char* bbuf) {
+  int a_at[G::kATurned ? MT : 2], b_at[NT];
+  if constexpr (G::kATurned) {
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      u32x4 fb[NT];
+    for (int i = 0; i < MT; ++i) a_at[i] = turned_at(wm * MT + i);
+  } else {
 #pragma unroll
-      for (int j = 0; j < NT; ++j) fb[j] = turned_frag(bbuf, G::BN * E, ks, (wn * NT + j) * 16);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const u32x4 fa = a_frag(abuf, ks, i);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) mma_chunk(acc[i][j], fb[j], fa, T());
-      }
-    }
-  };
-  dma(0, a0, b0);
-  for (int k = 0; k < steps; k += 2) {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    dma(k + 1, a1, b1);
-    compute(a0, b0);
-    if (k + 1 < steps) {
-      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      dma(k + 2, a0, b0);
-      compute(a1, b1);
-    }
+    for (int ks = 0; ks < 2; ++ks)
+      a_at[ks] = (wm * MT * 16 + c) * 128 + (((ks * 4 + g) ^ ((c >> 1) & 7)) << 4);
   }
+#pragma unroll
+  for (int j = 0; j < NT; ++j) b_at[j] = turned_at(wn * NT + j);
+  auto a_frag = [&](const lds_char* buf, int ks, int i) -> u32x4 {
+    if constexpr (G::kATurned)
+      return turned_frag(buf, a_at[i], ks);
+    else
+      return *reinterpret_cast<const lds_u32x4*>(buf + a_at[ks] + i * 2048);
+  };
+  // 16-row tiles of this wave's band that hold rows
+  const int band_rows = a_rows - wm * MT * 16;
+  const int live = band_rows <= 0 ? 0 : min(MT, (band_rows + 15) / 16);
+  // Multiply one stage.  B's fragments of both steps are read first; mid() then releases B's buffer
+  // for the stage after next, while A's fragments stream through a ring of three row tiles.
+  auto compute = [&](const lds_char* abuf, const lds_char* bbuf, auto live_c, auto mid) {
+    constexpr int LIVE = decltype(live_c)::value, RING = 3;
+    if constexpr (LIVE == 0) {
+      mid();
+    } else {
+      u32x4 fa[RING][2], fb[2][NT];
+      auto ld_a = [&](int i) {
+        fa[i % RING][0] = a_frag(abuf, 0, i);
+        fa[i % RING][1] = a_frag(abuf, 1, i);
+      };
+      ld_a(0);
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) fb[ks][j] = turned_frag(bbuf, b_at[j], ks);
+      if constexpr (LIVE > 1) ld_a(1);
+      mid();
+      unroll_steps<LIVE>([&](auto I) {
+        constexpr int i = decltype(I)::value;
+        if constexpr (i + 2 < LIVE) ld_a(i + 2);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) mma_chunk(acc[i][j], fb[ks][j], fa[i % RING][ks], T());
+        if constexpr (E == 2) {  // the next tile's reads between this one's MFMAs
+          constexpr int R = i + 2 < LIVE ? (G::kATurned ? 4 : 2) : 0, M = 2 * NT;
+          unroll_steps<M>([&](auto MI) {
+            constexpr int m = decltype(MI)::value;
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            if constexpr (m < R) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+          });
+        }
+      });
+    }
+  };
+  auto buf_a = [&](auto I) -> lds_char* {
+    constexpr int j = decltype(I)::value % S;
+    return j == 0 ? a0 : j == 1 ? a1 : j == 2 ? a2 : a3;
+  };
+  auto buf_b = [&](auto I) -> lds_char* {
+    constexpr int j = decltype(I)::value % S;
+    return j == 0 ? b0 : j == 1 ? b1 : j == 2 ? b2 : b3;
+  };
+  constexpr int nA = G::kALoads, nB = G::kBLoads;
+  // Step k: stage k has landed (own loads waited for, then the barrier); A's stage k + S - 1 goes
+  // out into the buffer step k - 1 finished with, B's stage k + S once every wave holds this
+  // one's fragments.
+  auto step = [&](int k, auto I, auto live_c) {
+    if (k >= steps) return;
+    constexpr int i = decltype(I)::value;
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * (nA + nB) + nB)
+                 : "memory");
+    dma_a(k + S - 1, buf_a(IntC<i + S - 1>{}));
+    compute(buf_a(I), buf_b(I), live_c, [&] {
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      dma_b(k + S, buf_b(I));
+    });
+  };
+  if (steps > 0) {
+    unroll_steps<S>([&](auto I) {
+      dma_b(decltype(I)::value, buf_b(I));
+      if constexpr (decltype(I)::value < S - 1) dma_a(decltype(I)::value, buf_a(I));
+    });
+  }
+  if (issuer) __builtin_amdgcn_s_setprio(3);
+  auto k_loop = [&](auto live_c) {
+    for (int k = 0; k < steps; k += S)
+      unroll_steps<S>([&](auto I) { step(k + decltype(I)::value, I, live_c); });
+  };
+  // one copy of the loop per count of live row tiles; a turned operand's columns come in
+  // halves of the tile, so a band is whole or empty
+  if constexpr (G::kATurned) {
+    if (live == 0)
+      k_loop(IntC<0>{});
+    else
+      k_loop(IntC<MT>{});
+  } else {
+    unroll_steps<MT + 1>([&](auto V) {
+      if (live == decltype(V)::value) k_loop(V);
+    });
+  }
+  // drain the loads issued past the last stage before the LDS is used again
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
 
   // Epilogue through LDS, in passes of the row tiles that fit: B's fragment goes first in the
@@ -235,11 +321,14 @@ __device__ __attribute__((always_inline)) inline void grad_body(
 
 template <class T, class G>
 __device__ inline void grad_run(const T* A, int64_t a_pitch, int a_rows, const T* B,
-                                int64_t b_pitch, T* C, int64_t c_pitch, int64_t P,
-                                int64_t a_cols, int64_t b_cols, lds_char* base) {
-  lds_char* b = base + 2 * G::kABytes;
-  grad_body<T, G>(A, a_pitch, a_rows, B, b_pitch, C, c_pitch, P, a_cols, b_cols, base,
-                  base + G::kABytes, b, b + G::kBBytes);
+                                int64_t b_pitch, T* C, int64_t c_pitch, int64_t P, int b_cols,
+                                lds_char* base) {
+  constexpr int S = G::kStages, SA = G::kABytes, SB = G::kBBytes;
+  lds_char* b = base + S * SA;
+  // buffers past the ring's stages are never used
+  grad_body<T, G>(A, a_pitch, a_rows, B, b_pitch, C, c_pitch, P, b_cols, base, base + SA,
+                  base + (S > 2 ? 2 * SA : 0), base + (S > 3 ? 3 * SA : 0), b, b + SB,
+                  b + (S > 2 ? 2 * SB : 0), b + (S > 3 ? 3 * SB : 0));
 }
 
 // dgrad: one block per (row tile of an expert, 256 columns of K).
@@ -254,8 +343,8 @@ dgrad_kernel(const T* __restrict__ dy, const int32_t* __restrict__ offsets,
   if (!group_tile(offsets, table, E, R, G::BM, n_tiles, group_n, &rt, &nt)) return;
   const int col0 = nt * G::BN;
   grad_run<T, G>(dy + (int64_t)rt.begin * N, N, min(rt.end - rt.begin, G::BM),
-                 w + (int64_t)rt.e * N * K + col0, K, dx + (int64_t)rt.begin * K + col0, K, N, 0,
-                 K - col0, (lds_char*)smem_dyn);
+                 w + (int64_t)rt.e * N * K + col0, K, dx + (int64_t)rt.begin * K + col0, K, N,
+                 min(K - col0, G::BN), (lds_char*)smem_dyn);
 }
 
 // wgrad: one block per (expert, BM rows of N, BN columns of K).
@@ -276,7 +365,7 @@ wgrad_kernel(const T* __restrict__ dy, const T* __restrict__ x,
   const int row0 = mt * G::BM, col0 = nt * G::BN;
   grad_run<T, G>(dy + (int64_t)r0 * N + row0, N, min(N - row0, G::BM),
                  x + (int64_t)r0 * K + col0, K, dw + ((int64_t)e * N + row0) * K + col0, K,
-                 r1 - r0, N - row0, K - col0, (lds_char*)smem_dyn);
+                 r1 - r0, min(K - col0, G::BN), (lds_char*)smem_dyn);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -321,12 +410,12 @@ hipError_t launch_dgrad(int dtype, const void* dy, const int32_t* offsets,
   if (R <= 0) return hipSuccess;
   const GroupPlan p = dgrad_plan(R, E, dtype == 1 ? 2 : 4);
   if (dtype != 1)
-    return run_dgrad<float, GradTile<float, 128, 128, false>>(
+    return run_dgrad<float, GradTile<float, 128, 128, false, 4>>(
         (const float*)dy, offsets, table, (const float*)w, (float*)dx, p, R, E, N, K, s);
   if (p.bm == 128)
-    return run_dgrad<bf16, GradTile<bf16, 128, 256, false>>(
+    return run_dgrad<bf16, GradTile<bf16, 128, 256, false, 3>>(
         (const bf16*)dy, offsets, table, (const bf16*)w, (bf16*)dx, p, R, E, N, K, s);
-  return run_dgrad<bf16, GradTile<bf16, 256, 256, false>>(
+  return run_dgrad<bf16, GradTile<bf16, 256, 256, false, 2>>(
       (const bf16*)dy, offsets, table, (const bf16*)w, (bf16*)dx, p, R, E, N, K, s);
 }
 
@@ -344,9 +433,9 @@ static hipError_t run_wgrad(const T* dy, const T* x, const int32_t* offsets, T* 
 hipError_t launch_wgrad(int dtype, const void* dy, const void* x, const int32_t* offsets,
                         void* dw, int64_t R, int64_t E, int64_t N, int64_t K, hipStream_t s) {
   if (dtype != 1)
-    return run_wgrad<float, GradTile<float, 128, 128, true>>(
+    return run_wgrad<float, GradTile<float, 128, 128, true, 4>>(
         (const float*)dy, (const float*)x, offsets, (float*)dw, R, E, N, K, s);
-  return run_wgrad<bf16, GradTile<bf16, 256, 256, true>>(
+  return run_wgrad<bf16, GradTile<bf16, 256, 256, true, 2>>(
       (const bf16*)dy, (const bf16*)x, offsets, (bf16*)dw, R, E, N, K, s);
 }
 
