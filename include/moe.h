@@ -456,8 +456,9 @@ typedef struct {
   int32_t scale_type; /* moe_scale_type of the 8-bit operands; the gradients ignore it */
 } moe_group_shape;
 
-/* Bytes of device workspace the three grouped entry points below need (the tile table); 0 for
- * an invalid shape.  Host function. */
+/* Bytes of device workspace the three grouped entry points below need (the tile table and, for
+ * products with few, long tiles, up to 256 slots of fp32 partial sums, 64 MiB); 0 for an invalid
+ * shape.  The same size serves all three.  Host function. */
 size_t moe_group_workspace_size(const moe_group_shape* shape);
 
 /*

@@ -628,28 +628,6 @@ __device__ __attribute__((always_inline)) inline void prefill_gemm_tile(
       bb + SB, bb + (P::kBStages > 2 ? 2 * SB : 0), bb + (P::kBStages > 3 ? 3 * SB : 0));
 }
 
-// Down GEMM with few, long tiles: the tail split.  The t = m-tiles x n-tiles tiles (m-tiles
-// counted on the device) are numbered densely, n fastest within groups of group_n n-tiles.
-// The first floor(t / cus) * cus tiles run whole; the tail of t mod cus tiles, which would
-// leave most CUs idle through a last partial round, is split along the reduction into
-// S = min(s_max, cus / tail) pieces, each storing its tile of fp32 partial sums in a slot of
-// its own for tail_sum_kernel to add in piece order (deterministic).  S < 2: nothing splits.
-struct TailSplit {
-  int tiles, whole, tail, pieces;
-};
-__device__ inline TailSplit tail_split_of(int m_tiles, int n_tiles, int s_max) {
-  TailSplit p;
-  p.tiles = m_tiles * n_tiles;
-  p.whole = p.tiles / kSplitCUs * kSplitCUs;
-  p.tail = p.tiles - p.whole;
-  p.pieces = p.tail ? min(s_max, kSplitCUs / p.tail) : 1;
-  if (p.pieces < 2) {
-    p.whole = p.tiles;
-    p.tail = 0;
-    p.pieces = 1;
-  }
-  return p;
-}
 // One block per (m-tile, n-tile), or, with the tail split, per whole tile or per piece of a
 // tail tile.  Blocks are dealt round-robin to the 8 XCDs; the logical tile index is
 // remapped so each XCD walks a contiguous range of logical tiles, n fastest within

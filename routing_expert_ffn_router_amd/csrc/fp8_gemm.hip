@@ -41,7 +41,8 @@ struct Fp8Kern {
   bf16* y;
   uint8_t* hq;
   void* hs;
-  int n_tiles, group_n;
+  f32x4* partial;  // slots of partial sums (s_max > 1)
+  int n_tiles, group_n, s_max;
 };
 
 __device__ inline i32x8 join(const u32x4& a, const u32x4& b) {
@@ -196,10 +197,12 @@ __device__ inline void split_body(const Fp8Kern& a, const RowTile& rt, int rows,
 template <bool E8M0, int NT>
 __global__ void __launch_bounds__(512) split_kernel(const Fp8Kern a) {
   __shared__ f32x4 part[kSplitWaves * (kSplitRows / 16) * NT * kWave];
-  RowTile rt;
-  int nt;
-  if (!group_tile(a.offsets, a.table, a.E, a.R, kSplitRows, a.n_tiles, a.group_n, &rt, &nt))
+  TileWork w;
+  if (!tile_work(RowTiles(a.offsets, a.table, a.E, a.R, kSplitRows), a.n_tiles, a.group_n, 1,
+                 &w))
     return;
+  const RowTile rt = w.rt;
+  const int nt = w.nt;
   const int rows = min(rt.end - rt.begin, kSplitRows);
   if (rows <= 16)
     split_body<E8M0, NT, 1, 4>(a, rt, rows, nt, part);
@@ -234,7 +237,7 @@ typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
 
 template <int BM, bool SWIGLU, bool E8M0>
 __device__ __attribute__((always_inline)) inline void fp8_body(
-    const Fp8Kern& a, int e, int m_begin, int m_end, int nt, lds_char* __restrict__ a0,
+    const Fp8Kern& a, const TileWork& w, f32x4* __restrict__ slot, lds_char* __restrict__ a0,
     lds_char* __restrict__ a1, lds_char* __restrict__ a2, lds_char* __restrict__ b0,
     lds_char* __restrict__ b1, lds_char* __restrict__ b2, lds_u32* __restrict__ s0,
     lds_u32* __restrict__ s1) {
@@ -245,7 +248,11 @@ __device__ __attribute__((always_inline)) inline void fp8_body(
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int wm = wave >> 2, wn = wave & 3;
   const int c = lane & 15, g = lane >> 4;
-  const int rows = m_end - m_begin, KB = a.K / kScaleBlock;
+  const int e = w.rt.e, m_begin = w.rt.begin, nt = w.nt;
+  const int rows = w.rt.end - m_begin, KB = a.K / kScaleBlock;
+  // the steps of the reduction this block takes: all of them, or one piece
+  const int k_first = w.piece * KB / w.pieces;
+  const int steps = (w.piece + 1) * KB / w.pieces - k_first;
   const bool issuer = wave >= 4;
 
   // Direct loads: one covers eight rows of 128 bytes; issuing wave d fills blocks 4 i + d.  The
@@ -273,7 +280,7 @@ __device__ __attribute__((always_inline)) inline void fp8_body(
   }
   auto dma_a = [&](int kb, lds_char* abuf) {
     if (!issuer) return;
-    const uint32_t koff = (uint32_t)min(kb, KB - 1) * kScaleBlock;
+    const uint32_t koff = (uint32_t)(k_first + min(kb, steps - 1)) * kScaleBlock;
 #pragma unroll
     for (int i = 0; i < nA; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_rsrc(base_a),
@@ -282,7 +289,7 @@ __device__ __attribute__((always_inline)) inline void fp8_body(
   };
   auto dma_b = [&](int kb, lds_char* bbuf) {
     if (!issuer) return;
-    const uint32_t koff = (uint32_t)min(kb, KB - 1) * kScaleBlock;
+    const uint32_t koff = (uint32_t)(k_first + min(kb, steps - 1)) * kScaleBlock;
 #pragma unroll
     for (int i = 0; i < nB; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_rsrc(i < 4 ? base_b : base_b2),
@@ -315,7 +322,7 @@ __device__ __attribute__((always_inline)) inline void fp8_body(
   };
   auto scale_load = [&](int kb) {
     if (wave >= BM / 64) return;
-    const int k = min(kb, KB - 1);
+    const int k = k_first + min(kb, steps - 1);
     xs = scale_at(base_xs, vxs, k);
     ws0 = scale_at(base_ws0, 0, k);
     ws1 = scale_at(base_ws1, 0, k);
@@ -447,7 +454,7 @@ __device__ __attribute__((always_inline)) inline void fp8_body(
   constexpr int L = S % 2 == 0 ? S : 2 * S;  // the rings repeat
   if (issuer) __builtin_amdgcn_s_setprio(3);
   auto step = [&](int k, auto I, auto live) {
-    if (k >= KB) return;
+    if (k >= steps) return;
     constexpr int i = decltype(I)::value;
     // a wave either issues direct loads or brings scales: the count leaves the direct loads
     // of the S - 2 later stages in flight
@@ -463,7 +470,7 @@ __device__ __attribute__((always_inline)) inline void fp8_body(
   };
   // one copy of the loop per count of live row tiles, so that nothing is tested between MFMAs
   auto k_loop = [&](auto live) {
-    for (int k = 0; k < KB; k += L)
+    for (int k = 0; k < steps; k += L)
       unroll_steps<L>([&](auto I) { step(k + decltype(I)::value, I, live); });
   };
   unroll_steps<MT + 1>([&](auto V) {
@@ -471,6 +478,12 @@ __device__ __attribute__((always_inline)) inline void fp8_body(
   });
   // drain the loads issued past the last stage before the LDS is used again
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  if constexpr (!SWIGLU) {
+    if (slot) {  // one piece of the reduction: its partial sums
+      store_partial(slot, acc, live);
+      return;
+    }
+  }
   __syncthreads();
 
   // Epilogue through LDS: a lane holds four consecutive columns of row c of each 16-row tile.
@@ -544,14 +557,14 @@ __device__ __attribute__((always_inline)) inline void fp8_body(
 }
 
 template <int BM, bool SWIGLU, bool E8M0>
-__device__ inline void fp8_run(const Fp8Kern& a, int e, int m_begin, int m_end, int nt,
+__device__ inline void fp8_run(const Fp8Kern& a, const TileWork& w, f32x4* slot,
                                lds_char* base) {
   using P = Fp8Tile<BM>;
   constexpr int A = P::kABytes, B = P::kBBytes;
   lds_char* b = base + P::kStages * A;
   lds_u32* s = reinterpret_cast<lds_u32*>(base + P::kRing);
   // a third buffer exists only where the ring has three stages
-  fp8_body<BM, SWIGLU, E8M0>(a, e, m_begin, m_end, nt, base, base + A,
+  fp8_body<BM, SWIGLU, E8M0>(a, w, slot, base, base + A,
                              base + (P::kStages > 2 ? 2 * A : 0), b, b + B,
                              b + (P::kStages > 2 ? 2 * B : 0), s,
                              s + (P::kScaleWords * 4 + 255) / 256 * 64);
@@ -561,17 +574,18 @@ __device__ inline void fp8_run(const Fp8Kern& a, int e, int m_begin, int m_end, 
 template <int BM, bool SWIGLU, bool E8M0>
 __global__ void __launch_bounds__(512) fp8_kernel(const Fp8Kern a) {
   extern __shared__ __attribute__((aligned(1024))) char smem_dyn[];
-  RowTile rt;
-  int nt;
-  if (!group_tile(a.offsets, a.table, a.E, a.R, BM, a.n_tiles, a.group_n, &rt, &nt)) return;
+  TileWork w;
+  if (!tile_work(RowTiles(a.offsets, a.table, a.E, a.R, BM), a.n_tiles, a.group_n, a.s_max, &w))
+    return;
   lds_char* base = (lds_char*)smem_dyn;
+  f32x4* slot = w.slot < 0 ? nullptr : a.partial + (int64_t)w.slot * (BM * 64);
   if constexpr (BM > 128) {
-    if (rt.end - rt.begin > 128) {
-      fp8_run<BM, SWIGLU, E8M0>(a, rt.e, rt.begin, rt.end, nt, base);
+    if (w.rt.end - w.rt.begin > 128) {
+      fp8_run<BM, SWIGLU, E8M0>(a, w, slot, base);
       return;
     }
   }
-  fp8_run<std::min(BM, 128), SWIGLU, E8M0>(a, rt.e, rt.begin, rt.end, nt, base);
+  fp8_run<std::min(BM, 128), SWIGLU, E8M0>(a, w, slot, base);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -582,6 +596,22 @@ GroupPlan fp8_plan(int64_t R, int64_t E) {
   p.bm = R <= 32 * E ? 64 : R <= 128 * E ? 128 : 256;
   p.m_max = (R + E * (p.bm - 1)) / p.bm;
   return p;
+}
+
+GroupSplit group_split(const GroupPlan& p, int64_t columns, int64_t steps) {
+  GroupSplit g = {1, 0};
+  const int64_t n_tiles = (columns + 255) / 256, tiles = p.m_max * n_tiles;
+  // Worth a second launch and the partial sums' way through memory (about 30 us for 256 pieces)
+  // when a tile is long, and when the last partial round is a good part of all rounds.
+  if (steps >= 32 && tiles > 0 && tiles < 8 * kSplitCUs) {
+    g.s_max = (int)std::min<int64_t>(8, steps / 8);
+    g.bytes = std::min<int64_t>(kSplitCUs, tiles * g.s_max) * p.bm * 256 * 4;
+  }
+  return g;
+}
+
+GroupSplit fp8_split(int64_t R, int64_t E, int64_t N, int64_t K) {
+  return group_split(fp8_plan(R, E), N, K / kScaleBlock);
 }
 
 // Bound on the blocks that hold a tile, of m_max x n_tiles, rounded up to the 8 XCDs' shares.
@@ -600,6 +630,10 @@ template <int BM, bool SWIGLU, bool E8M0>
 static hipError_t run_tiles(Fp8Kern k, int64_t m_max, hipStream_t s) {
   constexpr int BN = SWIGLU ? 128 : 256;
   k.n_tiles = (k.N + BN - 1) / BN;
+  // tiles are cut along the reduction where the plan has room for their partial sums
+  const GroupSplit split = fp8_split(k.R, k.E, k.N, k.K);
+  k.s_max = SWIGLU ? 1 : split.s_max;
+  if (k.s_max > 1 && !k.partial) return hipErrorInvalidValue;
   // few rows: the activations are what tiles share, so an expert's column tiles run together
   // (decode experts 1735 -> 1726 us)
   k.group_n = BM <= 64 ? k.n_tiles : std::min(k.n_tiles, 8);
@@ -608,7 +642,10 @@ static hipError_t run_tiles(Fp8Kern k, int64_t m_max, hipStream_t s) {
                                      hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;
   fp8_kernel<BM, SWIGLU, E8M0>
-      <<<grid_of(m_max, k.n_tiles), 512, lds, s>>>(k);
+      <<<grid_of(m_max, k.n_tiles) + (k.s_max > 1 ? kSplitCUs : 0), 512, lds, s>>>(k);
+  if ((e = hipGetLastError()) != hipSuccess || k.s_max < 2) return e;
+  partial_sum_kernel<BM, (BM > 128)><<<dim3(kSplitCUs, 8 * (BM / 32) / 4), 256, 0, s>>>(
+      k.partial, k.offsets, k.table, k.E, k.R, k.n_tiles, k.group_n, k.s_max, k.N, k.y);
   return hipGetLastError();
 }
 
@@ -647,7 +684,9 @@ hipError_t launch_fp8_gemm(const Fp8Args& a, hipStream_t s) {
   k.y = (bf16*)a.y;
   k.hq = (uint8_t*)a.hq;
   k.hs = a.h_scale;
+  k.partial = (f32x4*)a.partial;
   k.n_tiles = k.group_n = 0;
+  k.s_max = 1;
   const bool e8m0 = a.scale_type == kScaleE8M0;
   if (a.b1) return e8m0 ? run_fp8<true, true>(k, p, s) : run_fp8<true, false>(k, p, s);
   return e8m0 ? run_fp8<false, true>(k, p, s) : run_fp8<false, false>(k, p, s);

@@ -77,47 +77,170 @@ __device__ inline void dense_tile(int i, int m_tiles, int n_tiles, int group_n, 
 // table (about 2 us of its own and a gap before it); more experts take the table.
 static_assert(kScanExperts <= kWave, "one expert per lane");
 
+// A grouped product with few, long tiles: the tail split.  The t = m-tiles x n-tiles tiles (m-tiles
+// counted on the device) are numbered densely, n fastest within groups of group_n n-tiles.
+// The first floor(t / cus) * cus tiles run whole; the tail of t mod cus tiles, which would
+// leave most CUs idle through a last partial round, is split along the reduction into
+// S = min(s_max, cus / tail) pieces, each storing its tile of fp32 partial sums in a slot of
+// its own for another launch to add in piece order (deterministic).  S < 2: nothing splits.
+struct TailSplit {
+  int tiles, whole, tail, pieces;
+};
+__device__ inline TailSplit tail_split_of(int m_tiles, int n_tiles, int s_max) {
+  TailSplit p;
+  p.tiles = m_tiles * n_tiles;
+  p.whole = p.tiles / kSplitCUs * kSplitCUs;
+  p.tail = p.tiles - p.whole;
+  p.pieces = p.tail ? min(s_max, kSplitCUs / p.tail) : 1;
+  if (p.pieces < 2) {
+    p.whole = p.tiles;
+    p.tail = 0;
+    p.pieces = 1;
+  }
+  return p;
+}
+
 struct RowTile {
   int e, begin, end;  // expert, first row, end of the expert's rows
 };
+// What a block computes: a row tile and column tile, whole (slot < 0) or `piece` of `pieces` of its
+// reduction, whose partial sums go to slot `slot`.
+struct TileWork {
+  RowTile rt;
+  int nt, slot, piece, pieces;
+};
 
-// Block -> (row tile, column tile): the tiles are dealt to the 8 XCDs (blocks go round them in
-// turn) in contiguous shares of the tiles there are, so that a share's tiles keep their rows and
-// weights in one L2.  table: launch_tile_table's, or null (E <= kScanExperts).  offsets null: one
-// expert holds all R rows.  Offsets are clamped to [0, R].  False: no tile for this block.
-__device__ inline bool group_tile(const int32_t* offsets, const int32_t* table, int E, int R,
-                                  int bm, int n_tiles, int group_n, RowTile* rt, int* nt) {
-  int m_tiles, row0 = 0, tiles = 0, inc = 0;
-  if (table) {
-    m_tiles = table[0];
-  } else {
-    const int l = lane_id();
-    int row1 = 0;
-    if (l < E) {
-      row0 = offsets ? min(max(offsets[l], 0), R) : 0;
-      row1 = offsets ? min(offsets[l + 1], R) : R;
+// The row tiles of the experts, as a wave holds them: from the table, or one expert per lane.
+struct RowTiles {
+  const int32_t* offsets;  // nullable: one expert holds all R rows
+  const int32_t* table;    // launch_tile_table's, or null (E <= kScanExperts)
+  int R, bm, count;
+  int row0, tiles, inc;  // lane's expert: first row, row tiles, row tiles up to and with it
+
+  __device__ inline RowTiles(const int32_t* offsets_, const int32_t* table_, int E, int R_,
+                             int bm_)
+      : offsets(offsets_), table(table_), R(R_), bm(bm_), row0(0), tiles(0), inc(0) {
+    if (table) {
+      count = table[0];
+    } else {
+      const int l = lane_id();
+      int row1 = 0;
+      if (l < E) {  // offsets are clamped to [0, R]
+        row0 = offsets ? min(max(offsets[l], 0), R) : 0;
+        row1 = offsets ? min(offsets[l + 1], R) : R;
+      }
+      tiles = (max(row1 - row0, 0) + bm - 1) / bm;
+      inc = wave_inclusive_scan(tiles);
+      count = __builtin_amdgcn_readlane(inc, kWave - 1);
     }
-    tiles = (max(row1 - row0, 0) + bm - 1) / bm;
-    inc = wave_inclusive_scan(tiles);
-    m_tiles = __builtin_amdgcn_readlane(inc, kWave - 1);
   }
-  const int total = m_tiles * n_tiles;
-  const int xcd = blockIdx.x & 7, j = blockIdx.x >> 3, per = (total + 7) / 8;
-  const int i = xcd * per + j;
-  if (j >= per || i >= total) return false;
-  int mt;
-  dense_tile(i, m_tiles, n_tiles, group_n, &mt, nt);
-  if (table) {
-    rt->e = table[1 + 2 * mt];
-    rt->begin = table[2 + 2 * mt];
+  __device__ inline RowTile at(int mt) const {
+    RowTile t;
+    if (table) {
+      t.e = table[1 + 2 * mt];
+      t.begin = table[2 + 2 * mt];
+    } else {
+      t.e = __builtin_ctzll(__ballot(mt < inc));
+      t.begin = __builtin_amdgcn_readlane(row0, t.e) +
+                (mt - (__builtin_amdgcn_readlane(inc, t.e) -
+                       __builtin_amdgcn_readlane(tiles, t.e))) * bm;
+    }
+    t.end = offsets ? min(offsets[t.e + 1], R) : R;
+    return t;
+  }
+};
+
+// Block -> work.  Blocks go round the 8 XCDs in turn; each XCD takes a contiguous share of the
+// tiles there are, so that its tiles keep their rows and weights in one L2, then (s_max > 1) its
+// share of the tail's pieces.  False: nothing for this block.
+__device__ inline bool tile_work(const RowTiles& rows, int n_tiles, int group_n, int s_max,
+                                 TileWork* w) {
+  const int xcd = blockIdx.x & 7, j = blockIdx.x >> 3;
+  TailSplit ts;
+  if (s_max > 1) {
+    ts = tail_split_of(rows.count, n_tiles, s_max);
   } else {
-    rt->e = __builtin_ctzll(__ballot(mt < inc));
-    rt->begin = __builtin_amdgcn_readlane(row0, rt->e) +
-                (mt - (__builtin_amdgcn_readlane(inc, rt->e) -
-                       __builtin_amdgcn_readlane(tiles, rt->e))) * bm;
+    ts.whole = rows.count * n_tiles;
+    ts.tail = 0;
   }
-  rt->end = offsets ? min(offsets[rt->e + 1], R) : R;
+  const int w8 = (ts.whole + 7) / 8;
+  int tile;
+  w->slot = -1;
+  w->piece = 0;
+  w->pieces = 1;
+  if (j < w8) {
+    tile = xcd * w8 + j;
+    if (tile >= ts.whole) return false;
+  } else {
+    if (ts.tail == 0) return false;
+    const int all = ts.tail * ts.pieces, q8 = (all + 7) / 8, q = xcd * q8 + (j - w8);
+    if (j - w8 >= q8 || q >= all) return false;
+    w->piece = q / ts.tail;
+    w->pieces = ts.pieces;
+    const int i = q - w->piece * ts.tail;
+    w->slot = i * ts.pieces + w->piece;
+    tile = ts.whole + i;
+  }
+  int mt;
+  dense_tile(tile, rows.count, n_tiles, group_n, &mt, &w->nt);
+  w->rt = rows.at(mt);
   return true;
+}
+
+// Stores of partial sums and their sum, for tiles of eight waves as 2 x 4 whose wave (wm, wn)
+// holds MT x NT tiles of 16 x 16, lane l holding row l % 16 and columns 4 (l / 16) .. + 3 of each:
+// the slot keeps the registers as they are, 1 KB for each 16 x 16 tile of each wave.
+template <int MT, int NT>
+__device__ inline void store_partial(f32x4* slot, const f32x4 (&acc)[MT][NT], int live) {
+  const int wave = threadIdx.x / kWave;
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    if (i >= live) break;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      slot[((wave * MT + i) * NT + j) * kWave + lane_id()] = acc[i][j];
+  }
+}
+
+// One wave per (tail tile, wave, row tile i): grid (kSplitCUs, 8 * MT / 4), surplus blocks exit.
+// SHORT: a tile of at most 128 rows was computed by the 128-row tile (4 row tiles per wave).
+template <int BM, bool SHORT>
+__global__ void __launch_bounds__(256)
+partial_sum_kernel(const f32x4* __restrict__ acc, const int32_t* __restrict__ offsets,
+                   const int32_t* __restrict__ table, int E, int R, int n_tiles, int group_n,
+                   int s_max, int N, bf16* __restrict__ y) {
+  constexpr int NT = 4;
+  const RowTiles rows(offsets, table, E, R, BM);
+  const TailSplit ts = tail_split_of(rows.count, n_tiles, s_max);
+  if ((int)blockIdx.x >= ts.tail) return;
+  int mt, nt;
+  dense_tile(ts.whole + blockIdx.x, rows.count, n_tiles, group_n, &mt, &nt);
+  const RowTile rt = rows.at(mt);
+  const int MT = SHORT && rt.end - rt.begin <= 128 ? 4 : BM / 32;
+  const int unit = blockIdx.y * 4 + threadIdx.x / kWave;  // wave * MT + i
+  const int wave = unit / MT, i = unit - wave * MT;
+  if (wave >= 8) return;
+  const int lane = lane_id(), row = ((wave >> 2) * MT + i) * 16 + (lane & 15);
+  if (row - (lane & 15) >= min(rt.end - rt.begin, BM)) return;
+  const bool stored = row < min(rt.end - rt.begin, BM);
+  // a slot holds 8 waves of BM / 32 row tiles, whichever tile filled it
+  constexpr int kSlot = 8 * (BM / 32) * NT * kWave;
+  const f32x4* src = acc + (int64_t)blockIdx.x * ts.pieces * kSlot + unit * NT * kWave + lane;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int col = nt * 256 + (wave & 3) * 64 + j * 16;
+    if (col >= N) break;
+    f32x4 v = src[j * kWave];
+    for (int p = 1; p < ts.pieces; ++p) {
+      const f32x4 u = src[(int64_t)p * kSlot + j * kWave];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) v[q] += u[q];
+    }
+    typedef bf16 bf16x4 __attribute__((ext_vector_type(4)));
+    if (stored)
+      *reinterpret_cast<bf16x4*>(y + (int64_t)(rt.begin + row) * N + col + 4 * (lane >> 4)) =
+          bf16x4{(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]};
+  }
 }
 
 }  // namespace moe

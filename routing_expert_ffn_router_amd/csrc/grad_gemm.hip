@@ -68,12 +68,12 @@ __device__ inline __amdgpu_buffer_rsrc_t bounded_rsrc(uint64_t base, int64_t byt
 // them load as zeros), or a turned operand's first column, of a_rows columns; B: a turned operand's
 // first column, of b_cols.  The reduction runs over [0, P): a normal row's values, a turned
 // operand's rows.  C: the tile's first output; rows past a_rows and columns past b_cols are not
-// stored.
+// stored.  slot (nullable): the sums are one piece of the reduction and go there instead.
 template <class T, class G>
 __device__ __attribute__((always_inline)) inline void grad_body(
     const T* __restrict__ A, int64_t a_pitch, int a_rows, const T* __restrict__ B,
-    int64_t b_pitch, T* __restrict__ C, int64_t c_pitch, int64_t P, int b_cols,
-    lds_char* __restrict__ a0, lds_char* __restrict__ a1, lds_char* __restrict__ a2,
+    int64_t b_pitch, T* __restrict__ C, f32x4* __restrict__ slot, int64_t c_pitch, int64_t P,
+    int b_cols, lds_char* __restrict__ a0, lds_char* __restrict__ a1, lds_char* __restrict__ a2,
     lds_char* __restrict__ a3, lds_char* __restrict__ b0, lds_char* __restrict__ b1,
     lds_char* __restrict__ b2, lds_char* __restrict__ b3) {
   constexpr int E = sizeof(T), MT = G::MT, NT = G::NT, S = G::kStages;
@@ -281,6 +281,12 @@ __device__ __attribute__((always_inline)) inline void grad_body(
   }
   // drain the loads issued past the last stage before the LDS is used again
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  if constexpr (E == 2 && !G::kATurned) {
+    if (slot) {
+      store_partial(slot, acc, live);
+      return;
+    }
+  }
   __syncthreads();
 
   // Epilogue through LDS, in passes of the row tiles that fit: B's fragment goes first in the
@@ -321,30 +327,34 @@ __device__ __attribute__((always_inline)) inline void grad_body(
 
 template <class T, class G>
 __device__ inline void grad_run(const T* A, int64_t a_pitch, int a_rows, const T* B,
-                                int64_t b_pitch, T* C, int64_t c_pitch, int64_t P, int b_cols,
-                                lds_char* base) {
+                                int64_t b_pitch, T* C, f32x4* slot, int64_t c_pitch, int64_t P,
+                                int b_cols, lds_char* base) {
   constexpr int S = G::kStages, SA = G::kABytes, SB = G::kBBytes;
   lds_char* b = base + S * SA;
   // buffers past the ring's stages are never used
-  grad_body<T, G>(A, a_pitch, a_rows, B, b_pitch, C, c_pitch, P, b_cols, base, base + SA,
+  grad_body<T, G>(A, a_pitch, a_rows, B, b_pitch, C, slot, c_pitch, P, b_cols, base, base + SA,
                   base + (S > 2 ? 2 * SA : 0), base + (S > 3 ? 3 * SA : 0), b, b + SB,
                   b + (S > 2 ? 2 * SB : 0), b + (S > 3 ? 3 * SB : 0));
 }
 
-// dgrad: one block per (row tile of an expert, 256 columns of K).
+// dgrad: one block per (row tile of an expert, 256 columns of K), or per piece of its reduction.
 template <class T, class G>
 __global__ void __launch_bounds__(512)
 dgrad_kernel(const T* __restrict__ dy, const int32_t* __restrict__ offsets,
              const int32_t* __restrict__ table, const T* __restrict__ w, T* __restrict__ dx,
-             int R, int E, int N, int K, int n_tiles, int group_n) {
+             f32x4* __restrict__ partial, int R, int E, int N, int K, int n_tiles, int group_n,
+             int s_max) {
   extern __shared__ __attribute__((aligned(1024))) char smem_dyn[];
-  RowTile rt;
-  int nt;
-  if (!group_tile(offsets, table, E, R, G::BM, n_tiles, group_n, &rt, &nt)) return;
-  const int col0 = nt * G::BN;
-  grad_run<T, G>(dy + (int64_t)rt.begin * N, N, min(rt.end - rt.begin, G::BM),
-                 w + (int64_t)rt.e * N * K + col0, K, dx + (int64_t)rt.begin * K + col0, K, N,
-                 min(K - col0, G::BN), (lds_char*)smem_dyn);
+  TileWork k;
+  if (!tile_work(RowTiles(offsets, table, E, R, G::BM), n_tiles, group_n, s_max, &k)) return;
+  const int col0 = k.nt * G::BN, steps = (N + G::BP - 1) / G::BP;
+  const int p0 = k.piece * steps / k.pieces * G::BP;
+  const int p1 = min((k.piece + 1) * steps / k.pieces * G::BP, N);
+  f32x4* slot = k.slot < 0 ? nullptr : partial + (int64_t)k.slot * (G::BM * G::BN / 4);
+  grad_run<T, G>(dy + (int64_t)k.rt.begin * N + p0, N, min(k.rt.end - k.rt.begin, G::BM),
+                 w + ((int64_t)k.rt.e * N + p0) * K + col0, K,
+                 dx + (int64_t)k.rt.begin * K + col0, slot, K, p1 - p0, min(K - col0, G::BN),
+                 (lds_char*)smem_dyn);
 }
 
 // wgrad: one block per (expert, BM rows of N, BN columns of K).
@@ -364,7 +374,7 @@ wgrad_kernel(const T* __restrict__ dy, const T* __restrict__ x,
   const int r1 = offsets ? min(max(offsets[e + 1], r0), R) : R;
   const int row0 = mt * G::BM, col0 = nt * G::BN;
   grad_run<T, G>(dy + (int64_t)r0 * N + row0, N, min(N - row0, G::BM),
-                 x + (int64_t)r0 * K + col0, K, dw + ((int64_t)e * N + row0) * K + col0, K,
+                 x + (int64_t)r0 * K + col0, K, dw + ((int64_t)e * N + row0) * K + col0, nullptr, K,
                  r1 - r0, min(K - col0, G::BN), (lds_char*)smem_dyn);
 }
 
@@ -381,7 +391,7 @@ GroupPlan dgrad_plan(int64_t R, int64_t E, int elt) {
 int64_t group_max_blocks(int64_t R, int64_t E, int64_t N, int64_t K, int elt) {
   // row operands: at most (R + 63 E) / 64 row tiles by ceil(columns / 128), and up to 2048 blocks
   // where few blocks are split further; wgrad: every tile of every expert's weight
-  const int64_t rows = (R + E * 63) / 64 * (std::max(N, K) / 128) + 2048;
+  const int64_t rows = (R + E * 63) / 64 * (std::max(N, K) / 128) + 2048 + kSplitCUs;
   const int64_t b = elt == 2 ? 256 : 128;
   return std::max(rows, E * ((N + b - 1) / b) * ((K + b - 1) / b)) + 8;
 }
@@ -392,31 +402,51 @@ static hipError_t allow_lds(K kernel, int bytes) {
                              bytes);
 }
 
+GroupSplit dgrad_split(int64_t R, int64_t E, int64_t N, int64_t K, int elt) {
+  if (elt != 2) return GroupSplit{1, 0};
+  return group_split(dgrad_plan(R, E, elt), K, N / 64);
+}
+
 template <class T, class G>
 static hipError_t run_dgrad(const T* dy, const int32_t* offsets, const int32_t* table,
-                            const T* w, T* dx, const GroupPlan& p, int64_t R, int64_t E,
-                            int64_t N, int64_t K, hipStream_t s) {
-  const int n_tiles = (int)((K + G::BN - 1) / G::BN);
+                            const T* w, T* dx, void* partial, int64_t m_max, int64_t R,
+                            int64_t E, int64_t N, int64_t K, hipStream_t s) {
+  const int n_tiles = (int)((K + G::BN - 1) / G::BN), group_n = std::min(n_tiles, 8);
+  const int s_max = dgrad_split(R, E, N, K, sizeof(T)).s_max;
+  if (s_max > 1 && !partial) return hipErrorInvalidValue;
   hipError_t e = allow_lds(dgrad_kernel<T, G>, G::kLds);
   if (e != hipSuccess) return e;
-  dgrad_kernel<T, G><<<(unsigned)((p.m_max * n_tiles + 7) / 8 * 8), 512, G::kLds, s>>>(
-      dy, offsets, table, w, dx, (int)R, (int)E, (int)N, (int)K, n_tiles, std::min(n_tiles, 8));
-  return hipGetLastError();
+  const unsigned grid =
+      (unsigned)((m_max * n_tiles + 7) / 8 * 8) + (s_max > 1 ? kSplitCUs : 0);
+  dgrad_kernel<T, G><<<grid, 512, G::kLds, s>>>(dy, offsets, table, w, dx, (f32x4*)partial,
+                                                (int)R, (int)E, (int)N, (int)K, n_tiles, group_n,
+                                                s_max);
+  if ((e = hipGetLastError()) != hipSuccess || s_max < 2) return e;
+  if constexpr (sizeof(T) == 2) {
+    partial_sum_kernel<G::BM, false><<<dim3(kSplitCUs, 8 * G::MT / 4), 256, 0, s>>>(
+        (const f32x4*)partial, offsets, table, (int)E, (int)R, n_tiles, group_n, s_max, (int)K,
+        dx);
+    return hipGetLastError();
+  }
+  return hipErrorInvalidValue;
 }
 
 hipError_t launch_dgrad(int dtype, const void* dy, const int32_t* offsets,
-                        const int32_t* table, const void* w, void* dx, int64_t R, int64_t E,
-                        int64_t N, int64_t K, hipStream_t s) {
+                        const int32_t* table, const void* w, void* dx, void* partial, int64_t R,
+                        int64_t E, int64_t N, int64_t K, hipStream_t s) {
   if (R <= 0) return hipSuccess;
   const GroupPlan p = dgrad_plan(R, E, dtype == 1 ? 2 : 4);
   if (dtype != 1)
     return run_dgrad<float, GradTile<float, 128, 128, false, 4>>(
-        (const float*)dy, offsets, table, (const float*)w, (float*)dx, p, R, E, N, K, s);
+        (const float*)dy, offsets, table, (const float*)w, (float*)dx, partial, p.m_max, R, E, N,
+        K, s);
   if (p.bm == 128)
     return run_dgrad<bf16, GradTile<bf16, 128, 256, false, 3>>(
-        (const bf16*)dy, offsets, table, (const bf16*)w, (bf16*)dx, p, R, E, N, K, s);
+        (const bf16*)dy, offsets, table, (const bf16*)w, (bf16*)dx, partial, p.m_max, R, E, N, K,
+        s);
   return run_dgrad<bf16, GradTile<bf16, 256, 256, false, 2>>(
-      (const bf16*)dy, offsets, table, (const bf16*)w, (bf16*)dx, p, R, E, N, K, s);
+      (const bf16*)dy, offsets, table, (const bf16*)w, (bf16*)dx, partial, p.m_max, R, E, N, K,
+      s);
 }
 
 template <class T, class G>

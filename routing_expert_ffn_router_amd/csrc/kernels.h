@@ -142,6 +142,15 @@ struct GroupPlan {
 };
 GroupPlan fp8_plan(int64_t R, int64_t E);
 GroupPlan dgrad_plan(int64_t R, int64_t E, int elt);
+// The tail split of a product in 256-column tiles whose reduction takes `steps` steps: the most
+// pieces a tail tile is cut into (1: no split), and the bytes of their partial sums.
+struct GroupSplit {
+  int s_max;
+  int64_t bytes;
+};
+GroupSplit group_split(const GroupPlan& p, int64_t columns, int64_t steps);
+GroupSplit fp8_split(int64_t R, int64_t E, int64_t N, int64_t K);
+GroupSplit dgrad_split(int64_t R, int64_t E, int64_t N, int64_t K, int elt);
 inline int64_t group_table_ints(const GroupPlan& p) { return 1 + 2 * p.m_max; }
 // Whether the grouped launches read a tile table: with few experts the blocks find their tiles
 // from the offsets (group_tile) and take a null table.
@@ -166,14 +175,15 @@ struct Fp8Args {
   void* y;
   void* hq;
   void* h_scale;
+  void* partial;  // fp8_split().bytes of partial sums (not with b1)
 };
 hipError_t launch_fp8_gemm(const Fp8Args& a, hipStream_t s);
 
-// dtype 0 fp32, 1 bf16.  dgrad reads the table of dgrad_plan (or null: group_needs_table); wgrad
+// dtype 0 fp32, 1 bf16.  partial: dgrad_split().bytes.  dgrad reads the table of dgrad_plan (or null: group_needs_table); wgrad
 // needs only the offsets.
 hipError_t launch_dgrad(int dtype, const void* dy, const int32_t* offsets,
-                        const int32_t* table, const void* w, void* dx, int64_t R, int64_t E,
-                        int64_t N, int64_t K, hipStream_t s);
+                        const int32_t* table, const void* w, void* dx, void* partial, int64_t R,
+                        int64_t E, int64_t N, int64_t K, hipStream_t s);
 hipError_t launch_wgrad(int dtype, const void* dy, const void* x, const int32_t* offsets,
                         void* dw, int64_t R, int64_t E, int64_t N, int64_t K, hipStream_t s);
 // Upper bound on the blocks (512 threads each) of the grouped launches above.

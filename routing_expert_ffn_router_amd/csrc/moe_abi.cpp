@@ -526,13 +526,24 @@ int64_t group_table_bytes(int64_t R, int64_t E, int elt) {
   return align_up((a > b ? a : b) * 4);
 }
 
+// The tile table, then the partial sums of split tiles.
+int64_t group_workspace(const moe_group_shape* g) {
+  const int elt = elt_bytes(g->dtype);
+  const int64_t a = moe::fp8_split(g->rows, g->E, g->N, g->K).bytes;
+  const int64_t b = moe::dgrad_split(g->rows, g->E, g->N, g->K, elt).bytes;
+  return group_table_bytes(g->rows, g->E, elt) + (a > b ? a : b);
+}
+void* group_partial(const moe_group_shape* g, void* ws) {
+  return static_cast<char*>(ws) + group_table_bytes(g->rows, g->E, elt_bytes(g->dtype));
+}
+
 // Checks shared by the grouped entry points; the operands are checked by the caller.
 int check_group_call(const moe_group_shape* g, const int32_t* offsets, const void* ws,
                      size_t ws_bytes) {
   const int rc = check_group(g);
   if (rc != MOE_OK) return rc;
   if (!offsets && g->E != 1) return MOE_ERR_INVALID_ARG;
-  if (!ws || (int64_t)ws_bytes < group_table_bytes(g->rows, g->E, elt_bytes(g->dtype)))
+  if (!ws || (int64_t)ws_bytes < group_workspace(g))
     return MOE_ERR_WORKSPACE;
   if (((uintptr_t)ws & (kAlign - 1)) != 0) return MOE_ERR_ALIGNMENT;
   return MOE_OK;
@@ -574,14 +585,14 @@ int check_fp8_shape(const moe_shape* s, int scale_type) {
   return MOE_OK;
 }
 
-// The regions of moe_layer with the row buffers in 8 bits and no split reductions.
+// The regions of moe_layer with the row buffers in 8 bits.
 Layout fp8_layout(const moe_shape* s, int scale_type) {
   Layout L = make_layout(s);
   const int64_t R = max_rows(s);
   L.size[MOE_WS_SCHED] = moe::group_table_ints(moe::fp8_plan(R, s->E)) * 4;
   L.size[MOE_WS_X_PERM] = fp8_rows_bytes(s->T > R ? s->T : R, s->d, scale_type);
   L.size[MOE_WS_H] = fp8_rows_bytes(R, s->F, scale_type);
-  L.size[MOE_WS_DOWN_ACC] = 0;
+  L.size[MOE_WS_DOWN_ACC] = moe::fp8_split(R, s->E, s->d, s->F).bytes;
   int64_t o = 0;
   for (int i = 0; i < MOE_WS_COUNT; ++i) {
     L.off[i] = o;
@@ -658,6 +669,7 @@ int fp8_experts(const moe_shape* s, int scale_type, const void* x, const int32_t
   a.K = s->F;
   a.y = y_perm;
   a.hq = a.h_scale = nullptr;
+  a.partial = region<void>(ws, L, MOE_WS_DOWN_ACC);
   return hip_status(moe::launch_fp8_gemm(a, st));
 }
 
@@ -667,7 +679,7 @@ extern "C" {
 
 size_t moe_group_workspace_size(const moe_group_shape* g) {
   if (check_group(g) != MOE_OK) return 0;
-  return (size_t)group_table_bytes(g->rows, g->E, elt_bytes(g->dtype));
+  return (size_t)group_workspace(g);
 }
 
 int moe_quantize(int64_t rows, int64_t K, int64_t block_rows, int dtype, int scale_type,
@@ -717,6 +729,7 @@ int moe_grouped_gemm_fp8(const moe_group_shape* g, const void* xq, const void* x
   a.offsets = expert_offsets;
   a.table = table;
   a.y = y;
+  a.partial = group_partial(g, ws);
   return hip_status(moe::launch_fp8_gemm(a, st));
 }
 
@@ -731,8 +744,8 @@ int moe_grouped_dgrad(const moe_group_shape* g, const void* dy, const int32_t* e
   if ((rc = group_table(g, moe::dgrad_plan(g->rows, g->E, elt_bytes(g->dtype)), expert_offsets, ws, &table, st)) !=
       MOE_OK)
     return rc;
-  return hip_status(moe::launch_dgrad(g->dtype, dy, expert_offsets, table, w, dx, g->rows, g->E,
-                                      g->N, g->K, st));
+  return hip_status(moe::launch_dgrad(g->dtype, dy, expert_offsets, table, w, dx,
+                                      group_partial(g, ws), g->rows, g->E, g->N, g->K, st));
 }
 
 int moe_grouped_wgrad(const moe_group_shape* g, const void* dy, const void* x,

@@ -208,7 +208,8 @@ def test_fp8_workspace_layout(T, d, E, k, F, C, flags, kind):
     # the quantized token rows, or packed rows, whichever are more, and the hidden rows
     assert room["x_perm"] >= rows(max(T, R), d) and room["h"] >= rows(R, F)
     assert room["y_perm"] >= R * d * 2 and room["src_token"] >= 4 * R
-    assert room["down_acc"] == 0
+    # partial sums of at most 256 pieces of 256 x 256 outputs
+    assert room["down_acc"] <= 256 * 256 * 256 * 4
     # the table: the count, then (expert, first row) of each row tile
     assert room["sched"] >= 4 * (1 + 2 * tiles(R, E))
 

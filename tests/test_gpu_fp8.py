@@ -163,6 +163,9 @@ def _check_product(c, y, skip_rows=()):
     ([129, 255, 256, 257, 0, 511], 640, 384),     # the 256-row tile and its shorter last tiles
     ([513], 128, 4096),
     ([700, 30, 3, 0], 2176, 256),
+    ([65, 100, 0, 90], 384, 4224),         # few, long tiles: reductions in pieces
+    ([300, 128, 129, 1], 640, 4096),
+    ([33] * 3 + [0] * 60 + [50] * 6, 256, 4096),
 ])
 def test_grouped_product(counts, N, K, kind):
     c = _product_case(counts, N, K, kind, seed=sum(counts) + N, slack=3)

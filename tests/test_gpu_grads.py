@@ -60,7 +60,8 @@ def _within(got, a, b, half):
 CASES = [
     ([1], 128, 128), ([0, 1, 0], 128, 256), ([2, 0, 31, 32, 33], 384, 128),
     ([63, 64, 65, 0], 128, 384), ([127, 128, 129], 256, 256), ([300, 5, 0, 257], 384, 640),
-    ([700], 640, 384), ([1, 2, 3, 0, 0, 0, 4, 190], 256, 1152)]
+    ([700], 640, 384), ([1, 2, 3, 0, 0, 0, 4, 190], 256, 1152),
+    ([300, 0, 129, 5], 2176, 384), ([20, 31, 1] + [0] * 62 + [40], 2048, 128)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
