@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(512) split_kernel(const Fp8Kern a) {
   __shared__ f32x4 part[kSplitWaves * (kSplitRows / 16) * NT * kWave];
   TileWork w;
   if (!tile_work(RowTiles(a.offsets, a.table, a.E, a.R, kSplitRows), a.n_tiles, a.group_n, 1,
-                 &w))
+                 blockIdx.x >> 3, &w))
     return;
   const RowTile rt = w.rt;
   const int nt = w.nt;
@@ -227,7 +227,9 @@ struct Fp8Tile {
   static constexpr int kABytes = BM * 128, kBBytes = 256 * 128;
   static constexpr int kScaleWords = 2 * BM + 2;
   static constexpr int kRing = kStages * (kABytes + kBBytes);
-  static constexpr int kLds = kRing + 2 * ((kScaleWords * 4 + 255) / 256 * 256);
+  static constexpr int kScaleBytes = (kScaleWords * 4 + 255) / 256 * 256;
+  // rings, two buffers of scales, the rows' offsets
+  static constexpr int kLds = kRing + 2 * kScaleBytes + BM * 4;
   static_assert(kLds <= 160 * 1024, "LDS of one CU");
 };
 
@@ -235,203 +237,28 @@ typedef __attribute__((address_space(3))) uint32_t lds_u32;
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
 
+// A block fills its CU's LDS and works through its share of the tiles.  While the outputs of one
+// tile leave through the activations' part of the LDS, the first weight stages of the next
+// arrive in theirs.
 template <int BM, bool SWIGLU, bool E8M0>
 __device__ __attribute__((always_inline)) inline void fp8_body(
-    const Fp8Kern& a, const TileWork& w, f32x4* __restrict__ slot, lds_char* __restrict__ a0,
-    lds_char* __restrict__ a1, lds_char* __restrict__ a2, lds_char* __restrict__ b0,
-    lds_char* __restrict__ b1, lds_char* __restrict__ b2, lds_u32* __restrict__ s0,
-    lds_u32* __restrict__ s1) {
+    const Fp8Kern& a, lds_char* __restrict__ a0, lds_char* __restrict__ a1,
+    lds_char* __restrict__ a2, lds_char* __restrict__ b0, lds_char* __restrict__ b1,
+    lds_char* __restrict__ b2, lds_u32* __restrict__ s0, lds_u32* __restrict__ s1,
+    lds_u32* __restrict__ row_offset) {
   using P = Fp8Tile<BM>;
   constexpr int S = P::kStages, MT = BM / 32, NT = 4;
   constexpr int BN = SWIGLU ? 128 : 256;
-  const int tid = threadIdx.x, lane = lane_id();
-  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int wm = wave >> 2, wn = wave & 3;
-  const int c = lane & 15, g = lane >> 4;
-  const int e = w.rt.e, m_begin = w.rt.begin, nt = w.nt;
-  const int rows = w.rt.end - m_begin, KB = a.K / kScaleBlock;
-  // the steps of the reduction this block takes: all of them, or one piece
-  const int k_first = w.piece * KB / w.pieces;
-  const int steps = (w.piece + 1) * KB / w.pieces - k_first;
-  const bool issuer = wave >= 4;
-
-  // Direct loads: one covers eight rows of 128 bytes; issuing wave d fills blocks 4 i + d.  The
-  // rows of blocks i and i + 1 are 32 apart, which leaves the lane's piece the same: one lane
-  // offset and a scalar for each i (weights; those past N, the upper half of a last column tile,
-  // read the lower half again).  Activation rows are gathered or clamped: an offset each.
+  constexpr int nA = BM / 32, nB = 8;  // direct loads per stage and issuing wave
+  constexpr int ES = E8M0 ? 1 : 4;     // bytes of a scale
   // Few rows per expert: each weight line is read by one tile, and the non-temporal hint keeps
   // it from displacing the activation rows (decode experts 1853 -> 1735 us).
-  constexpr int nA = BM / 32, nB = 8;
   constexpr bool kStreamW = BM <= 64;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wm = wave >> 2, wn = wave & 3;
+  const int KB = a.K / kScaleBlock;
+  const bool issuer = wave >= 4, scaler = wave < BM / 64;
   const int dslot = wave & 3;
-  const int64_t w_row0 = (int64_t)e * a.N + nt * BN;
-  const uint64_t base_a = uniform_u64(a.src ? a.xq : a.xq + (int64_t)m_begin * a.K);
-  const uint64_t base_b = uniform_u64(a.b0 + w_row0 * a.K);
-  const uint64_t base_b2 = SWIGLU ? uniform_u64(a.b1 + w_row0 * a.K)
-                                  : base_b + (nt * BN + 128 < a.N ? (uint64_t)128 * a.K : 0);
-  uint32_t va[nA];
-  const int dr = dslot * 8 + lane / 8;
-  const uint32_t piece = ((lane & 7) ^ ((dr >> 1) & 7)) * 16;
-  const uint32_t vb = (uint32_t)dr * (uint32_t)a.K + piece;
-#pragma unroll
-  for (int i = 0; i < nA; ++i) {
-    const int row = min(i * 32 + dr, rows - 1);
-    va[i] = (uint32_t)(a.src ? x_row(a, m_begin + row) : row) * (uint32_t)a.K + piece;
-  }
-  auto dma_a = [&](int kb, lds_char* abuf) {
-    if (!issuer) return;
-    const uint32_t koff = (uint32_t)(k_first + min(kb, steps - 1)) * kScaleBlock;
-#pragma unroll
-    for (int i = 0; i < nA; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_rsrc(base_a),
-                                               abuf + (i * 4 + dslot) * 1024, 16, va[i], koff,
-                                               0, 0);
-  };
-  auto dma_b = [&](int kb, lds_char* bbuf) {
-    if (!issuer) return;
-    const uint32_t koff = (uint32_t)(k_first + min(kb, steps - 1)) * kScaleBlock;
-#pragma unroll
-    for (int i = 0; i < nB; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_rsrc(i < 4 ? base_b : base_b2),
-                                               bbuf + (i * 4 + dslot) * 1024, 16, vb,
-                                               koff + (uint32_t)(i & 3) * 32u * (uint32_t)a.K, 0,
-                                               kStreamW ? 2 : 0);
-  };
-
-  // scales: thread t < BM brings row t's, one step ahead in registers, one in LDS
-  constexpr int ES = E8M0 ? 1 : 4;  // bytes of a scale
-  // the second block of weights: the up matrix, or the next 128 columns (the last column tile
-  // of an odd count repeats its first)
-  const int64_t wsi = ((int64_t)e * (a.N / 128) + nt * (BN / 128)) * KB;
-  const uint64_t base_ws0 = uniform_u64(static_cast<const char*>(a.b0s) + wsi * ES);
-  const uint64_t base_ws1 =
-      SWIGLU ? uniform_u64(static_cast<const char*>(a.b1s) + wsi * ES)
-             : base_ws0 + (nt * BN + 128 < a.N ? (uint64_t)KB * ES : 0);
-  // (rows of a tile, or all gathered rows, lie within 2^31 bytes of scales)
-  const uint64_t base_xs =
-      uniform_u64(static_cast<const char*>(a.xs) + (a.src ? 0 : (int64_t)m_begin * KB * ES));
-  const int s_rel = min(tid, rows - 1);
-  const uint32_t vxs = (uint32_t)(a.src ? x_row(a, m_begin + s_rel) : s_rel) *
-                       (uint32_t)(KB * ES);
-  uint32_t xs = 0, ws0 = 0, ws1 = 0;
-  auto scale_at = [&](uint64_t base, uint32_t voff, int k) -> uint32_t {
-    if constexpr (E8M0)
-      return __builtin_amdgcn_raw_buffer_load_b8(buffer_rsrc(base), voff, k, 0);
-    else
-      return __builtin_amdgcn_raw_buffer_load_b32(buffer_rsrc(base), voff, k * 4, 0);
-  };
-  auto scale_load = [&](int kb) {
-    if (wave >= BM / 64) return;
-    const int k = k_first + min(kb, steps - 1);
-    xs = scale_at(base_xs, vxs, k);
-    ws0 = scale_at(base_ws0, 0, k);
-    ws1 = scale_at(base_ws1, 0, k);
-  };
-  auto scale_put = [&](lds_u32* s) {
-    if (wave >= BM / 64) return;
-    if constexpr (E8M0) {
-      s[tid] = xs;
-      if (tid == 0) {
-        s[BM] = ws0;
-        s[BM + 1] = ws1;
-      }
-    } else {
-      s[tid] = __float_as_uint(__uint_as_float(xs) * __uint_as_float(ws0));
-      s[BM + tid] = __float_as_uint(__uint_as_float(xs) * __uint_as_float(ws1));
-    }
-  };
-
-  f32x4 acc[MT][NT];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-  // 16-row tiles of this wave's band that hold rows
-  const int band_rows = rows - wm * MT * 16;
-  const int live = band_rows <= 0 ? 0 : min(MT, (band_rows + 15) / 16);  // uniform
-  const int swz = (c >> 1) & 7;
-  // a fragment's two pieces: byte offsets of the lane's row, row tiles and column tiles a
-  // constant apart; with SwiGLU a wave's column tiles are two gate tiles and the up tiles of the
-  // same columns
-  const int slot0 = (g ^ swz) * 16, slot1 = ((g + 4) ^ swz) * 16;
-  const int af0 = (wm * MT * 16 + c) * 128 + slot0, af1 = af0 - slot0 + slot1;
-  const int bf0 = (wn * (SWIGLU ? 32 : 64) + c) * 128 + slot0, bf1 = bf0 - slot0 + slot1;
-  auto frag = [&](const lds_char* buf, int o0, int o1, int rows_on) {
-    const u32x4 lo = *reinterpret_cast<const lds_u32x4*>(buf + o0 + rows_on * 128);
-    const u32x4 hi = *reinterpret_cast<const lds_u32x4*>(buf + o1 + rows_on * 128);
-    return join(lo, hi);
-  };
-  auto b_rows_on = [](int j) { return SWIGLU ? (j / 2) * 128 + (j % 2) * 16 : j * 16; };
-  const int s_row = wm * MT * 16 + c;
-  // Multiply one stage.  The row fragments stream through a ring of three, each read two row
-  // tiles ahead of its MFMAs; the reads are spread between the MFMAs.  LIVE: the band's
-  // 16-row tiles that hold rows (compile-time; k_loop picks the copy).  fp32 scales: a row
-  // tile's four products are added to its sums behind the next tile's MFMAs.
-  auto compute = [&](const lds_char* abuf, const lds_char* bbuf, const lds_u32* s, auto live, auto mid) {
-    constexpr int LIVE = decltype(live)::value, RING = 3;
-    if constexpr (LIVE == 0) mid();
-    if constexpr (LIVE > 0) {
-      i32x8 fa[RING], fb[NT];
-      // (fp32 scales outlive their fragment by one row tile)
-      float sa[RING + 1], sb[RING + 1];
-      uint32_t sx[RING];
-      auto ld_a = [&](int i) {
-        fa[i % RING] = frag(abuf, af0, af1, i * 16);
-        if constexpr (E8M0) {
-          sx[i % RING] = s[s_row + i * 16];
-        } else {
-          sa[i % (RING + 1)] = __uint_as_float(s[(SWIGLU ? 0 : (wn >> 1) * BM) + s_row + i * 16]);
-          if constexpr (SWIGLU) sb[i % (RING + 1)] = __uint_as_float(s[BM + s_row + i * 16]);
-        }
-      };
-      uint32_t w0 = 0, w1 = 0;
-      if constexpr (E8M0) {
-        w0 = s[BM + (SWIGLU ? 0 : wn >> 1)];
-        w1 = SWIGLU ? s[BM + 1] : w0;
-      }
-      ld_a(0);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) fb[j] = frag(bbuf, bf0, bf1, b_rows_on(j));
-      if constexpr (LIVE > 1) ld_a(1);
-      mid();
-      constexpr int kAReads = SWIGLU && !E8M0 ? 4 : 3;  // LDS reads of one ld_a
-      f32x4 p[2][NT];
-      unroll_steps<LIVE>([&](auto I) {
-        constexpr int i = decltype(I)::value;
-        if constexpr (i + 2 < LIVE) ld_a(i + 2);
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          if constexpr (E8M0)
-            mma_e8m0(acc[i][j], fb[j], fa[i % RING], j < 2 ? w0 : w1, sx[i % RING]);
-          else
-            p[i & 1][j] = mma_zero(fb[j], fa[i % RING]);
-        }
-        if constexpr (!E8M0 && i > 0) {
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-            add_scaled(acc[i - 1][j], p[(i - 1) & 1][j],
-                       SWIGLU && j >= 2 ? sb[(i - 1) % (RING + 1)]
-                                        : sa[(i - 1) % (RING + 1)]);
-        }
-        // this tile's MFMAs, the reads and the previous tile's additions between them
-        constexpr int R = i + 2 < LIVE ? kAReads : 0;
-        unroll_steps<NT>([&](auto J) {
-          constexpr int j = decltype(J)::value;
-          __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-          if constexpr (R > j) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-          if constexpr (!E8M0 && i > 0) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
-        });
-      });
-      if constexpr (!E8M0) {
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-          add_scaled(acc[LIVE - 1][j], p[(LIVE - 1) & 1][j],
-                     SWIGLU && j >= 2 ? sb[(LIVE - 1) % (RING + 1)]
-                                        : sa[(LIVE - 1) % (RING + 1)]);
-      }
-    }
-  };
 
   auto buf_a = [&](auto I) -> lds_char* {
     constexpr int j = decltype(I)::value % S;
@@ -441,151 +268,386 @@ __device__ __attribute__((always_inline)) inline void fp8_body(
     constexpr int j = decltype(I)::value % S;
     return j == 0 ? b0 : j == 1 ? b1 : b2;
   };
-  // Step k: stage k has landed (own loads waited for, then the barrier), the loads of stage
-  // k + S - 1 go out into the buffer that step k - 1 finished reading, the scales of step k + 1 go
-  // to LDS and those of k + 2 are asked for.
-  scale_load(0);
-  scale_put(s0);
-  scale_load(1);
-  unroll_steps<S>([&](auto I) {
-    dma_b(decltype(I)::value, buf_b(I));
-    if constexpr (decltype(I)::value < S - 1) dma_a(decltype(I)::value, buf_a(I));
-  });
-  constexpr int L = S % 2 == 0 ? S : 2 * S;  // the rings repeat
+
+  const RowTiles row_tiles(a.offsets, a.table, a.E, a.R, BM);
+  TileWork w;
+  int work = blockIdx.x >> 3;
+  if (!tile_work(row_tiles, a.n_tiles, a.group_n, a.s_max, work, &w)) return;
+
+  // Direct loads: one covers eight rows of 128 bytes; issuing wave d fills blocks 4 i + d.  The
+  // rows of blocks i and i + 1 are 32 apart, which leaves the lane's piece the same: one lane
+  // offset and a scalar for each i (weights; those past N, the upper half of a last column tile,
+  // read the lower half again).
+  auto direct_row = [&] { return dslot * 8 + (tile_thread() & (kWave - 1)) / 8; };
+  auto piece_of = [&](int dr) {
+    return (uint32_t)(((tile_thread() & 7) ^ ((dr >> 1) & 7)) * 16);
+  };
+  const int dr0 = direct_row();
+  const uint32_t vb = (uint32_t)dr0 * (uint32_t)a.K + piece_of(dr0);
+  // the weights' side of a tile
+  struct Weights {
+    uint64_t b, b2;
+    int k_first, steps;  // the steps of the reduction it takes: all of them, or one piece
+  };
+  auto weights_of = [&](const TileWork& t) {
+    Weights r;
+    const int64_t row0 = (int64_t)t.rt.e * a.N + t.nt * BN;
+    r.b = uniform_u64(a.b0 + row0 * a.K);
+    r.b2 = SWIGLU ? uniform_u64(a.b1 + row0 * a.K)
+                  : r.b + (t.nt * BN + 128 < a.N ? (uint64_t)128 * a.K : 0);
+    r.k_first = t.piece * KB / t.pieces;
+    r.steps = (t.piece + 1) * KB / t.pieces - r.k_first;
+    return r;
+  };
+  auto dma_b = [&](const Weights& r, int kb, lds_char* bbuf) {
+    if (!issuer) return;
+    const uint32_t koff = (uint32_t)(r.k_first + min(kb, r.steps - 1)) * kScaleBlock;
+#pragma unroll
+    for (int i = 0; i < nB; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_rsrc(i < 4 ? r.b : r.b2),
+                                               bbuf + (i * 4 + dslot) * 1024, 16, vb,
+                                               koff + (uint32_t)(i & 3) * 32u * (uint32_t)a.K, 0,
+                                               kStreamW ? 2 : 0);
+  };
+  // The rows' side.  Gathered rows (gate and up only) have an offset each, kept in LDS (registers
+  // are short), else they lie one behind the other.  Rows past the expert's get offsets past
+  // the resource's end: they load as zeros, from nowhere.  Thread t < BM looks after row t: its
+  // source is asked for (row_source) well before its offset is needed (rows_of).
+  int src = 0;
+  uint32_t vxs = 0;
+  uint64_t base_a = 0, base_xs = 0;
+  auto row_source = [&](const TileWork& t) {
+    if (SWIGLU && a.src && scaler) src = a.src[min(t.rt.begin + tile_thread(), t.rt.end - 1)];
+  };
+  auto rows_of = [&](const TileWork& t) {
+    const bool gather = SWIGLU && a.src;
+    base_a = uniform_u64(gather ? a.xq : a.xq + (int64_t)t.rt.begin * a.K);
+    // (rows of a tile, or all gathered rows, lie within 2^31 bytes of scales)
+    base_xs = uniform_u64(static_cast<const char*>(a.xs) +
+                          (gather ? 0 : (int64_t)t.rt.begin * KB * ES));
+    const int row_t = tile_thread();
+    const int row = gather ? min(max(src, 0), a.x_rows - 1)
+                           : min(row_t, t.rt.end - t.rt.begin - 1);
+    vxs = (uint32_t)row * (uint32_t)(KB * ES);
+    if (SWIGLU && scaler)
+      row_offset[row_t] =
+          row_t < t.rt.end - t.rt.begin ? (uint32_t)row * (uint32_t)a.K : 0x80000000u;
+  };
+
+  Weights wt = weights_of(w);
+  row_source(w);
+  unroll_steps<S>([&](auto I) { dma_b(wt, decltype(I)::value, buf_b(I)); });
+  rows_of(w);
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // the rows' offsets
   if (issuer) __builtin_amdgcn_s_setprio(3);
-  auto step = [&](int k, auto I, auto live) {
-    if (k >= steps) return;
-    constexpr int i = decltype(I)::value;
-    // a wave either issues direct loads or brings scales: the count leaves the direct loads
-    // of the S - 2 later stages in flight
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * (nA + nB) + nB)
-                 : "memory");
-    dma_a(k + S - 1, buf_a(IntC<i + S - 1>{}));
-    scale_put(i % 2 ? s0 : s1);
-    scale_load(k + 2);
-    compute(buf_a(I), buf_b(I), i % 2 ? s1 : s0, live, [&] {
-      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-      dma_b(k + S, buf_b(I));
+
+  for (;;) {
+    const int rows = w.rt.end - w.rt.begin, m_begin = w.rt.begin, nt = w.nt;
+    const int tid = tile_thread(), c = tid & 15, g = (tid >> 4) & 3;
+    auto dma_a = [&](int kb, lds_char* abuf) {
+      if (!issuer) return;
+      const uint32_t koff = (uint32_t)(wt.k_first + min(kb, wt.steps - 1)) * kScaleBlock;
+      uint32_t va[nA];
+      if constexpr (SWIGLU) {
+        const int dr = direct_row();
+        const uint32_t piece = piece_of(dr);
+#pragma unroll
+        for (int i = 0; i < nA; ++i) va[i] = row_offset[i * 32 + dr] + piece;
+      }
+#pragma unroll
+      for (int i = 0; i < nA; ++i)
+        if constexpr (SWIGLU)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(buffer_rsrc(base_a),
+                                                   abuf + (i * 4 + dslot) * 1024, 16, va[i],
+                                                   koff, 0, 0);
+        else
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(
+              bounded_rsrc(base_a, (int64_t)min(rows, BM) * a.K), abuf + (i * 4 + dslot) * 1024,
+              16, vb, koff + (uint32_t)i * 32u * (uint32_t)a.K, 0, 0);
+    };
+    // Scales: thread t < BM brings row t's, one step ahead in registers, one in LDS.  The second
+    // block of weights: the up matrix, or the next 128 columns (the last column tile of an odd
+    // count repeats its first).
+    const int64_t wsi = ((int64_t)w.rt.e * (a.N / 128) + nt * (BN / 128)) * KB;
+    const uint64_t base_ws0 = uniform_u64(static_cast<const char*>(a.b0s) + wsi * ES);
+    const uint64_t base_ws1 = SWIGLU ? uniform_u64(static_cast<const char*>(a.b1s) + wsi * ES)
+                                     : base_ws0 + (nt * BN + 128 < a.N ? (uint64_t)KB * ES : 0);
+    uint32_t xs = 0, ws0 = 0, ws1 = 0;
+    auto scale_at = [&](uint64_t base, uint32_t voff, int k) -> uint32_t {
+      if constexpr (E8M0)
+        return __builtin_amdgcn_raw_buffer_load_b8(buffer_rsrc(base), voff, k, 0);
+      else
+        return __builtin_amdgcn_raw_buffer_load_b32(buffer_rsrc(base), voff, k * 4, 0);
+    };
+    auto scale_load = [&](int kb) {
+      if (!scaler) return;
+      const int k = wt.k_first + min(kb, wt.steps - 1);
+      xs = scale_at(base_xs, vxs, k);
+      ws0 = scale_at(base_ws0, 0, k);
+      ws1 = scale_at(base_ws1, 0, k);
+    };
+    auto scale_put = [&](lds_u32* s) {
+      if (!scaler) return;
+      if constexpr (E8M0) {
+        s[tid] = xs;
+        if (tid == 0) {
+          s[BM] = ws0;
+          s[BM + 1] = ws1;
+        }
+      } else {
+        s[tid] = __float_as_uint(__uint_as_float(xs) * __uint_as_float(ws0));
+        s[BM + tid] = __float_as_uint(__uint_as_float(xs) * __uint_as_float(ws1));
+      }
+    };
+
+    f32x4 acc[MT][NT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    // 16-row tiles of this wave's band that hold rows
+    const int band_rows = rows - wm * MT * 16;
+    const int live = band_rows <= 0 ? 0 : min(MT, (band_rows + 15) / 16);  // uniform
+    const int swz = (c >> 1) & 7;
+    // a fragment's two pieces: byte offsets of the lane's row, row tiles and column tiles a
+    // constant apart; with SwiGLU a wave's column tiles are two gate tiles and the up tiles of
+    // the same columns
+    const int slot0 = (g ^ swz) * 16, slot1 = ((g + 4) ^ swz) * 16;
+    const int af0 = (wm * MT * 16 + c) * 128 + slot0, af1 = af0 - slot0 + slot1;
+    const int bf0 = (wn * (SWIGLU ? 32 : 64) + c) * 128 + slot0, bf1 = bf0 - slot0 + slot1;
+    auto frag = [&](const lds_char* buf, int o0, int o1, int rows_on) {
+      const u32x4 lo = *reinterpret_cast<const lds_u32x4*>(buf + o0 + rows_on * 128);
+      const u32x4 hi = *reinterpret_cast<const lds_u32x4*>(buf + o1 + rows_on * 128);
+      return join(lo, hi);
+    };
+    auto b_rows_on = [](int j) { return SWIGLU ? (j / 2) * 128 + (j % 2) * 16 : j * 16; };
+    const int s_row = wm * MT * 16 + c;
+    // Multiply one stage.  The row fragments stream through a ring of three, each read two row
+    // tiles ahead of its MFMAs; the reads are spread between the MFMAs.  LIVE: the band's
+    // 16-row tiles that hold rows (compile-time; k_loop picks the copy).  fp32 scales: a row
+    // tile's four products are added to its sums behind the next tile's MFMAs.
+    auto compute = [&](const lds_char* abuf, const lds_char* bbuf, const lds_u32* s, auto live, auto mid) {
+      constexpr int LIVE = decltype(live)::value, RING = 3;
+      if constexpr (LIVE == 0) mid();
+      if constexpr (LIVE > 0) {
+        i32x8 fa[RING], fb[NT];
+        uint32_t sx[RING];
+        auto ld_a = [&](int i) {
+          fa[i % RING] = frag(abuf, af0, af1, i * 16);
+          if constexpr (E8M0) sx[i % RING] = s[s_row + i * 16];
+        };
+        // fp32 scales: read at their row tile's MFMAs, used behind the next one's
+        float sa[2], sb[2];
+        auto ld_s = [&](int i) {
+          sa[i & 1] = __uint_as_float(s[(SWIGLU ? 0 : (wn >> 1) * BM) + s_row + i * 16]);
+          sb[i & 1] = SWIGLU ? __uint_as_float(s[BM + s_row + i * 16]) : sa[i & 1];
+        };
+        uint32_t w0 = 0, w1 = 0;
+        if constexpr (E8M0) {
+          w0 = s[BM + (SWIGLU ? 0 : wn >> 1)];
+          w1 = SWIGLU ? s[BM + 1] : w0;
+        }
+        ld_a(0);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) fb[j] = frag(bbuf, bf0, bf1, b_rows_on(j));
+        if constexpr (LIVE > 1) ld_a(1);
+        mid();
+        f32x4 p[2][NT];
+        unroll_steps<LIVE>([&](auto I) {
+          constexpr int i = decltype(I)::value;
+          if constexpr (i + 2 < LIVE) ld_a(i + 2);
+          if constexpr (!E8M0) ld_s(i);
+#pragma unroll
+          for (int j = 0; j < NT; ++j) {
+            if constexpr (E8M0) {
+              mma_e8m0(acc[i][j], fb[j], fa[i % RING], j < 2 ? w0 : w1, sx[i % RING]);
+            } else {
+              p[i & 1][j] = mma_zero(fb[j], fa[i % RING]);
+              if constexpr (i > 0)
+                add_scaled(acc[i - 1][j], p[(i - 1) & 1][j],
+                           j < 2 ? sa[(i - 1) & 1] : sb[(i - 1) & 1]);
+            }
+          }
+          // the reads and the previous tile's additions between this tile's MFMAs (scaled ones
+          // count as vector instructions)
+          constexpr int R = (i + 2 < LIVE ? (E8M0 ? 3 : 2) : 0) + (E8M0 ? 0 : SWIGLU ? 2 : 1);
+          unroll_steps<NT>([&](auto J) {
+            constexpr int j = decltype(J)::value;
+            __builtin_amdgcn_sched_group_barrier(E8M0 ? 0x002 : 0x008, 1, 0);
+            if constexpr (R > j) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            if constexpr (!E8M0 && i > 0) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+          });
+        });
+        if constexpr (!E8M0) {
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            add_scaled(acc[LIVE - 1][j], p[(LIVE - 1) & 1][j], j < 2 ? sa[(LIVE - 1) & 1] : sb[(LIVE - 1) & 1]);
+        }
+      }
+    };
+
+    // Step k: stage k has landed (own loads waited for, then the barrier); the activations' stage
+    // k + S - 1 goes out into the buffer step k - 1 finished with and, once every wave holds this
+    // step's weight fragments, the weights' stage k + S into theirs.  The scales of step k + 1 go
+    // to LDS and those of k + 2 are asked for.
+    //
+    // Loads a wave may leave in flight at the top of step k: those of the S - 2 later stages and one
+    // more of weights; in the first steps, whose weights all went out before the first
+    // activations, the later activations and a weight stage for each step made.
+    auto wait = [&](auto N) {
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(decltype(N)::value)
+                   : "memory");
+    };
+    constexpr int L = S % 2 == 0 ? S : 2 * S;  // the rings repeat
+    auto step = [&](int k, auto I, auto live_c) {
+      if (k >= wt.steps) return;
+      constexpr int i = decltype(I)::value;
+      if (i == 0 && k == 0)
+        wait(IntC<(S - 2) * nA>{});
+      else if (S == 3 && i == 1 && k == 1)
+        wait(IntC<(S - 2) * nA + nB>{});
+      else
+        wait(IntC<(S - 2) * (nA + nB) + nB>{});
+      dma_a(k + S - 1, buf_a(IntC<i + S - 1>{}));
+      scale_put(i % 2 ? s0 : s1);
+      scale_load(k + 2);
+      compute(buf_a(I), buf_b(I), i % 2 ? s1 : s0, live_c, [&] {
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        dma_b(wt, k + S, buf_b(I));
+      });
+    };
+    unroll_steps<S - 1>([&](auto I) { dma_a(decltype(I)::value, buf_a(I)); });
+    scale_load(0);
+    scale_put(s0);
+    scale_load(1);
+    // one copy of the loop per count of live row tiles, so that nothing is tested between MFMAs
+    auto k_loop = [&](auto live_c) {
+      for (int k = 0; k < wt.steps; k += L)
+        unroll_steps<L>([&](auto I) { step(k + decltype(I)::value, I, live_c); });
+    };
+    unroll_steps<MT + 1>([&](auto V) {
+      if (live == decltype(V)::value) k_loop(V);
     });
-  };
-  // one copy of the loop per count of live row tiles, so that nothing is tested between MFMAs
-  auto k_loop = [&](auto live) {
-    for (int k = 0; k < steps; k += L)
-      unroll_steps<L>([&](auto I) { step(k + decltype(I)::value, I, live); });
-  };
-  unroll_steps<MT + 1>([&](auto V) {
-    if (live == decltype(V)::value) k_loop(V);
-  });
-  // drain the loads issued past the last stage before the LDS is used again
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  if constexpr (!SWIGLU) {
-    if (slot) {  // one piece of the reduction: its partial sums
-      store_partial(slot, acc, live);
-      return;
-    }
-  }
-  __syncthreads();
+    // drain the loads issued past the last stage; every wave is done with the rings
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
-  // Epilogue through LDS: a lane holds four consecutive columns of row c of each 16-row tile.
-  // The 16-byte piece p of row r lands in slot p ^ (r & 15).
-  if constexpr (SWIGLU) {
-    constexpr int kRow = 128 * 4;  // fp32
-    static_assert(BM * kRow <= P::kRing, "the tile of h fits the rings");
+    // the next tile's sources and first weights
+    TileWork next;
+    work += gridDim.x >> 3;
+    const bool more = tile_work(row_tiles, a.n_tiles, a.group_n, a.s_max, work, &next);
+    if (more) {
+      wt = weights_of(next);
+      row_source(next);
+      unroll_steps<S>([&](auto I) { dma_b(wt, decltype(I)::value, buf_b(I)); });
+    }
+
+    // Epilogue through the activations' rings, in passes of IP row tiles of both bands: a lane
+    // holds four consecutive columns of row c of each 16-row tile.  Row r of a pass has its
+    // 16-byte piece p in slot p ^ (r & 15).
+    constexpr int kRow = 512;  // 128 fp32 values of h, or 256 bf16 ones of y
+    const int tid_e = tile_thread(), c_e = tid_e & 15, g_e = (tid_e >> 4) & 3;
+    constexpr int IP = std::min(MT, S * P::kABytes / (32 * kRow));
+    static_assert(IP >= 1, "one row tile of both bands fits");
+    if (w.slot >= 0) {  // one piece of the reduction: its partial sums
+      if constexpr (!SWIGLU) store_partial(a.partial + (int64_t)w.slot * (BM * 64), acc, live);
+    } else {
 #pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const int r = (wm * MT + i) * 16 + c;
+      for (int i0 = 0; i0 < MT; i0 += IP) {
+        if (i0) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int p = (wn * 32 + j * 16 + 4 * g) / 4;
-        f32x4 v;
+        for (int ii = 0; ii < IP; ++ii) {
+          if (i0 + ii >= MT) break;
+          const int r = (wm * IP + ii) * 16 + c_e;
+          lds_char* row = a0 + r * kRow;
+          const f32x4(&v)[NT] = acc[i0 + ii];
+          if constexpr (SWIGLU) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = silu_f32(acc[i][j][q]) * acc[i][j + 2][q];
-        *reinterpret_cast<lds_f32x4*>(a0 + r * kRow + ((p ^ (r & 15)) << 4)) = v;
+            for (int j = 0; j < 2; ++j) {
+              f32x4 h;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) h[q] = silu_f32(v[j][q]) * v[j + 2][q];
+              *reinterpret_cast<lds_f32x4*>(row + (((wn * 8 + j * 4 + g_e) ^ (r & 15)) << 4)) = h;
+            }
+          } else {
+            typedef bf16 bf16x4 __attribute__((ext_vector_type(4)));
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              const int b = (wn * 64 + j * 16 + 4 * g_e) * 2;
+              *reinterpret_cast<__attribute__((address_space(3))) bf16x4*>(
+                  row + (((b >> 4) ^ (r & 15)) << 4) + (b & 15)) =
+                  bf16x4{(bf16)v[j][0], (bf16)v[j][1], (bf16)v[j][2], (bf16)v[j][3]};
+            }
+          }
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        // staged row r of the pass is row at(r) of the tile
+        auto at = [&](int r) {
+          return ((r / (IP * 16)) * MT + i0) * 16 + r % (IP * 16);
+        };
+        auto in_tile = [&](int r) {
+          return (i0 + (r / 16) % IP) < MT && at(r) < min(rows, BM);
+        };
+        if constexpr (SWIGLU) {
+          // eight lanes per row, each four pieces of four columns
+          const int sub = tid_e & 7;
+          for (int r = tid_e / 8; r < 32 * IP; r += 64) {
+            if (!in_tile(r)) continue;
+            f32x4 v[4];
+            uint32_t m = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              v[j] = *reinterpret_cast<const lds_f32x4*>(
+                  a0 + r * kRow + (((j * 8 + sub) ^ (r & 15)) << 4));
+#pragma unroll
+              for (int q = 0; q < 4; ++q) m = max(m, abs_bits(v[j][q]));
+            }
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 8));
+            const bool finite = m < kInfBits;
+            const int ex = finite ? scale_exponent(m) : 0;
+            const float k = inv_scale(ex);
+            const int64_t row = m_begin + at(r);
+            uint8_t* dst = a.hq + row * a.N + nt * 128 + sub * 4;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<uint32_t*>(dst + j * 32) =
+                  finite ? pack_e4m3(v[j][0] * k, v[j][1] * k, v[j][2] * k, v[j][3] * k) : kNan4;
+            if (sub == 0)
+              store_scale(a.hs, row * (a.N / 128) + nt, E8M0 ? kScaleE8M0 : kScaleF32, ex,
+                          finite);
+          }
+        } else {
+          for (int q = tid_e; q < 32 * IP * 32; q += 512) {
+            const int r = q / 32, p = q % 32, col = nt * 256 + p * 8;
+            if (!in_tile(r) || col >= a.N) continue;
+            *reinterpret_cast<u32x4*>(a.y + (int64_t)(m_begin + at(r)) * a.N + col) =
+                *reinterpret_cast<const lds_u32x4*>(a0 + r * kRow + ((p ^ (r & 15)) << 4));
+          }
+        }
       }
     }
-    __syncthreads();
-    // eight lanes per row, each four pieces of four columns
-    const int sub = tid & 7;
-    for (int r = tid / 8; r < min(BM, rows); r += 64) {
-      f32x4 v[4];
-      uint32_t m = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        v[j] = *reinterpret_cast<const lds_f32x4*>(a0 + r * kRow +
-                                                   (((j * 8 + sub) ^ (r & 15)) << 4));
-#pragma unroll
-        for (int q = 0; q < 4; ++q) m = max(m, abs_bits(v[j][q]));
-      }
-#pragma unroll
-      for (int o = 1; o < 8; o <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 8));
-      const bool finite = m < kInfBits;
-      const int ex = finite ? scale_exponent(m) : 0;
-      const float k = inv_scale(ex);
-      uint8_t* dst = a.hq + (int64_t)(m_begin + r) * a.N + nt * 128 + sub * 4;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        *reinterpret_cast<uint32_t*>(dst + j * 32) =
-            finite ? pack_e4m3(v[j][0] * k, v[j][1] * k, v[j][2] * k, v[j][3] * k) : kNan4;
-      if (sub == 0)
-        store_scale(a.hs, (int64_t)(m_begin + r) * (a.N / 128) + nt,
-                    E8M0 ? kScaleE8M0 : kScaleF32, ex, finite);
-    }
-  } else {
-    constexpr int kRow = 256 * 2;  // bf16
-    static_assert(BM * kRow <= P::kRing, "the tile of y fits the rings");
-    typedef bf16 bf16x4 __attribute__((ext_vector_type(4)));
-    typedef __attribute__((address_space(3))) bf16x4 lds_bf16x4;
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const int r = (wm * MT + i) * 16 + c;
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int b = (wn * 64 + j * 16 + 4 * g) * 2;
-        *reinterpret_cast<lds_bf16x4*>(a0 + r * kRow + (((b >> 4) ^ (r & 15)) << 4) + (b & 15)) =
-            bf16x4{(bf16)acc[i][j][0], (bf16)acc[i][j][1], (bf16)acc[i][j][2],
-                   (bf16)acc[i][j][3]};
-      }
-    }
-    __syncthreads();
-    for (int q = tid; q < min(BM, rows) * 32; q += 512) {
-      const int r = q / 32, p = q % 32, col = nt * 256 + p * 8;
-      if (col >= a.N) continue;
-      *reinterpret_cast<u32x4*>(a.y + (int64_t)(m_begin + r) * a.N + col) =
-          *reinterpret_cast<const lds_u32x4*>(a0 + r * kRow + ((p ^ (r & 15)) << 4));
-    }
+    if (!more) return;
+    w = next;
+    rows_of(w);
+    // every wave has read the staged rows, and the offsets of the next ones are there
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   }
 }
 
-template <int BM, bool SWIGLU, bool E8M0>
-__device__ inline void fp8_run(const Fp8Kern& a, const TileWork& w, f32x4* slot,
-                               lds_char* base) {
-  using P = Fp8Tile<BM>;
-  constexpr int A = P::kABytes, B = P::kBBytes;
-  lds_char* b = base + P::kStages * A;
-  lds_u32* s = reinterpret_cast<lds_u32*>(base + P::kRing);
-  // a third buffer exists only where the ring has three stages
-  fp8_body<BM, SWIGLU, E8M0>(a, w, slot, base, base + A,
-                             base + (P::kStages > 2 ? 2 * A : 0), b, b + B,
-                             b + (P::kStages > 2 ? 2 * B : 0), s,
-                             s + (P::kScaleWords * 4 + 255) / 256 * 64);
-}
-
-// BM: the tile height of the table; tiles of at most 128 rows run the 128-row tile.
+// BM: the tile height of the table.
 template <int BM, bool SWIGLU, bool E8M0>
 __global__ void __launch_bounds__(512) fp8_kernel(const Fp8Kern a) {
   extern __shared__ __attribute__((aligned(1024))) char smem_dyn[];
-  TileWork w;
-  if (!tile_work(RowTiles(a.offsets, a.table, a.E, a.R, BM), a.n_tiles, a.group_n, a.s_max, &w))
-    return;
+  using P = Fp8Tile<BM>;
+  constexpr int A = P::kABytes, B = P::kBBytes;
   lds_char* base = (lds_char*)smem_dyn;
-  f32x4* slot = w.slot < 0 ? nullptr : a.partial + (int64_t)w.slot * (BM * 64);
-  if constexpr (BM > 128) {
-    if (w.rt.end - w.rt.begin > 128) {
-      fp8_run<BM, SWIGLU, E8M0>(a, w, slot, base);
-      return;
-    }
-  }
-  fp8_run<std::min(BM, 128), SWIGLU, E8M0>(a, w, slot, base);
+  lds_char* b = base + P::kStages * A;
+  lds_u32* s = reinterpret_cast<lds_u32*>(base + P::kRing);
+  // a third buffer exists only where the ring has three stages
+  fp8_body<BM, SWIGLU, E8M0>(a, base, base + A, base + (P::kStages > 2 ? 2 * A : 0), b, b + B,
+                             b + (P::kStages > 2 ? 2 * B : 0), s, s + P::kScaleBytes / 4,
+                             s + P::kScaleBytes / 2);
 }
 
 // ---------------------------------------------------------------------------------------
@@ -637,14 +699,16 @@ static hipError_t run_tiles(Fp8Kern k, int64_t m_max, hipStream_t s) {
   // few rows: the activations are what tiles share, so an expert's column tiles run together
   // (decode experts 1735 -> 1726 us)
   k.group_n = BM <= 64 ? k.n_tiles : std::min(k.n_tiles, 8);
-  constexpr int lds = std::max(Fp8Tile<BM>::kLds, Fp8Tile<std::min(BM, 128)>::kLds);
+  constexpr int lds = Fp8Tile<BM>::kLds;
   hipError_t e = hipFuncSetAttribute((const void*)fp8_kernel<BM, SWIGLU, E8M0>,
                                      hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;
-  fp8_kernel<BM, SWIGLU, E8M0>
-      <<<grid_of(m_max, k.n_tiles) + (k.s_max > 1 ? kSplitCUs : 0), 512, lds, s>>>(k);
+  // one block per CU at most (a multiple of the 8 XCDs)
+  const unsigned grid = std::min<unsigned>(
+      grid_of(m_max, k.n_tiles) + (k.s_max > 1 ? kSplitCUs : 0), kSplitCUs);
+  fp8_kernel<BM, SWIGLU, E8M0><<<grid, 512, lds, s>>>(k);
   if ((e = hipGetLastError()) != hipSuccess || k.s_max < 2) return e;
-  partial_sum_kernel<BM, (BM > 128)><<<dim3(kSplitCUs, 8 * (BM / 32) / 4), 256, 0, s>>>(
+  partial_sum_kernel<BM, false><<<dim3(kSplitCUs, 8 * (BM / 32) / 4), 256, 0, s>>>(
       k.partial, k.offsets, k.table, k.E, k.R, k.n_tiles, k.group_n, k.s_max, k.N, k.y);
   return hipGetLastError();
 }

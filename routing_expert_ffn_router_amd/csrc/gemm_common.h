@@ -37,6 +37,13 @@ __device__ inline __amdgpu_buffer_rsrc_t buffer_rsrc(uint64_t base) {
                                            kFlags);
 }
 
+// A buffer resource over [base, base + bytes): loads past its end give zeros.  (Loads lie within
+// 2^31 bytes of the base, so an end beyond that needs no exact value.)
+__device__ inline __amdgpu_buffer_rsrc_t bounded_rsrc(uint64_t base, int64_t bytes) {
+  const int n = (int)min(max(bytes, (int64_t)0), (int64_t)0x7fffffff);
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), 0, n, 0x00020000);
+}
+
 template <int N>
 using IntC = std::integral_constant<int, N>;
 // f(IntC<0>{}), ..., f(IntC<L-1>{}), with compile-time indices
@@ -70,6 +77,14 @@ __device__ inline void dense_tile(int i, int m_tiles, int n_tiles, int group_n, 
     *mt = rem / gw;
     *nt = full * group_n + rem % gw;
   }
+}
+
+// The thread's index, opaque to the compiler: what a tile derives from it is computed again for each
+// tile, not kept in registers around the loop over tiles.
+__device__ inline int tile_thread() {
+  int t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
 }
 
 // Tiles of rows grouped by expert.  With at most kScanExperts experts a wave finds its row tile
@@ -150,12 +165,12 @@ struct RowTiles {
   }
 };
 
-// Block -> work.  Blocks go round the 8 XCDs in turn; each XCD takes a contiguous share of the
-// tiles there are, so that its tiles keep their rows and weights in one L2, then (s_max > 1) its
-// share of the tail's pieces.  False: nothing for this block.
-__device__ inline bool tile_work(const RowTiles& rows, int n_tiles, int group_n, int s_max,
+// Work j of this block's XCD.  Blocks go round the 8 XCDs in turn; each XCD takes a contiguous
+// share of the tiles there are, so that its tiles keep their rows and weights in one L2, then
+// (s_max > 1) its share of the tail's pieces.  False: no such work, nor any after it.
+__device__ inline bool tile_work(const RowTiles& rows, int n_tiles, int group_n, int s_max, int j,
                                  TileWork* w) {
-  const int xcd = blockIdx.x & 7, j = blockIdx.x >> 3;
+  const int xcd = blockIdx.x & 7;
   TailSplit ts;
   if (s_max > 1) {
     ts = tail_split_of(rows.count, n_tiles, s_max);
@@ -168,13 +183,13 @@ __device__ inline bool tile_work(const RowTiles& rows, int n_tiles, int group_n,
   w->slot = -1;
   w->piece = 0;
   w->pieces = 1;
-  if (j < w8) {
+  if (j < w8 && xcd * w8 + j < ts.whole) {
     tile = xcd * w8 + j;
-    if (tile >= ts.whole) return false;
   } else {
     if (ts.tail == 0) return false;
+    // (with a tail, the whole tiles are a multiple of the CUs: every XCD has w8 of them)
     const int all = ts.tail * ts.pieces, q8 = (all + 7) / 8, q = xcd * q8 + (j - w8);
-    if (j - w8 >= q8 || q >= all) return false;
+    if (j < w8 || j - w8 >= q8 || q >= all) return false;
     w->piece = q / ts.tail;
     w->pieces = ts.pieces;
     const int i = q - w->piece * ts.tail;

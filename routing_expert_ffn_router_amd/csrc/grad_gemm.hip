@@ -57,13 +57,6 @@ __device__ inline int turned_slot(int p, int q) {
   return q ^ (((p >> 2) & 3) << 2);
 }
 
-// A buffer resource over [base, base + bytes): loads past its end give zeros.  (Loads lie within
-// 2^31 bytes of the base, so an end beyond that needs no exact value.)
-__device__ inline __amdgpu_buffer_rsrc_t bounded_rsrc(uint64_t base, int64_t bytes) {
-  const int n = (int)min(max(bytes, (int64_t)0), (int64_t)0x7fffffff);
-  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), 0, n, 0x00020000);
-}
-
 // One tile.  A: a normal operand's first row, of a_rows rows of pitch a_pitch elements (rows past
 // them load as zeros), or a turned operand's first column, of a_rows columns; B: a turned operand's
 // first column, of b_cols.  The reduction runs over [0, P): a normal row's values, a turned
@@ -77,7 +70,7 @@ __device__ __attribute__((always_inline)) inline void grad_body(
     lds_char* __restrict__ a3, lds_char* __restrict__ b0, lds_char* __restrict__ b1,
     lds_char* __restrict__ b2, lds_char* __restrict__ b3) {
   constexpr int E = sizeof(T), MT = G::MT, NT = G::NT, S = G::kStages;
-  const int tid = threadIdx.x, lane = lane_id();
+  const int tid = tile_thread(), lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int wm = wave >> 2, wn = wave & 3;
   const int c = lane & 15, g = lane >> 4;
@@ -337,7 +330,10 @@ __device__ inline void grad_run(const T* A, int64_t a_pitch, int a_rows, const T
                   b + (S > 2 ? 2 * SB : 0), b + (S > 3 ? 3 * SB : 0));
 }
 
-// dgrad: one block per (row tile of an expert, 256 columns of K), or per piece of its reduction.
+// A block fills its CU's LDS and works through its share of the tiles: the next one's loads go out
+// while the stores of the last are under way, where a block for each tile would wait for them.
+//
+// dgrad: a tile is a row tile of an expert by 256 columns of K, or a piece of its reduction.
 template <class T, class G>
 __global__ void __launch_bounds__(512)
 dgrad_kernel(const T* __restrict__ dy, const int32_t* __restrict__ offsets,
@@ -345,37 +341,44 @@ dgrad_kernel(const T* __restrict__ dy, const int32_t* __restrict__ offsets,
              f32x4* __restrict__ partial, int R, int E, int N, int K, int n_tiles, int group_n,
              int s_max) {
   extern __shared__ __attribute__((aligned(1024))) char smem_dyn[];
+  const RowTiles rows(offsets, table, E, R, G::BM);
   TileWork k;
-  if (!tile_work(RowTiles(offsets, table, E, R, G::BM), n_tiles, group_n, s_max, &k)) return;
-  const int col0 = k.nt * G::BN, steps = (N + G::BP - 1) / G::BP;
-  const int p0 = k.piece * steps / k.pieces * G::BP;
-  const int p1 = min((k.piece + 1) * steps / k.pieces * G::BP, N);
-  f32x4* slot = k.slot < 0 ? nullptr : partial + (int64_t)k.slot * (G::BM * G::BN / 4);
-  grad_run<T, G>(dy + (int64_t)k.rt.begin * N + p0, N, min(k.rt.end - k.rt.begin, G::BM),
-                 w + ((int64_t)k.rt.e * N + p0) * K + col0, K,
-                 dx + (int64_t)k.rt.begin * K + col0, slot, K, p1 - p0, min(K - col0, G::BN),
-                 (lds_char*)smem_dyn);
+  for (int j = blockIdx.x >> 3; tile_work(rows, n_tiles, group_n, s_max, j, &k);
+       j += gridDim.x >> 3) {
+    const int col0 = k.nt * G::BN, steps = (N + G::BP - 1) / G::BP;
+    const int p0 = k.piece * steps / k.pieces * G::BP;
+    const int p1 = min((k.piece + 1) * steps / k.pieces * G::BP, N);
+    f32x4* slot = k.slot < 0 ? nullptr : partial + (int64_t)k.slot * (G::BM * G::BN / 4);
+    grad_run<T, G>(dy + (int64_t)k.rt.begin * N + p0, N, min(k.rt.end - k.rt.begin, G::BM),
+                   w + ((int64_t)k.rt.e * N + p0) * K + col0, K,
+                   dx + (int64_t)k.rt.begin * K + col0, slot, K, p1 - p0, min(K - col0, G::BN),
+                   (lds_char*)smem_dyn);
+    // every wave's reads of the LDS are done
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  }
 }
 
-// wgrad: one block per (expert, BM rows of N, BN columns of K).
+// wgrad: a tile is an expert's BM rows of N by BN columns of K.
 template <class T, class G>
 __global__ void __launch_bounds__(512)
 wgrad_kernel(const T* __restrict__ dy, const T* __restrict__ x,
              const int32_t* __restrict__ offsets, T* __restrict__ dw, int R, int E, int N, int K,
              int m_tiles, int n_tiles) {
   extern __shared__ __attribute__((aligned(1024))) char smem_dyn[];
-  const int total = E * m_tiles * n_tiles;
-  const int xcd = blockIdx.x & 7, j = blockIdx.x >> 3, per = (total + 7) / 8;
-  const int t = xcd * per + j;
-  if (j >= per || t >= total) return;
-  const int e = t / (m_tiles * n_tiles), rem = t - e * (m_tiles * n_tiles);
-  const int mt = rem / n_tiles, nt = rem - mt * n_tiles;
-  const int r0 = offsets ? min(max(offsets[e], 0), R) : 0;
-  const int r1 = offsets ? min(max(offsets[e + 1], r0), R) : R;
-  const int row0 = mt * G::BM, col0 = nt * G::BN;
-  grad_run<T, G>(dy + (int64_t)r0 * N + row0, N, min(N - row0, G::BM),
-                 x + (int64_t)r0 * K + col0, K, dw + ((int64_t)e * N + row0) * K + col0, nullptr, K,
-                 r1 - r0, min(K - col0, G::BN), (lds_char*)smem_dyn);
+  const int total = E * m_tiles * n_tiles, per = (total + 7) / 8;
+  const int first = (blockIdx.x & 7) * per, end = min(first + per, total);
+  for (int t = first + (blockIdx.x >> 3); t < end; t += gridDim.x >> 3) {
+    const int e = t / (m_tiles * n_tiles), rem = t - e * (m_tiles * n_tiles);
+    const int mt = rem / n_tiles, nt = rem - mt * n_tiles;
+    const int r0 = offsets ? min(max(offsets[e], 0), R) : 0;
+    const int r1 = offsets ? min(max(offsets[e + 1], r0), R) : R;
+    const int row0 = mt * G::BM, col0 = nt * G::BN;
+    grad_run<T, G>(dy + (int64_t)r0 * N + row0, N, min(N - row0, G::BM),
+                   x + (int64_t)r0 * K + col0, K, dw + ((int64_t)e * N + row0) * K + col0,
+                   nullptr, K, r1 - r0, min(K - col0, G::BN), (lds_char*)smem_dyn);
+    // every wave's reads of the LDS are done
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  }
 }
 
 // ---------------------------------------------------------------------------------------
@@ -394,6 +397,11 @@ int64_t group_max_blocks(int64_t R, int64_t E, int64_t N, int64_t K, int elt) {
   const int64_t rows = (R + E * 63) / 64 * (std::max(N, K) / 128) + 2048 + kSplitCUs;
   const int64_t b = elt == 2 ? 256 : 128;
   return std::max(rows, E * ((N + b - 1) / b) * ((K + b - 1) / b)) + 8;
+}
+
+// One block per CU at most, a multiple of the 8 XCDs.
+static unsigned grid_of(int64_t tiles) {
+  return (unsigned)std::min<int64_t>((tiles + 7) / 8 * 8, kSplitCUs);
 }
 
 template <class K>
@@ -416,8 +424,7 @@ static hipError_t run_dgrad(const T* dy, const int32_t* offsets, const int32_t* 
   if (s_max > 1 && !partial) return hipErrorInvalidValue;
   hipError_t e = allow_lds(dgrad_kernel<T, G>, G::kLds);
   if (e != hipSuccess) return e;
-  const unsigned grid =
-      (unsigned)((m_max * n_tiles + 7) / 8 * 8) + (s_max > 1 ? kSplitCUs : 0);
+  const unsigned grid = grid_of(m_max * n_tiles + (s_max > 1 ? kSplitCUs : 0));
   dgrad_kernel<T, G><<<grid, 512, G::kLds, s>>>(dy, offsets, table, w, dx, (f32x4*)partial,
                                                 (int)R, (int)E, (int)N, (int)K, n_tiles, group_n,
                                                 s_max);
@@ -455,7 +462,7 @@ static hipError_t run_wgrad(const T* dy, const T* x, const int32_t* offsets, T* 
   const int64_t mt = (N + G::BM - 1) / G::BM, nt = (K + G::BN - 1) / G::BN;
   hipError_t e = allow_lds(wgrad_kernel<T, G>, G::kLds);
   if (e != hipSuccess) return e;
-  wgrad_kernel<T, G><<<(unsigned)((E * mt * nt + 7) / 8 * 8), 512, G::kLds, s>>>(
+  wgrad_kernel<T, G><<<grid_of(E * mt * nt), 512, G::kLds, s>>>(
       dy, x, offsets, dw, (int)R, (int)E, (int)N, (int)K, (int)mt, (int)nt);
   return hipGetLastError();
 }
