@@ -427,8 +427,9 @@ __device__ __attribute__((always_inline)) inline void fp8_body(
     // tiles ahead of its MFMAs; the reads are spread between the MFMAs.  LIVE: the band's
     // 16-row tiles that hold rows (compile-time; k_loop picks the copy).  fp32 scales: a row
     // tile's four products are added to its sums behind the next tile's MFMAs.
-    auto compute = [&](const lds_char* abuf, const lds_char* bbuf, const lds_u32* s, auto live, auto mid) {
-      constexpr int LIVE = decltype(live)::value, RING = 3;
+    auto compute = [&](const lds_char* abuf, const lds_char* bbuf, const lds_u32* s,
+                       auto live_c, auto mid) {
+      constexpr int LIVE = decltype(live_c)::value, RING = 3;
       if constexpr (LIVE == 0) mid();
       if constexpr (LIVE > 0) {
         i32x8 fa[RING], fb[NT];
@@ -482,7 +483,8 @@ __device__ __attribute__((always_inline)) inline void fp8_body(
         if constexpr (!E8M0) {
 #pragma unroll
           for (int j = 0; j < NT; ++j)
-            add_scaled(acc[LIVE - 1][j], p[(LIVE - 1) & 1][j], j < 2 ? sa[(LIVE - 1) & 1] : sb[(LIVE - 1) & 1]);
+            add_scaled(acc[LIVE - 1][j], p[(LIVE - 1) & 1][j],
+                       j < 2 ? sa[(LIVE - 1) & 1] : sb[(LIVE - 1) & 1]);
         }
       }
     };
@@ -492,8 +494,8 @@ __device__ __attribute__((always_inline)) inline void fp8_body(
     // step's weight fragments, the weights' stage k + S into theirs.  The scales of step k + 1 go
     // to LDS and those of k + 2 are asked for.
     //
-    // Loads a wave may leave in flight at the top of step k: those of the S - 2 later stages and one
-    // more of weights; in the first steps, whose weights all went out before the first
+    // Loads a wave may leave in flight at the top of step k: those of the S - 2 later stages and
+    // one more of weights; in the first steps, whose weights all went out before the first
     // activations, the later activations and a weight stage for each step made.
     auto wait = [&](auto N) {
       asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(decltype(N)::value)

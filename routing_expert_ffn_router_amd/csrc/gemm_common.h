@@ -79,8 +79,8 @@ __device__ inline void dense_tile(int i, int m_tiles, int n_tiles, int group_n, 
   }
 }
 
-// The thread's index, opaque to the compiler: what a tile derives from it is computed again for each
-// tile, not kept in registers around the loop over tiles.
+// The thread's index, opaque to the compiler: what a tile derives from it is computed again for
+// each tile, not kept in registers around the loop over tiles.
 __device__ inline int tile_thread() {
   int t = threadIdx.x;
   asm volatile("" : "+v"(t));

@@ -12,8 +12,8 @@
 //     buffer -> LDS loads.  wgrad's last stage ends inside the tile: the buffer resource ends
 //     with the expert's last row, and loads past its end write zeros, so the neighbour's rows (or
 //     what lies behind the last expert) add nothing, whatever they hold.
-//   - LDS slots are permuted within a row so that the sixteen or thirty-two rows a wave reads at once
-//     fall into different banks.
+//   - LDS slots are permuted within a row so that the sixteen or thirty-two rows a wave reads at
+//     once fall into different banks.
 //   - Sums are fp32 (fp32 operands: fp32 MFMA), in the order of p, rounded once at the end.
 #include <algorithm>
 

@@ -179,8 +179,8 @@ struct Fp8Args {
 };
 hipError_t launch_fp8_gemm(const Fp8Args& a, hipStream_t s);
 
-// dtype 0 fp32, 1 bf16.  partial: dgrad_split().bytes.  dgrad reads the table of dgrad_plan (or null: group_needs_table); wgrad
-// needs only the offsets.
+// dtype 0 fp32, 1 bf16.  partial: dgrad_split().bytes.  dgrad reads the table of dgrad_plan (or
+// null: group_needs_table); wgrad needs only the offsets.
 hipError_t launch_dgrad(int dtype, const void* dy, const int32_t* offsets,
                         const int32_t* table, const void* w, void* dx, void* partial, int64_t R,
                         int64_t E, int64_t N, int64_t K, hipStream_t s);

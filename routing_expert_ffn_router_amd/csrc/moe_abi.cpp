@@ -712,9 +712,8 @@ int moe_grouped_gemm_fp8(const moe_group_shape* g, const void* xq, const void* x
   if (!y) return MOE_ERR_INVALID_ARG;
   if (!aligned16(y)) return MOE_ERR_ALIGNMENT;
   int32_t* table = nullptr;
-  if ((rc = group_table(g, moe::fp8_plan(g->rows, g->E), expert_offsets, ws, &table, st)) !=
-      MOE_OK)
-    return rc;
+  rc = group_table(g, moe::fp8_plan(g->rows, g->E), expert_offsets, ws, &table, st);
+  if (rc != MOE_OK) return rc;
   moe::Fp8Args a = {};
   a.xq = xq;
   a.x_scale = x_scale;
@@ -741,9 +740,9 @@ int moe_grouped_dgrad(const moe_group_shape* g, const void* dy, const int32_t* e
   if (!dy || !w || !dx) return MOE_ERR_INVALID_ARG;
   if (!aligned16(dy) || !aligned16(w) || !aligned16(dx)) return MOE_ERR_ALIGNMENT;
   int32_t* table = nullptr;
-  if ((rc = group_table(g, moe::dgrad_plan(g->rows, g->E, elt_bytes(g->dtype)), expert_offsets, ws, &table, st)) !=
-      MOE_OK)
-    return rc;
+  rc = group_table(g, moe::dgrad_plan(g->rows, g->E, elt_bytes(g->dtype)), expert_offsets, ws,
+                   &table, st);
+  if (rc != MOE_OK) return rc;
   return hip_status(moe::launch_dgrad(g->dtype, dy, expert_offsets, table, w, dx,
                                       group_partial(g, ws), g->rows, g->E, g->N, g->K, st));
 }
