@@ -217,29 +217,26 @@ __device__ inline void store_partial(f32x4* slot, const f32x4 (&acc)[MT][NT], in
   }
 }
 
-// One wave per (tail tile, wave, row tile i): grid (kSplitCUs, 8 * MT / 4), surplus blocks exit.
-// SHORT: a tile of at most 128 rows was computed by the 128-row tile (4 row tiles per wave).
-template <int BM, bool SHORT>
+// The slots' sum, rounded to bf16: one wave per (tail tile, wave, row tile i), grid (kSplitCUs, 8 *
+// MT / 4), surplus blocks exit.  Bound by HBM and its launch (256 slots of 256 KB in 16-20 us).
+template <int BM>
 __global__ void __launch_bounds__(256)
 partial_sum_kernel(const f32x4* __restrict__ acc, const int32_t* __restrict__ offsets,
                    const int32_t* __restrict__ table, int E, int R, int n_tiles, int group_n,
                    int s_max, int N, bf16* __restrict__ y) {
-  constexpr int NT = 4;
+  constexpr int NT = 4, MT = BM / 32;
   const RowTiles rows(offsets, table, E, R, BM);
   const TailSplit ts = tail_split_of(rows.count, n_tiles, s_max);
   if ((int)blockIdx.x >= ts.tail) return;
   int mt, nt;
   dense_tile(ts.whole + blockIdx.x, rows.count, n_tiles, group_n, &mt, &nt);
   const RowTile rt = rows.at(mt);
-  const int MT = SHORT && rt.end - rt.begin <= 128 ? 4 : BM / 32;
   const int unit = blockIdx.y * 4 + threadIdx.x / kWave;  // wave * MT + i
   const int wave = unit / MT, i = unit - wave * MT;
-  if (wave >= 8) return;
   const int lane = lane_id(), row = ((wave >> 2) * MT + i) * 16 + (lane & 15);
   if (row - (lane & 15) >= min(rt.end - rt.begin, BM)) return;
   const bool stored = row < min(rt.end - rt.begin, BM);
-  // a slot holds 8 waves of BM / 32 row tiles, whichever tile filled it
-  constexpr int kSlot = 8 * (BM / 32) * NT * kWave;
+  constexpr int kSlot = 8 * MT * NT * kWave;
   const f32x4* src = acc + (int64_t)blockIdx.x * ts.pieces * kSlot + unit * NT * kWave + lane;
 #pragma unroll
   for (int j = 0; j < NT; ++j) {

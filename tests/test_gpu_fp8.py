@@ -166,6 +166,10 @@ def _check_product(c, y, skip_rows=()):
     ([65, 100, 0, 90], 384, 4224),         # few, long tiles: reductions in pieces
     ([300, 128, 129, 1], 640, 4096),
     ([33] * 3 + [0] * 60 + [50] * 6, 256, 4096),
+    ([2, 0, 1, 3] * 16, 256, 256),         # as many experts as lanes, and one more
+    ([2, 0, 1, 3] * 16 + [70], 128, 256),
+    ([0] * 1000 + [5] * 24, 128, 128),
+    ([3], 128, 65536),                     # a long reduction
 ])
 def test_grouped_product(counts, N, K, kind):
     c = _product_case(counts, N, K, kind, seed=sum(counts) + N, slack=3)
@@ -431,6 +435,8 @@ LAYERS = {
     "slot major": (mi.Workload("fp8_slot", 300, 128, 4, 2, 256, 1.0, "bf16", 0.5),
                    moe.MOE_FLAG_SLOT_MAJOR),
     "one token": (mi.Workload("fp8_one", 1, 128, 4, 1, 128, None, "bf16"), 0),
+    "grouped": (mi.Workload("fp8_grp", 90, 128, 80, 4, 128, None, "bf16", 0.5),
+                moe.MOE_FLAG_BIAS_SELECTION_ONLY),
     "tall": (mi.Workload("fp8_tall", 1500, 256, 4, 2, 384, 1.25, "bf16"), 0),
 }
 
@@ -439,7 +445,8 @@ LAYERS = {
 @pytest.mark.parametrize("name", list(LAYERS))
 def test_layer_fp8_equals_its_steps(name, kind):
     w, flags = LAYERS[name]
-    s, dev, lay, q = _layer_case(w, flags, kind)
+    groups = (4, 2) if name == "grouped" else (0, 0)
+    s, dev, lay, q = _layer_case(w, flags, kind, *groups)
     out = lay(dev["x"], dev["w_router"], dev["b"], *q).clone()
     want, drops, kept = _composed(s, dev, q, ref.SCALES[kind])
     torch.cuda.synchronize()
@@ -452,6 +459,19 @@ def test_layer_fp8_equals_its_steps(name, kind):
     rel = float((out.float() - ref_out.float()).norm() / ref_out.float().norm())
     log(f"layer_fp8 {name} {kind}: {rel:.3f} of the bf16 layer's norm")
     assert rel < 0.125
+
+
+def test_two_layers_at_once_on_two_streams():
+    cases = [_layer_case(LAYERS[n][0], LAYERS[n][1]) for n in ("decode", "tall")]
+    want = [lay(dev["x"], dev["w_router"], dev["b"], *q).clone() for _, dev, lay, q in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(4):
+        for st, (_, dev, lay, q) in zip(streams, cases):
+            lay(dev["x"], dev["w_router"], dev["b"], *q, stream=st)
+    torch.cuda.synchronize()
+    for (_, _, lay, _), o in zip(cases, want):
+        assert torch.equal(lay.out, o)
 
 
 def test_layer_fp8_of_no_tokens():

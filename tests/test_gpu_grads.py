@@ -61,7 +61,9 @@ CASES = [
     ([1], 128, 128), ([0, 1, 0], 128, 256), ([2, 0, 31, 32, 33], 384, 128),
     ([63, 64, 65, 0], 128, 384), ([127, 128, 129], 256, 256), ([300, 5, 0, 257], 384, 640),
     ([700], 640, 384), ([1, 2, 3, 0, 0, 0, 4, 190], 256, 1152),
-    ([300, 0, 129, 5], 2176, 384), ([20, 31, 1] + [0] * 62 + [40], 2048, 128)]
+    ([300, 0, 129, 5], 2176, 384), ([20, 31, 1] + [0] * 62 + [40], 2048, 128),
+    ([1, 0, 2, 3] * 16, 128, 128), ([0] * 1000 + [2] * 24, 128, 128), ([5], 32768, 128),
+    ([40], 128, 32768)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
