@@ -16,9 +16,10 @@
 //     once fall into different banks.
 //   - Sums are fp32 (fp32 operands: fp32 MFMA), in the order of p, rounded once at the end.
 // Bounds and measurements (bf16): many rows, the matrix units and the LDS reads that feed them
-// (dgrad of 8191 rows, 14336 -> 4096, 8 experts 0.84 ms; wgrad of 32767 rows, 32 experts of 2048 x 7168
-// 1.12 ms, 16 stages a tile, so that its first loads and its stores weigh more); few rows, HBM (86
-// rows, 32 experts of 13824 x 3328: dgrad reads the weights at 6.6 TB/s, wgrad writes them at 5.0).
+// (dgrad of 8191 rows, 14336 -> 4096, 8 experts 0.82 ms; wgrad of 32767 rows, 32 experts of 2048 x
+// 7168 0.95 to 1.04 ms, 16 stages a tile, so that its first loads and its stores weigh more; one
+// dense matrix of 4096 x 14336 and 8192 rows 1420 and 1270 TFLOP/s); few rows, HBM (86 rows, 32
+// experts of 13824 x 3328: dgrad reads the weights at 6.6 TB/s, wgrad writes them at 5.0).
 #include <algorithm>
 
 #include "gemm_common.h"
@@ -193,8 +194,8 @@ __device__ __attribute__((always_inline)) inline void grad_body(
   // 16-row tiles of this wave's band that hold rows
   const int band_rows = a_rows - wm * MT * 16;
   const int live = band_rows <= 0 ? 0 : min(MT, (band_rows + 15) / 16);
-  // Multiply one stage.  B's fragments of both steps are read first; mid() then releases B's buffer
-  // for the stage after next, while A's fragments stream through a ring of three row tiles.
+  // Multiply one stage.  B's fragments of both steps are read first, and mid() releases B's
+  // buffer for the stage after next, while A's stream through a ring of three row tiles.
   auto compute = [&](const lds_char* abuf, const lds_char* bbuf, auto live_c, auto mid) {
     constexpr int LIVE = decltype(live_c)::value, RING = 3;
     if constexpr (LIVE == 0) {
@@ -211,7 +212,6 @@ __device__ __attribute__((always_inline)) inline void grad_body(
 #pragma unroll
         for (int j = 0; j < NT; ++j) fb[ks][j] = turned_frag(bbuf, b_at[j], ks);
       if constexpr (LIVE > 1) ld_a(1);
-      mid();
       unroll_steps<LIVE>([&](auto I) {
         constexpr int i = decltype(I)::value;
         if constexpr (i + 2 < LIVE) ld_a(i + 2);
@@ -219,6 +219,10 @@ __device__ __attribute__((always_inline)) inline void grad_body(
         for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
           for (int j = 0; j < NT; ++j) mma_chunk(acc[i][j], fb[ks][j], fa[i % RING][ks], T());
+        // B's buffer is released behind the fourth row tile: its MFMAs cover the wait (dgrad
+        // and wgrad of many rows, as at the top: 870 and 1050 us released at once, 843 and 1009 behind the second row
+        // tile, 818 and 953 behind the fourth, 855 and 1005 behind the sixth)
+        if constexpr (i == std::min(3, LIVE - 1)) mid();
         if constexpr (E == 2) {  // the next tile's reads between this one's MFMAs
           constexpr int R = i + 2 < LIVE ? (G::kATurned ? 4 : 2) : 0, M = 2 * NT;
           unroll_steps<M>([&](auto MI) {
