@@ -146,7 +146,10 @@ struct RowTiles {
       }
       tiles = (max(row1 - row0, 0) + bm - 1) / bm;
       inc = wave_inclusive_scan(tiles);
-      count = __builtin_amdgcn_readlane(inc, kWave - 1);
+      // at most GroupPlan::m_max, as the table: offsets that decrease would count rows twice, and
+      // the slots of partial sums are laid out for m_max tiles
+      count = min(__builtin_amdgcn_readlane(inc, kWave - 1),
+                  (int)(((uint32_t)R + (uint32_t)(E * (bm - 1))) / (uint32_t)bm));
     }
   }
   __device__ inline RowTile at(int mt) const {

@@ -219,9 +219,9 @@ __device__ __attribute__((always_inline)) inline void grad_body(
         for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
           for (int j = 0; j < NT; ++j) mma_chunk(acc[i][j], fb[ks][j], fa[i % RING][ks], T());
-        // B's buffer is released behind the fourth row tile: its MFMAs cover the wait (dgrad
-        // and wgrad of many rows, as at the top: 870 and 1050 us released at once, 843 and 1009 behind the second row
-        // tile, 818 and 953 behind the fourth, 855 and 1005 behind the sixth)
+        // B's buffer is released behind the fourth row tile: its MFMAs cover the wait (dgrad and
+        // wgrad of many rows, as at the top: 870 and 1050 us released at once, 843 and 1009 behind
+        // the second row tile, 818 and 953 behind the fourth, 855 and 1005 behind the sixth)
         if constexpr (i == std::min(3, LIVE - 1)) mid();
         if constexpr (E == 2) {  // the next tile's reads between this one's MFMAs
           constexpr int R = i + 2 < LIVE ? (G::kATurned ? 4 : 2) : 0, M = 2 * NT;
