@@ -45,7 +45,7 @@ struct Fp8Kern {
   const void* b1s;
   int R, E, N, K;
   const int32_t* offsets;  // nullable: one expert holds all R rows
-  const int32_t* table;    // nullable with few experts (group_tile)
+  const int32_t* table;    // nullable with few experts (RowTiles)
   bf16* y;
   uint8_t* hq;
   void* hs;
@@ -654,6 +654,9 @@ __global__ void __launch_bounds__(512) fp8_kernel(const Fp8Kern a) {
 // ---------------------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------------------
+// Row-tile heights by rows per expert (256 experts of 2048 x 2048, E8M0): 64 against 128 at 31 rows
+// 206 and 210 us, at 48 rows 230 and 218; 128 against 256 at 100 rows 246 and 253 us, at 160 rows
+// 353 and 287.
 GroupPlan fp8_plan(int64_t R, int64_t E) {
   GroupPlan p;
   p.bm = R <= 32 * E ? 64 : R <= 128 * E ? 128 : 256;
@@ -661,20 +664,26 @@ GroupPlan fp8_plan(int64_t R, int64_t E) {
   return p;
 }
 
-GroupSplit group_split(const GroupPlan& p, int64_t columns, int64_t steps) {
+GroupSplit group_split(const GroupPlan& p, int64_t E, int64_t columns, int64_t steps,
+                       int64_t least) {
   GroupSplit g = {1, 0};
   const int64_t n_tiles = (columns + 255) / 256, tiles = p.m_max * n_tiles;
-  // Worth a second launch and the partial sums' way through memory (about 30 us for 256 pieces)
-  // when a tile is long, and when the last partial round is a good part of all rounds.
-  if (steps >= 32 && tiles > 0 && tiles < 8 * kSplitCUs) {
+  // Worth a second launch and the partial sums' way through memory when a tile is long (at least
+  // `least` steps) and the last partial round is a good part of all rounds; a single expert's rows
+  // that fill whole rounds have none (8192 rows, 8192 -> 4096 220 us with the launch, 215
+  // without).
+  if (E == 1 && tiles % kSplitCUs == 0) return g;
+  if (steps >= least && tiles > 0 && tiles < 8 * kSplitCUs) {
     g.s_max = (int)std::min<int64_t>(8, steps / 8);
     g.bytes = std::min<int64_t>(kSplitCUs, tiles * g.s_max) * p.bm * 256 * 4;
   }
   return g;
 }
 
+// (8192 rows, 8 experts, K -> 4096, E8M0, split against whole: K = 4096 169 and 168 us, 6144 254
+// and 267, 7168 266 and 283, 14336 496 and 570; 2048 rows, K = 4096 61 and 57)
 GroupSplit fp8_split(int64_t R, int64_t E, int64_t N, int64_t K) {
-  return group_split(fp8_plan(R, E), N, K / kScaleBlock);
+  return group_split(fp8_plan(R, E), E, N, K / kScaleBlock, 48);
 }
 
 // Bound on the blocks that hold a tile, of m_max x n_tiles, rounded up to the 8 XCDs' shares.
@@ -717,11 +726,17 @@ static hipError_t run_tiles(Fp8Kern k, int64_t m_max, hipStream_t s) {
 template <bool SWIGLU, bool E8M0>
 static hipError_t run_fp8(const Fp8Kern& k, const GroupPlan& p, hipStream_t s) {
   if constexpr (!SWIGLU) {
-    // at most 64 rows per expert on average and fewer 128-column tiles than CUs
+    // Few tiles and at most 64 rows per expert on average; every block reads all its rows, so
+    // more rows need fewer columns (one expert, K = 4096, E8M0, split against tiles: 16 rows N =
+    // 16384 21 and 25 us, N = 28672 37 and 29; 32 rows N = 16384 26 and 27; 64 rows N = 16384
+    // 36 and 27; K = 2048, fp32 scales, 64 rows N = 7168 11.5 and 17.8).
     const int64_t m64 = (k.R + (int64_t)k.E * (kSplitRows - 1)) / kSplitRows;
-    if (!k.table && k.R <= kSplitRows * k.E && m64 * (k.N / 128) < 256)
-      return k.R <= 16 * k.E || m64 * (k.N / 32) < 192 ? run_split<E8M0, 1>(k, m64, s)
-                                                       : run_split<E8M0, 2>(k, m64, s);
+    const int64_t most = k.R > 32 * (int64_t)k.E ? 96 : 192;
+    if (!k.table && k.R <= kSplitRows * (int64_t)k.E && m64 * (k.N / 128) < most)
+      // 16 columns a block while 32 would leave CUs idle (64 rows: N = 4096 16.4 against 18.3 us,
+      // N = 7168 18.2 against 11.5)
+      return m64 * (k.N / 32) < 192 ? run_split<E8M0, 1>(k, m64, s)
+                                    : run_split<E8M0, 2>(k, m64, s);
   }
   if (p.bm == 64) return run_tiles<64, SWIGLU, E8M0>(k, p.m_max, s);
   if (p.bm == 128) return run_tiles<128, SWIGLU, E8M0>(k, p.m_max, s);

@@ -141,19 +141,21 @@ struct GroupPlan {
   int64_t m_max;  // bound on the row tiles over all experts
 };
 GroupPlan fp8_plan(int64_t R, int64_t E);
-GroupPlan dgrad_plan(int64_t R, int64_t E, int elt);
-// The tail split of a product in 256-column tiles whose reduction takes `steps` steps: the most
-// pieces a tail tile is cut into (1: no split), and the bytes of their partial sums.
+GroupPlan dgrad_plan(int64_t R, int64_t E, int elt);  // elt: bytes of a value
+// The tail split of a product in 256-column tiles whose reduction takes `steps` steps, where those
+// are at least `least`: the most pieces a tail tile is cut into (1: no split), and the bytes of
+// their partial sums.
 struct GroupSplit {
   int s_max;
   int64_t bytes;
 };
-GroupSplit group_split(const GroupPlan& p, int64_t columns, int64_t steps);
+GroupSplit group_split(const GroupPlan& p, int64_t E, int64_t columns, int64_t steps,
+                       int64_t least);
 GroupSplit fp8_split(int64_t R, int64_t E, int64_t N, int64_t K);
 GroupSplit dgrad_split(int64_t R, int64_t E, int64_t N, int64_t K, int elt);
 inline int64_t group_table_ints(const GroupPlan& p) { return 1 + 2 * p.m_max; }
 // Whether the grouped launches read a tile table: with few experts the blocks find their tiles
-// from the offsets (group_tile) and take a null table.
+// from the offsets (RowTiles) and take a null table.
 constexpr int kScanExperts = 64;
 inline bool group_needs_table(int64_t E) { return E > kScanExperts; }
 

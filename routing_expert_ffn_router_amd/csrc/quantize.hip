@@ -137,8 +137,10 @@ static hipError_t run_quantize(int64_t rows, int64_t K, int64_t block_rows, int 
     return hipGetLastError();
   }
   const int64_t groups = rows * kblocks;
-  // sixteen groups per block and step
-  if (groups <= 16384)
+  // sixteen groups per block and step: one step where the blocks are few (256 x 7168 bf16 2.5
+  // against 3.4 us, 1024 x 4096 3.4 against 3.8; 2048 x 4096 the same), else four in flight (8192 x
+  // 4096 18.0 against 19.8 us)
+  if (groups <= 32768)
     quantize_rows_kernel<T, 1><<<(unsigned)((groups + 15) / 16), 256, 0, s>>>(
         x, groups, scale_type, q, scale);
   else

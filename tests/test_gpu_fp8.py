@@ -166,6 +166,8 @@ def _check_product(c, y, skip_rows=()):
     ([65, 100, 0, 90], 384, 4224),         # few, long tiles: reductions in pieces
     ([300, 128, 129, 1], 640, 4096),
     ([33] * 3 + [0] * 60 + [50] * 6, 256, 4096),
+    ([65, 100, 0, 90], 384, 6272), ([300, 128, 129, 1], 640, 6272),
+    ([33] * 3 + [0] * 60 + [50] * 6, 256, 6272),
     ([2, 0, 1, 3] * 16, 256, 256),         # as many experts as lanes, and one more
     ([2, 0, 1, 3] * 16 + [70], 128, 256),
     ([0] * 1000 + [5] * 24, 128, 128),

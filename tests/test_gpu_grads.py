@@ -62,8 +62,9 @@ CASES = [
     ([63, 64, 65, 0], 128, 384), ([127, 128, 129], 256, 256), ([300, 5, 0, 257], 384, 640),
     ([700], 640, 384), ([1, 2, 3, 0, 0, 0, 4, 190], 256, 1152),
     ([300, 0, 129, 5], 2176, 384), ([20, 31, 1] + [0] * 62 + [40], 2048, 128),
-    ([1, 0, 2, 3] * 16, 128, 128), ([0] * 1000 + [2] * 24, 128, 128), ([5], 32768, 128),
-    ([40], 128, 32768)]
+    ([1, 0, 2, 3] * 16, 128, 128), ([2, 0, 7, 1], 6272, 384), ([300, 0, 129, 5], 6272, 384),
+    ([20, 31, 1] + [0] * 62 + [40], 6272, 128), ([0] * 1000 + [2] * 24, 128, 128),
+    ([5], 32768, 128), ([40], 128, 32768)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
@@ -253,7 +254,7 @@ def test_offsets_that_decrease_stay_within_the_buffers():
     # two experts that claim all rows: more row tiles than the workspace's slots are laid out for.
     # What such rows get is not defined, but nothing past dx and the workspace is written, the
     # weights' gradients follow the clamped ranges, and a good call after it is right.
-    c = _case([1024] * 4, 2048, 256, "bf16", 41)
+    c = _case([1024] * 4, 8192, 256, "bf16", 41)
     bad = torch.tensor([0, 4096, 0, 4096, 0], dtype=torch.int32)
     gs = moe.group_shape(c["R"], c["E"], c["N"], c["K"], moe.MOE_BF16)
     size = moe.group_workspace_size(gs)
