@@ -732,7 +732,7 @@ static hipError_t run_fp8(const Fp8Kern& k, const GroupPlan& p, hipStream_t s) {
     // 36 and 27; K = 2048, fp32 scales, 64 rows N = 7168 11.5 and 17.8).
     const int64_t m64 = (k.R + (int64_t)k.E * (kSplitRows - 1)) / kSplitRows;
     const int64_t most = k.R > 32 * (int64_t)k.E ? 96 : 192;
-    if (!k.table && k.R <= kSplitRows * (int64_t)k.E && m64 * (k.N / 128) < most)
+    if (!group_needs_table(k.E) && k.R <= kSplitRows * (int64_t)k.E && m64 * (k.N / 128) < most)
       // 16 columns a block while 32 would leave CUs idle (64 rows: N = 4096 16.4 against 18.3 us,
       // N = 7168 18.2 against 11.5)
       return m64 * (k.N / 32) < 192 ? run_split<E8M0, 1>(k, m64, s)
@@ -760,7 +760,7 @@ hipError_t launch_fp8_gemm(const Fp8Args& a, hipStream_t s) {
   k.N = (int)a.N;
   k.K = (int)a.K;
   k.offsets = a.offsets;
-  k.table = a.table;
+  k.table = group_needs_table(a.E) ? a.table : nullptr;
   k.y = (bf16*)a.y;
   k.hq = (uint8_t*)a.hq;
   k.hs = a.h_scale;

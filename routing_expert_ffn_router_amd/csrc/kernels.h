@@ -155,7 +155,8 @@ GroupSplit fp8_split(int64_t R, int64_t E, int64_t N, int64_t K);
 GroupSplit dgrad_split(int64_t R, int64_t E, int64_t N, int64_t K, int elt);
 inline int64_t group_table_ints(const GroupPlan& p) { return 1 + 2 * p.m_max; }
 // Whether the grouped launches read a tile table: with few experts the blocks find their tiles
-// from the offsets (RowTiles) and take a null table.
+// from the offsets (RowTiles) and any table is passed over.  Every caller goes by this, so that
+// one shape runs the same kernels and adds in the same order from all of them.
 constexpr int kScanExperts = 64;
 inline bool group_needs_table(int64_t E) { return E > kScanExperts; }
 

@@ -619,7 +619,7 @@ int check_fp8_weights(const moe_fp8_tensor* w_gate, const moe_fp8_tensor* w_up,
 }
 
 // The expert launches over checked arguments: x quantized, gate/up, down.  With table_ready the
-// workspace holds the tile table of these offsets.
+// workspace holds the tile table of these offsets, where the launches read one.
 int fp8_experts(const moe_shape* s, int scale_type, const void* x, const int32_t* src_token,
                 const int32_t* offsets, const moe_fp8_tensor* w_gate,
                 const moe_fp8_tensor* w_up, const moe_fp8_tensor* w_down, void* ws,
@@ -628,9 +628,8 @@ int fp8_experts(const moe_shape* s, int scale_type, const void* x, const int32_t
   const int64_t cap = s->T > R ? s->T : R;  // rows the x region is laid out for
   char* xq = region<char>(ws, L, MOE_WS_X_PERM);
   char* hq = region<char>(ws, L, MOE_WS_H);
-  int32_t* table = moe::group_needs_table(s->E) || table_ready
-                       ? region<int32_t>(ws, L, MOE_WS_SCHED)
-                       : nullptr;
+  int32_t* table =
+      moe::group_needs_table(s->E) ? region<int32_t>(ws, L, MOE_WS_SCHED) : nullptr;
   hipError_t e = moe::launch_quantize(x_rows, s->d, 1, s->dtype, scale_type, x, xq,
                                       xq + align_up(cap * s->d), st);
   if (e != hipSuccess) return MOE_ERR_HIP;
@@ -818,12 +817,14 @@ int moe_layer_fp8(const moe_shape* s, int scale_type, const void* x, const void*
   void* y_perm = region<void>(ws, L, MOE_WS_Y_PERM);
   rc = route_impl(s, x, w_router, b_router, logits, 0, idx, gates, stt, st);
   if (rc != MOE_OK) return rc;
-  // tables only, the experts' tile table among them: the gate/up product gathers the rows
+  // tables only, the experts' tile table among them where the products read one: the gate/up
+  // product gathers the rows
   const moe::GroupPlan p = moe::fp8_plan(max_rows(s), s->E);
+  int32_t* table =
+      moe::group_needs_table(s->E) ? region<int32_t>(ws, L, MOE_WS_SCHED) : nullptr;
   rc = dispatch_launch(s, idx, nullptr, region<int32_t>(ws, L, MOE_WS_TILE_HIST),
                        region<int32_t>(ws, L, MOE_WS_TILE_BASE), routed, kept, offsets, src,
-                       nullptr, dest, dr, nullptr, st, region<int32_t>(ws, L, MOE_WS_SCHED), p.bm,
-                       p.m_max);
+                       nullptr, dest, dr, nullptr, st, table, p.bm, p.m_max);
   if (rc != MOE_OK || s->T == 0) return rc;
   rc = fp8_experts(s, scale_type, x, src, offsets, w_gate, w_up, w_down, ws, L, y_perm, st,
                    /*table_ready=*/true);

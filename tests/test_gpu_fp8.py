@@ -463,6 +463,28 @@ def test_layer_fp8_equals_its_steps(name, kind):
     assert rel < 0.125
 
 
+@pytest.mark.parametrize("kind", ["f32", "e8m0"])
+@pytest.mark.parametrize("E,T,k,d,F", [(4, 64, 2, 4096, 2048), (8, 100, 2, 2048, 2304),
+                                       (1, 37, 1, 7168, 4096), (64, 20, 2, 256, 2048),
+                                       (65, 20, 2, 256, 2048)])
+def test_layer_fp8_adds_in_its_steps_order(E, T, k, d, F, kind):
+    # few tokens and reductions of 16 to 32 steps, which the down product spreads over the waves
+    # of a block: the layer and its steps have to choose the same kernel.  Block scales far apart
+    # (and no powers of two, where the type has others) make sums that fp32 has to round, so that
+    # another order shows, in a few of the many values.
+    w = mi.Workload(f"fp8_few{E}", T, d, E, k, F, None, "bf16")
+    s, dev, lay, q = _layer_case(w, 0, kind)
+    g = torch.Generator().manual_seed(E)
+    if kind == "f32":
+        q[2][1].mul_(torch.exp(torch.randn(q[2][1].shape, generator=g)).cuda())
+    else:
+        q[2][1].add_(torch.randint(-6, 7, q[2][1].shape, generator=g).to(torch.int8).cuda())
+    out = lay(dev["x"], dev["w_router"], dev["b"], *q).clone()
+    want, _, _ = _composed(s, dev, q, ref.SCALES[kind])
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
 def test_two_layers_at_once_on_two_streams():
     cases = [_layer_case(LAYERS[n][0], LAYERS[n][1]) for n in ("decode", "tall")]
     want = [lay(dev["x"], dev["w_router"], dev["b"], *q).clone() for _, dev, lay, q in cases]
