@@ -424,7 +424,11 @@ int moe_layer(const moe_shape* shape, const void* x, const void* w_router,
  * scale for each block of 128: an activation row [K] has K / 128 scales, a weight matrix
  * [N, K] has [N / 128, K / 128] of them, one for each 128 x 128 block.  A value stands for
  * e4m3 * scale.  Scales are contiguous row-major arrays of one of two types:
- *   MOE_SCALE_F32   float: any finite value (block scales as checkpoints store them)
+ *   MOE_SCALE_F32   float: any finite value (block scales as checkpoints store them).  A
+ *                   product of two scales past fp32's largest number is carried all the same
+ *                   (such tiles take two to two and a half times as long); one below 2^-126
+ *                   may be rounded to a multiple of 2^-149, which changes a block's part of a
+ *                   sum by at most 2^-125
  *   MOE_SCALE_E8M0  one byte v, standing for 2^(v - 127); 255 stands for NaN.  The matrix
  *                   instruction multiplies these itself.
  * [EP-checks] "Memory must be counted by phase": expert weights are the largest line of the

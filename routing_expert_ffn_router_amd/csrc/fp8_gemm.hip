@@ -8,7 +8,13 @@
 //   - E8M0 scales are operands of that instruction: a lane gives the exponent byte of its row
 //     (the same for the four lanes that hold the row's 128 values).
 //   - fp32 scales: the instruction starts from zero and acc += product * (xs * ws) follows in
-//     fp32.
+//     fp32.  Where an xs * ws is past fp32's largest number (2^100 and 2^30), though the block's
+//     dot product may be 0 or small, a tile is computed again with the exponents given to the
+//     instruction, which adds them in a wider range, and only what is left of each scale, 1 <= m
+//     < 4, multiplied in fp32 (a product where every tile is: 530 -> 1243 us, 638 -> 1297; that
+//     form alone in place of the usual one costs 8 to 17 % of every product).  The few-tiles form
+//     below always takes it: its loads hide the difference (16 rows, K = 4096, N = 16384 21.1 and
+//     21.3 us).
 // The order of the 128 values within a step is free (both operands use one order and the scale is
 // the same for all), so a lane takes the 16-byte pieces g and g + 4 of its row's 128 bytes (g
 // = lane / 16).  The weight fragment goes first: a lane then holds one row's four consecutive
@@ -67,6 +73,20 @@ __device__ inline void mma_e8m0(f32x4& acc, const i32x8& w, const i32x8& x, uint
 __device__ inline f32x4 mma_zero(const i32x8& w, const i32x8& x) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0,
                                                           0, 0, 0, 0);
+}
+__device__ inline f32x4 mma_zero(const i32x8& w, const i32x8& x, uint32_t sw, uint32_t sx) {
+  f32x4 p = f32x4{0.f, 0.f, 0.f, 0.f};
+  mma_e8m0(p, w, x, sw, sx);
+  return p;
+}
+// An fp32 scale as 2^(e - 127) * m: its exponent byte e, kept within 1 and 253 so that 2^(127 - e)
+// is a normal number, and m, which is exact: 1 <= |m| < 4, less for a subnormal scale (an infinity
+// or a NaN stays one).
+__device__ inline uint32_t scale_byte(uint32_t bits) {
+  return min(max((bits >> 23) & 255u, 1u), 253u);
+}
+__device__ inline float scale_rest(uint32_t bits) {
+  return __uint_as_float(bits) * __uint_as_float((254u - scale_byte(bits)) << 23);
 }
 __device__ inline void add_scaled(f32x4& acc, const f32x4& p, float s) {
 #pragma unroll
@@ -150,8 +170,8 @@ __device__ inline void split_body(const Fp8Kern& a, const RowTile& rt, int rows,
         if constexpr (E8M0)
           mma_e8m0(acc[i][j], w, x, s.ws, s.xs[i]);
         else
-          add_scaled(acc[i][j], mma_zero(w, x),
-                     __uint_as_float(s.ws) * __uint_as_float(s.xs[i]));
+          add_scaled(acc[i][j], mma_zero(w, x, scale_byte(s.ws), scale_byte(s.xs[i])),
+                     scale_rest(s.ws) * scale_rest(s.xs[i]));
       }
     }
   };
@@ -224,8 +244,8 @@ struct Fp8Tile {
   static constexpr int kScaleWords = 2 * BM + 2;
   static constexpr int kRing = kStages * (kABytes + kBBytes);
   static constexpr int kScaleBytes = (kScaleWords * 4 + 255) / 256 * 256;
-  // rings, two buffers of scales, the rows' offsets
-  static constexpr int kLds = kRing + 2 * kScaleBytes + BM * 4;
+  // rings, two buffers of scales, the rows' offsets, the word that asks for exact scales
+  static constexpr int kLds = kRing + 2 * kScaleBytes + BM * 4 + 16;
   static_assert(kLds <= 160 * 1024, "LDS of one CU");
 };
 
@@ -241,7 +261,7 @@ __device__ __attribute__((always_inline)) inline void fp8_body(
     const Fp8Kern& a, lds_char* __restrict__ a0, lds_char* __restrict__ a1,
     lds_char* __restrict__ a2, lds_char* __restrict__ b0, lds_char* __restrict__ b1,
     lds_char* __restrict__ b2, lds_u32* __restrict__ s0, lds_u32* __restrict__ s1,
-    lds_u32* __restrict__ row_offset) {
+    lds_u32* __restrict__ row_offset, lds_u32* __restrict__ exact_word) {
   using P = Fp8Tile<BM>;
   constexpr int S = P::kStages, MT = BM / 32, NT = 4;
   constexpr int BN = SWIGLU ? 128 : 256;
@@ -334,10 +354,16 @@ __device__ __attribute__((always_inline)) inline void fp8_body(
   row_source(w);
   unroll_steps<S>([&](auto I) { dma_b(wt, decltype(I)::value, buf_b(I)); });
   rows_of(w);
+  if (!E8M0 && tile_thread() == 0) *exact_word = 0;
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");  // the rows' offsets
   if (issuer) __builtin_amdgcn_s_setprio(3);
 
   for (;;) {
+    // (what the last round left, in scalar registers again)
+    base_a = uniform_u64(base_a);
+    base_xs = uniform_u64(base_xs);
+    wt.b = uniform_u64(wt.b);
+    wt.b2 = uniform_u64(wt.b2);
     const int rows = w.rt.end - w.rt.begin, m_begin = w.rt.begin, nt = w.nt;
     const int tid = tile_thread(), c = tid & 15, g = (tid >> 4) & 3;
     auto dma_a = [&](int kb, lds_char* abuf) {
@@ -369,6 +395,7 @@ __device__ __attribute__((always_inline)) inline void fp8_body(
     const uint64_t base_ws1 = SWIGLU ? uniform_u64(static_cast<const char*>(a.b1s) + wsi * ES)
                                      : base_ws0 + (nt * BN + 128 < a.N ? (uint64_t)KB * ES : 0);
     uint32_t xs = 0, ws0 = 0, ws1 = 0;
+    float largest = 0.0f;  // of the products of scales
     auto scale_at = [&](uint64_t base, uint32_t voff, int k) -> uint32_t {
       if constexpr (E8M0)
         return __builtin_amdgcn_raw_buffer_load_b8(buffer_rsrc(base), voff, k, 0);
@@ -391,8 +418,11 @@ __device__ __attribute__((always_inline)) inline void fp8_body(
           s[BM + 1] = ws1;
         }
       } else {
-        s[tid] = __float_as_uint(__uint_as_float(xs) * __uint_as_float(ws0));
-        s[BM + tid] = __float_as_uint(__uint_as_float(xs) * __uint_as_float(ws1));
+        const float p0 = __uint_as_float(xs) * __uint_as_float(ws0);
+        const float p1 = __uint_as_float(xs) * __uint_as_float(ws1);
+        s[tid] = __float_as_uint(p0);
+        s[BM + tid] = __float_as_uint(p1);
+        largest = fmaxf(largest, fmaxf(fabsf(p0), fabsf(p1)));
       }
     };
 
@@ -530,8 +560,44 @@ __device__ __attribute__((always_inline)) inline void fp8_body(
     unroll_steps<MT + 1>([&](auto V) {
       if (live == decltype(V)::value) k_loop(V);
     });
+    if (!E8M0 && largest > 0x1.fffffep127f) *exact_word = 1;
     // drain the loads issued past the last stage; every wave is done with the rings
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+    // A product of scales past fp32's largest number: the tile again, a stage at a time, with the
+    // exponents in the instruction.
+    if constexpr (!E8M0) {
+      if (__builtin_expect(__builtin_amdgcn_readfirstlane(*exact_word), 0)) {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < wt.steps; ++k) {
+          dma_b(wt, k, b0);
+          dma_a(k, a0);
+          scale_load(k);
+          if (scaler) s0[tid] = xs;
+          const uint32_t w0 = scale_at(SWIGLU || wn < 2 ? base_ws0 : base_ws1, 0, wt.k_first + k);
+          const uint32_t w1 = SWIGLU ? scale_at(base_ws1, 0, wt.k_first + k) : w0;
+          asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+          i32x8 fb[NT];
+#pragma unroll
+          for (int j = 0; j < NT; ++j) fb[j] = frag(b0, bf0, bf1, b_rows_on(j));
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            const i32x8 fa = frag(a0, af0, af1, i * 16);
+            const uint32_t x = s0[s_row + i * 16];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+              const uint32_t u = j < 2 ? w0 : w1;
+              add_scaled(acc[i][j], mma_zero(fb[j], fa, scale_byte(u), scale_byte(x)),
+                         scale_rest(u) * scale_rest(x));
+            }
+          }
+          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        }
+      }
+    }
 
     // the next tile's sources and first weights
     TileWork next;
@@ -633,6 +699,7 @@ __device__ __attribute__((always_inline)) inline void fp8_body(
     rows_of(w);
     // every wave has read the staged rows, and the offsets of the next ones are there
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (!E8M0 && tile_thread() == 0) *exact_word = 0;  // (read by all, set behind the next loop)
   }
 }
 
@@ -648,7 +715,7 @@ __global__ void __launch_bounds__(512) fp8_kernel(const Fp8Kern a) {
   // a third buffer exists only where the ring has three stages
   fp8_body<BM, SWIGLU, E8M0>(a, base, base + A, base + (P::kStages > 2 ? 2 * A : 0), b, b + B,
                              b + (P::kStages > 2 ? 2 * B : 0), s, s + P::kScaleBytes / 4,
-                             s + P::kScaleBytes / 2);
+                             s + P::kScaleBytes / 2, s + P::kScaleBytes / 2 + BM);
 }
 
 // ---------------------------------------------------------------------------------------

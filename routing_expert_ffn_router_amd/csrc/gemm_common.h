@@ -21,11 +21,13 @@ __device__ inline float silu_f32(float g) {
 typedef __attribute__((address_space(3))) char lds_char;
 
 // A wave-uniform 64-bit address, moved to scalar registers.
-__device__ inline uint64_t uniform_u64(const void* p) {
-  const uint64_t a = reinterpret_cast<uint64_t>(p);
+__device__ inline uint64_t uniform_u64(uint64_t a) {
   const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)a);
   const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(a >> 32));
   return ((uint64_t)hi << 32) | lo;
+}
+__device__ inline uint64_t uniform_u64(const void* p) {
+  return uniform_u64(reinterpret_cast<uint64_t>(p));
 }
 // Raw buffer resource for byte offsets below 2^31 from a uniform base address.  Selecting
 // between bases (scalar) rather than between descriptors keeps the descriptor in scalar

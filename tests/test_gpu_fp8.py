@@ -214,6 +214,62 @@ def test_nan_stays_in_its_row_and_column(rows, kind):
     assert torch.equal(y[~bad], clean[~bad])
 
 
+@pytest.mark.parametrize("counts,N,K", [
+    ([24, 7], 256, 384),                       # the reduction over a block's waves
+    ([20, 32, 9], 16512, 384),                 # tiles of 64, 128 and 256 rows
+    ([70, 90], 384, 640), ([200, 300, 65], 256, 512),
+    ([65, 100, 90], 384, 6272)])               # a reduction in pieces
+def test_fp32_scales_whose_product_is_past_the_range(counts, N, K):
+    c = _product_case(counts, N, K, "f32", seed=N + K)
+    clean = _run_product(c)
+    a, b = counts[0], K // 128
+    # expert 1, its second block of columns and of the reduction: 2^30 for the weights.  Rows of
+    # 2^98 there: zeros, and one value of 2^-9, so that the sums stay below 448 * 2^119; a
+    # negative scale that is no power of two.
+    c["ws"][1, 1, 1] = 2.0 ** 30
+    for row, scale, value in ((a + 1, 2.0 ** 100, 0.0), (a + 2, 2.0 ** 98, 2.0 ** -9),
+                              (a + 3, -1.37 * 2.0 ** 97, -2.0 ** -9)):
+        c["xs"][row, 1] = scale
+        c["xq"][row, 128:256] = 0
+        c["xq"][row, 128 + 17] = value
+    # a row of small values: products below 2^-126 are rounded at 2^-149, times 2^24.7 at most
+    c["xs"][a + 4] = 2.0 ** -120
+    y = _run_product(c)
+    off = c["offsets"].tolist()
+    for e, (r0, r1) in enumerate(zip(off, off[1:])):
+        x = ref.dequantize(c["xq"][r0:r1], c["xs"][r0:r1], 1)
+        w = ref.dequantize(c["wq"][e], c["ws"][e], 128)
+        want, err = ref.product(x, w)
+        err = err + b * 2.0 ** -125
+        tol = HALF_BF16 * (want.abs() + err) + err
+        assert bool(((y[r0:r1].double() - want).abs() <= tol).all()), e
+    # what has other scales is the same bit for bit
+    rows = torch.ones(c["R"], dtype=torch.bool)
+    rows[a:off[2]] = False
+    assert torch.equal(y[rows], clean[rows])
+    rows[a:off[2]] = True
+    rows[a + 1:a + 5] = False
+    assert torch.equal(y[rows][:, :128], clean[rows][:, :128])
+    assert torch.equal(y[rows][:, 256:], clean[rows][:, 256:])
+
+
+@pytest.mark.parametrize("T,E", [(20, 4), (300, 4), (600, 2)])
+def test_experts_rows_of_zeros_under_scales_past_the_range(T, E):
+    # rows whose one value meets weights of zero: the same as rows of zeros, though the scales'
+    # product is 2^130 and more
+    c = _ffn_case(T, E, 1, 256, 256, "f32", seed=T)
+    rows = [3, T - 1]
+    c["x"][rows] = 0
+    for n in ("wg", "wu"):
+        c[n][0][:, :, 5] = 0
+        c[n][1][:, :, 0] = 2.0 ** 40
+    want, _ = _run_ffn(c)
+    c["x"][rows, 5] = 1.5 * 2.0 ** 99
+    got, _ = _run_ffn(c)
+    assert bool(torch.isfinite(want.float()).all())
+    assert torch.equal(got, want)
+
+
 def test_product_of_zero_rows():
     gs = moe.group_shape(0, 4, 128, 128)
     ws = torch.empty(moe.group_workspace_size(gs), dtype=torch.uint8, device="cuda")
