@@ -736,10 +736,19 @@ GroupSplit group_split(const GroupPlan& p, int64_t E, int64_t columns, int64_t s
   GroupSplit g = {1, 0};
   const int64_t n_tiles = (columns + 255) / 256, tiles = p.m_max * n_tiles;
   // Worth a second launch and the partial sums' way through memory when a tile is long (at least
-  // `least` steps) and the last partial round is a good part of all rounds; a single expert's rows
-  // that fill whole rounds have none (8192 rows, 8192 -> 4096 220 us with the launch, 215
-  // without).
-  if (E == 1 && tiles % kSplitCUs == 0) return g;
+  // `least` steps) and the last partial round is a good part of all rounds.  That round is known
+  // for a single expert's rows, and where all tiles are fewer than the CUs.  One expert's last
+  // round that is whole, or too full to cut any tile in two, has nothing to split (8192 rows, 8192
+  // -> 4096 220 us with the launch, 215 without; 2048 rows, 4096 -> 5120, 160 tiles, 59 and 56).
+  const int64_t last = E == 1 || tiles < kSplitCUs ? tiles % kSplitCUs : kSplitCUs;
+  if (E == 1 && (last == 0 || last > kSplitCUs / 2)) return g;
+  // Few tiles in the last round leave most CUs idle through it: split from 32 steps.  Whole against
+  // split, dgrad: 256 rows, 4096 -> 2048 (8 tiles of 64 steps) 77 and 39 us; 1024 rows, 2048 ->
+  // 5120 (80 tiles of 32) 45.4 and 44.5; 4096 rows, 2048 -> 2048 (128 tiles of 32) 46.2 and 53.6;
+  // 4096 rows, 4096 -> 5120 (320 tiles) 173 and 148; 8 experts, 1024 rows, 2048 -> 2048 (at most
+  // 88 tiles) 34.5 and 32.4, 2048 -> 5120 (at most 220) 35.6 and 38.7.  8-bit, one expert, 256
+  // rows, 4096 -> 2048 53 and 35, 1024 rows, 4096 -> 5120 (80 tiles) 55 and 48.
+  if (last <= 3 * kSplitCUs / 8) least = std::min<int64_t>(least, 32);
   if (steps >= least && tiles > 0 && tiles < 8 * kSplitCUs) {
     g.s_max = (int)std::min<int64_t>(8, steps / 8);
     g.bytes = std::min<int64_t>(kSplitCUs, tiles * g.s_max) * p.bm * 256 * 4;

@@ -143,8 +143,8 @@ struct GroupPlan {
 GroupPlan fp8_plan(int64_t R, int64_t E);
 GroupPlan dgrad_plan(int64_t R, int64_t E, int elt);  // elt: bytes of a value
 // The tail split of a product in 256-column tiles whose reduction takes `steps` steps, where those
-// are at least `least`: the most pieces a tail tile is cut into (1: no split), and the bytes of
-// their partial sums.
+// are at least `least` (fewer where the tail leaves most CUs idle): the most pieces a tail tile
+// is cut into (1: no split), and the bytes of their partial sums.
 struct GroupSplit {
   int s_max;
   int64_t bytes;

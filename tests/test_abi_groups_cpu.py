@@ -129,6 +129,22 @@ def test_group_workspace_holds_every_tile_table(rows, E):
     assert need % 256 == 0 and need >= 4 * (1 + 2 * tiles(rows, E))
 
 
+@pytest.mark.parametrize("kw,slots", [
+    # one expert's few tiles leave most CUs idle: pieces from 32 steps of the reduction.  dgrad
+    # takes N in steps of 64, tiles of 256 rows (128 up to 16 rows) by 256 columns of K
+    (dict(rows=256, E=1, N=4096, K=2048), 8 * 8), (dict(rows=1024, E=1, N=2048, K=5120), 80 * 4),
+    (dict(rows=300, E=1, N=1920, K=1024), 0),
+    # whole rounds before a short last one; a last round of more than half the CUs has no pieces
+    (dict(rows=4096, E=1, N=2048, K=5120), 320 * 4), (dict(rows=4096, E=1, N=4096, K=2176), 0),
+    (dict(rows=4096, E=1, N=10240, K=4096), 0),
+    # the 8-bit product takes K in steps of 128, and columns of N
+    (dict(rows=256, E=1, N=1920, K=4096), 8 * 4), (dict(rows=4096, E=1, N=1024, K=5120), 64 * 5),
+])
+def test_few_tiles_have_room_for_pieces(kw, slots):
+    have = moe.group_workspace_size(group(**kw))
+    assert have - min(slots, 256) * 256 * 256 * 4 in range(256, 4096)
+
+
 # -------------------------------------------------------------- experts' network and layer
 def fp8(q=P, scale=P):
     return moe.MoeFp8Tensor(q, scale)

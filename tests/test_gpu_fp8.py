@@ -178,6 +178,16 @@ def test_grouped_product(counts, N, K, kind):
     _check_product(c, _run_product(c))
 
 
+@pytest.mark.parametrize("kind", ["f32", "e8m0"])
+@pytest.mark.parametrize("counts,N,K", [
+    ([256], 1024, 4096), ([80], 2048, 4224), ([1000], 1152, 5120), ([70, 0, 66], 384, 4096),
+    ([200, 1, 300], 640, 4224),
+    ([4200], 5120, 4096)])  # 340 tiles: a whole round, then pieces
+def test_few_tiles_in_pieces(counts, N, K, kind):
+    c = _product_case(counts, N, K, kind, seed=N + K, slack=3)
+    _check_product(c, _run_product(c))
+
+
 def test_grouped_product_many_experts():
     g = torch.Generator().manual_seed(11)
     counts = torch.randint(0, 20, (256,), generator=g).tolist()

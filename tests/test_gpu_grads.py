@@ -80,6 +80,21 @@ def test_dgrad(counts, N, K, dtype):
     assert bool((dx[:off[0]] == SENTINEL).all()) and bool((dx[off[-1]:] == SENTINEL).all())
 
 
+@pytest.mark.parametrize("counts,N,K", [
+    ([256], 4096, 2048), ([9], 2048, 1152), ([257], 2176, 384), ([1000], 2048, 5120),
+    ([60, 0, 9], 2048, 512), ([0, 300, 1, 20], 4224, 640),
+    ([4200], 2048, 5120)])  # 340 tiles: a whole round, then pieces
+def test_dgrad_of_few_tiles_in_pieces(counts, N, K):
+    c = _case(counts, N, K, "bf16", seed=N + K + len(counts), slack=3, first=2)
+    dx = _dgrad(c)
+    off = c["offsets"].tolist()
+    for e, (a, b) in enumerate(zip(off, off[1:])):
+        if b > a:
+            assert _within(dx[a:b].cuda(), c["dy"][a:b].cuda().double(),
+                           c["w"][e].cuda().double(), 2.0 ** -8), e
+    assert bool((dx[:off[0]] == SENTINEL).all()) and bool((dx[off[-1]:] == SENTINEL).all())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("counts,N,K", CASES)
 def test_wgrad(counts, N, K, dtype):
