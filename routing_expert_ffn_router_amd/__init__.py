@@ -558,6 +558,8 @@ def _scale_types(ty: _Types, scale_type: int) -> tuple:
 
 def _fp8_weight(w, name: str, ty: _Types, scale_type: int, E: int, N: int, K: int,
                 gpu: int) -> MoeFp8Tensor:
+    if not isinstance(w, (tuple, list)) or len(w) != 2:
+        raise ValueError(f"{name} is not a pair (e4m3 values, scales)")
     q, scale = w
     return MoeFp8Tensor(_arg(q, name, ty.e4m3, (E, N, K), gpu),
                         _arg(scale, f"{name}'s scale", _scale_types(ty, scale_type),
@@ -569,13 +571,15 @@ def quantize(x, block_rows: int, scale_type: int, q, scale, stream=None) -> None
     block_rows 1 and [..., N / 128, K / 128] for 128, a matrix's scales after another's as its
     rows are; a list [rows / block_rows, K / 128] of them is taken as well."""
     ty, gpu = _begin()
+    if x is None:
+        raise ValueError("x is missing")
     shape = x.shape
     if len(shape) < 2 or block_rows not in (1, 128) or shape[-1] % 128 or shape[-2] % block_rows:
         raise ValueError(f"x of shape {tuple(shape)} has no {block_rows} x 128 blocks")
     K = shape[-1]
     rows = x.numel() // K if K else 0
     want = (*shape[:-2], shape[-2] // block_rows, K // 128)
-    if len(shape) > 2 and scale.dim() == 2:
+    if len(shape) > 2 and scale is not None and scale.dim() == 2:
         want = (rows // block_rows, K // 128)
     _check("moe_quantize", load_library().moe_quantize(
         rows, K, block_rows, ty.acts.get(x.dtype, -1), scale_type,

@@ -249,6 +249,24 @@ def test_binding_refuses_host_tensors_and_wrong_types(monkeypatch):
             call(**kw)
 
 
+def test_binding_names_what_is_missing(monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    x, q = torch.zeros((2, 128, 128)), torch.zeros((2, 128, 128), dtype=torch.uint8)
+    scale = torch.zeros((2, 1, 1))
+    for args in ((None, 1, 0, q, scale), (x, 128, 0, None, scale), (x, 128, 0, q, None)):
+        with pytest.raises(ValueError):
+            moe.quantize(*args)
+    w = (q, scale)
+    s = moe.shape(4, 128, 2, 1, 128)
+    a = torch.zeros((4, 128), dtype=torch.bfloat16)
+    # (the first weight to be looked at is refused, before anything on the host is)
+    for ws in ((None, w, w), ((q,), w, w), (q, w, w), ((None, scale), w, w)):
+        with pytest.raises(ValueError, match="w_gate|w_up|w_down"):
+            moe.expert_ffn_fp8(s, 0, a, None, torch.zeros(3, dtype=torch.int32), *ws, None, a)
+        with pytest.raises(ValueError, match="w_gate|w_up|w_down"):
+            moe.layer_fp8(s, 0, a, a[:2], None, *ws, None, a)
+
+
 # --------------------------------------------------------------- the tests' own plain forms
 def test_plain_quantizer_is_the_least_scale_and_the_nearest_value():
     g = torch.Generator().manual_seed(0)
