@@ -195,6 +195,26 @@ def test_grouped_product_many_experts():
     _check_product(c, _run_product(c))
 
 
+@pytest.mark.parametrize("kind", ["f32", "e8m0"])
+@pytest.mark.parametrize("counts,N,K", [
+    # more than 256 tiles: blocks go on to a second and third tile, of other heights, experts and
+    # columns.  Tiles of 64, 128 and 256 rows, found from the offsets and (65 experts) a table
+    ([20, 64, 0, 9, 1], 25728, 256), ([20, 64, 0, 9, 1], 33024, 384),
+    ([65, 100, 0, 90], 25728, 384), ([1, 128, 70], 33024, 256),
+    ([300, 129, 0, 513], 15488, 384), ([700, 5, 257], 17664, 256),
+    ([3, 17, 0, 1, 64] * 13, 2176, 384), ([60, 0, 70, 128, 1] * 13, 2176, 256),
+    ([300, 1, 0, 257, 129] * 13, 1152, 256),
+    # a round of whole tiles, then a short one in pieces
+    ([4200, 0, 9000], 1152, 6272), ([40, 64] * 8, 4224, 6272), ([40, 20] * 8, 4224, 6272),
+    ([128, 100, 20] * 9, 2688, 6144),
+])
+def test_blocks_that_work_through_several_tiles(counts, N, K, kind):
+    c = _product_case(counts, N, K, kind, seed=sum(counts) + N, slack=3, first=2)
+    y = _run_product(c)
+    on_gpu = {k: v.cuda() if torch.is_tensor(v) else v for k, v in c.items()}  # large in 64 bits
+    _check_product(on_gpu, y.cuda())
+
+
 @pytest.mark.parametrize("rows", [1, 40, 300])
 def test_dense_product_without_offsets(rows):
     c = _product_case([rows], 256, 384, "f32", seed=rows)
@@ -437,6 +457,17 @@ def _check_ffn(c):
     (100, 4, 2, 512, 384), (333, 3, 2, 256, 896), (700, 2, 1, 640, 256), (130, 64, 6, 256, 128)])
 def test_expert_ffn_fp8(T, E, k, d, F, kind):
     _check_ffn(_ffn_case(T, E, k, d, F, kind, seed=T + F))
+
+
+@pytest.mark.parametrize("kind", ["f32", "e8m0"])
+@pytest.mark.parametrize("gathered", [True, False])
+@pytest.mark.parametrize("T,E,k,d,F", [
+    # gate and up in more than 256 tiles of 64, 128 and 256 rows: the next tile's sources and
+    # weights are asked for during the epilogue.  (F / 128 column tiles for each row tile)
+    (40, 4, 2, 128, 11392), (230, 5, 1, 256, 9600), (700, 2, 1, 128, 8576),
+    (330, 66, 2, 128, 640)])
+def test_experts_that_work_through_several_tiles(T, E, k, d, F, kind, gathered):
+    _check_ffn(_ffn_case(T, E, k, d, F, kind, seed=T + F, gathered=gathered))
 
 
 @pytest.mark.parametrize("T", [20, 400])

@@ -95,6 +95,44 @@ def test_dgrad_of_few_tiles_in_pieces(counts, N, K):
     assert bool((dx[:off[0]] == SENTINEL).all()) and bool((dx[off[-1]:] == SENTINEL).all())
 
 
+@pytest.mark.parametrize("dtype,counts,N,K", [
+    # more than 256 tiles: blocks go on to a second and third one (tiles of 256 and, with few
+    # rows, 128 rows; fp32 128), found from the offsets and (65 experts) a table
+    ("bf16", [20, 300, 0, 5], 128, 16768), ("bf16", [300, 129, 70], 384, 16896),
+    ("bf16", [9, 0, 16, 1, 3], 128, 22912), ("bf16", [1, 300, 0, 257, 20] * 13, 256, 1152),
+    ("f32", [20, 300, 0, 5], 128, 8576), ("f32", [130, 1, 70], 384, 11392),
+    ("f32", [1, 130, 0, 17, 20] * 13, 128, 1152),
+    # a round of whole tiles, then a short one in pieces
+    ("bf16", [4200, 0, 9000], 6272, 1152), ("bf16", [1, 12, 3, 16] * 8, 6144, 2432)])
+def test_dgrad_blocks_that_work_through_several_tiles(dtype, counts, N, K):
+    c = _case(counts, N, K, dtype, seed=N + sum(counts), slack=3, first=2)
+    dx = _dgrad(c)
+    off = c["offsets"].tolist()
+    for e, (a, b) in enumerate(zip(off, off[1:])):
+        if b > a:
+            assert _within(dx[a:b].cuda(), c["dy"][a:b].cuda().double(),
+                           c["w"][e].cuda().double(), DTYPES[dtype][2]), e
+    assert bool((dx[:off[0]] == SENTINEL).all()) and bool((dx[off[-1]:] == SENTINEL).all())
+
+
+@pytest.mark.parametrize("dtype,counts,N,K", [
+    # 256 blocks at once (fp32: 512): tiles with rows follow each other, and empty experts between
+    ("bf16", [70, 1, 0, 129], 2176, 2944), ("bf16", [300, 64, 65], 2432, 2688),
+    ("bf16", [33, 0, 200, 7, 64] * 13, 640, 640),
+    ("f32", [70, 1, 0, 129], 1664, 1792), ("f32", [31, 33, 200], 2048, 1920),
+    ("f32", [33, 0, 200, 7, 64] * 13, 384, 384)])
+def test_wgrad_blocks_that_work_through_several_tiles(dtype, counts, N, K):
+    c = _case(counts, N, K, dtype, seed=K + sum(counts), slack=5, first=1)
+    dw = _wgrad(c)
+    off = c["offsets"].tolist()
+    for e, (a, b) in enumerate(zip(off, off[1:])):
+        if b == a:
+            assert bool((dw[e] == 0).all()), e
+        else:
+            assert _within(dw[e].cuda(), c["dy"][a:b].cuda().double().t(),
+                           c["x"][a:b].cuda().double(), DTYPES[dtype][2]), e
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("counts,N,K", CASES)
 def test_wgrad(counts, N, K, dtype):
