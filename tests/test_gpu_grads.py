@@ -208,6 +208,38 @@ def test_gradients_match_differences_of_the_forward_product():
         assert abs(a - b) <= tol, (a, b, tol)
 
 
+def test_gradients_equal_exact_differences_of_the_forward_product():
+    # The loss sum(dy * h W^T) is linear in h and in W, so a difference over any step is its
+    # derivative.  Whole numbers of at most 3 keep every product and sum a whole number below 2^24
+    # (130 rows or 384 columns of at most 9, steps twice that), which fp32 holds exactly: nothing is
+    # rounded on either side, and each row's and each expert's derivative has to be equal.
+    counts, d, F = [30, 0, 130, 28], 256, 384
+    E, R = len(counts), sum(counts)
+    g = torch.Generator().manual_seed(12)
+    whole = lambda *s: torch.randint(-3, 4, s, generator=g).float()  # noqa: E731
+    c = {"dy": whole(R, d), "x": whole(R, F), "w": whole(E, d, F), "offsets": offsets_of(counts),
+         "R": R, "E": E, "N": d, "K": F, "dtype": "f32"}
+    vh, vw = whole(R, F), whole(E, d, F)
+    s = moe.shape(R, d, E, 1, F, 0, moe.MOE_F32)
+    ws = torch.empty(moe.workspace_size(s), dtype=torch.uint8, device="cuda")
+
+    def forward(h, w):
+        y = torch.zeros((R, d), device="cuda")
+        moe.expert_down(s, h.cuda(), c["offsets"].cuda(), w.cuda(), ws, y)
+        return y.cpu().double()
+
+    dx, dw, dy = _dgrad(c).double(), _wgrad(c).double(), c["dy"].double()
+    by_h = (dy * (forward(c["x"] + vh, c["w"]) - forward(c["x"] - vh, c["w"]))).sum(1) / 2
+    by_w = (dy * (forward(c["x"], c["w"] + vw) - forward(c["x"], c["w"] - vw))).sum(1) / 2
+    # (hardly any derivative is zero, so that nothing missing can pass)
+    assert int((by_h != 0).sum()) > 0.9 * R
+    assert torch.equal((dx * vh.double()).sum(1), by_h)
+    off = c["offsets"].tolist()
+    want = torch.stack([by_w[a:b].sum() for a, b in zip(off, off[1:])])
+    assert torch.equal((dw * vw.double()).sum((1, 2)), want)
+    assert int((want != 0).sum()) == 3
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_training_step_of_the_experts_network(dtype):
     """Forward through the framework's grouped products, backward through the gradients, as a
