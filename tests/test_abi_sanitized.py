@@ -109,3 +109,76 @@ def test_host_code_under_address_and_ub_sanitizers():
                        timeout=600)
     assert r.returncode == 0, (r.stdout[-2000:], r.stderr[-4000:])
     assert r.stdout.split()[0] == "ok"
+
+
+CHILD_GROUPS = r"""
+import ctypes, itertools, sys
+sys.path.insert(0, ROOT)
+import routing_expert_ffn_router_amd as moe
+lib = moe.load_library(LIB)
+big = [-(1 << 62), -1, 0, 1, 8, 37, 128, 4096, (1 << 29) + 128, (1 << 31) - 1, 1 << 31, 1 << 40,
+       (1 << 62) + 128]
+wide = [-128, 0, 100, 128, 2048, 6272, 1 << 20, (1 << 20) + 128, 1 << 40, (1 << 62) + 128]
+experts = [-1, 0, 1, 8, 64, 65, 1024, 1025, 1 << 40]
+types = [(0, 0), (1, 1), (1, 0), (2, 0), (1, 2), (-1, -1)]
+# never dereferenced: every call below is refused, its workspace, an operand or the shape missing
+P, W, BIG = 1 << 40, 1 << 40, (1 << 64) - 1
+n = 0
+for rows, E, N, K, (dt, st) in itertools.product(big, experts, wide, wide, types):
+    g = ctypes.byref(moe.MoeGroupShape(rows, E, N, K, dt, st))
+    size = lib.moe_group_workspace_size(g)
+    assert size < 1 << 40
+    assert lib.moe_grouped_gemm_fp8(g, P, P, P, P, P, None, W, P, None) != 0
+    assert lib.moe_grouped_dgrad(g, P, P, P, None, W, P, None) != 0
+    assert lib.moe_grouped_wgrad(g, P, P, P, None, W, P, None) != 0
+    assert lib.moe_grouped_wgrad(g, P, P, P, P, BIG >> 1, None, None) != 0
+    if rows:
+        assert lib.moe_grouped_gemm_fp8(g, P, P, P, P, P, P, BIG >> 1, None, None) != 0
+        assert lib.moe_grouped_dgrad(g, P, P, P, P, BIG >> 1, None, None) != 0
+    n += 1
+for rows, K, block, (dt, st) in itertools.product(big, wide, [-1, 0, 1, 2, 128, 1 << 62], types):
+    assert lib.moe_quantize(rows, K, block, dt, st, P, P, None, None) != 0 or rows == 0
+    assert lib.moe_quantize(rows, K, block, dt, st, P + 8, P, P, None) != 0 or rows == 0
+off = (ctypes.c_int64 * len(moe.WS_REGIONS))()
+t = moe.MoeFp8Tensor(P, P)
+w, none = ctypes.byref(t), ctypes.byref(moe.MoeFp8Tensor(P, None))
+for T, d, E, k in itertools.product(big, wide, [1, 8, 64, 65, 1024, 1025, 0], [1, 2, 8, 64, 65, 0]):
+    for F, cap, dt, fl, st in ((256, 0, 1, 0, 0), (1 << 20, T, 1, 1, 1), (128, 1 << 40, 1, 7, 0),
+                               (384, -7, 0, 3, 1), (256, 5, 1, 8, 2)):
+        s = ctypes.byref(moe.shape(T, d, E, k, F, cap, dt, fl, 0, 0))
+        lib.moe_fp8_workspace_size(s, st)
+        lib.moe_fp8_workspace_layout(s, st, off)
+        assert lib.moe_fp8_workspace_layout(s, st, None) != 0
+        for gate, ws in ((w, None), (none, P)):
+            assert lib.moe_expert_ffn_fp8(s, st, P, P, P, gate, w, w, ws, W, P, None) != 0 or T == 0
+            assert lib.moe_expert_ffn_fp8(s, st, P, None, P, gate, w, w, ws, W, P, None) != 0 \
+                or T == 0
+            assert lib.moe_layer_fp8(s, st, P, P, None, gate, w, w, ws, W, P, None, None, None,
+                                     None, None) != 0
+        n += 1
+lib.moe_group_workspace_size(None)
+lib.moe_fp8_workspace_size(None, 0)
+assert lib.moe_fp8_workspace_layout(None, 0, off) != 0
+assert lib.moe_grouped_gemm_fp8(None, P, P, P, P, P, P, W, P, None) != 0
+assert lib.moe_grouped_dgrad(None, P, P, P, P, W, P, None) != 0
+assert lib.moe_grouped_wgrad(None, P, P, P, P, W, P, None) != 0
+assert lib.moe_expert_ffn_fp8(None, 0, P, P, P, w, w, w, P, W, P, None) != 0
+assert lib.moe_layer_fp8(None, 0, P, P, None, w, w, w, P, W, P, None, None, None, None, None) != 0
+print("ok", n)
+"""
+
+
+def test_groups_and_8_bit_host_code_under_the_sanitizers():
+    rt = _runtime()
+    if rt is None:
+        pytest.skip("no AddressSanitizer runtime in this ROCm install")
+    lib = _build.LIB_SANITIZED
+    if not _fresh(lib):
+        _build.build(sanitize=True)
+    code = CHILD_GROUPS.replace("ROOT", repr(ROOT)).replace("LIB", repr(lib))
+    env = dict(os.environ, LD_PRELOAD=rt, ASAN_OPTIONS="detect_leaks=0:abort_on_error=1",
+               UBSAN_OPTIONS="print_stacktrace=1:halt_on_error=1")
+    r = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True,
+                       timeout=600)
+    assert r.returncode == 0, (r.stdout[-2000:], r.stderr[-4000:])
+    assert r.stdout.split()[0] == "ok"
