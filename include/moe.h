@@ -450,7 +450,9 @@ typedef struct {
 /* A product grouped by expert: rows [expert_offsets[e], expert_offsets[e + 1]) of the row
  * operands belong to expert e, whose weight is matrix e of [E, N, K].  Groups may be empty and
  * of any length.  Limits: 0 <= rows < 2^31, 1 <= E <= 1024, N and K multiples of 128 and at
- * most 2^20, and a grid within 2^32 threads. */
+ * most 2^20, and fewer than 2^23 tiles of work, which the kernels number with 32 bits: with rows
+ * divided down and N and K up, (rows + 63 E) / 64 * max(N, K) / 128 + 2312 and E * (N / b) *
+ * (K / b) + 8, b = 256 for MOE_BF16 and 128 for MOE_F32, are both below 2^23. */
 typedef struct {
   int64_t rows;       /* row slots of the row operands */
   int64_t E;          /* experts */
@@ -535,6 +537,10 @@ int moe_fp8_workspace_layout(const moe_shape* shape, int scale_type, int64_t* of
  * moe_quantize (block_rows 1); gate and up are 8-bit products (moe_grouped_gemm_fp8, held in
  * fp32); h = silu(gate) * up is quantized by rows in the product's epilogue, without a
  * rounding before it; y_perm is the 8-bit product of h with w_down, rounded to bf16.
+ * What the instruction cuts off gate and up (above) moves an h near the middle of two e4m3
+ * values to the other one now and then: on normal data y_perm is 2.0e-3 of its norm away from
+ * the exact network over the same quantized rows, against 1.7e-3 for one whose gate and up are
+ * held in fp32 (its rounding to bf16 alone).
  * Same sources as moe_expert_ffn.
  *   x               with src_token: [T, d] bf16, row r of expert e reads x[src_token[r]] (an
  *                   entry outside [0, T), such as an empty padded slot's -1, reads a row of x

@@ -26,9 +26,10 @@
 //   once (256 experts of 7168 / 2048 with 256 tokens, E8M0: gate/up 1.09 ms, down 0.65 ms, 6.5
 //   TB/s; the same weights straight into registers reached 3.6-4.1 TB/s).
 //   256 rows (more than 128 on average; prefill): 64 KB of LDS writes and 192 KB of reads a step
-//   against 2048 cycles of its MFMAs, and two barriers: matrix units 43-45 % busy at 2.0-2.1 GHz
-//   (8 experts of 4096 / 14336 with 4096 tokens of 2: gate/up 0.98 ms with E8M0 scales and
-//   1.06 ms with fp32 ones, down 0.50-0.52 ms; one dense expert 2600 and 2450 TFLOP/s).
+//   against 2048 cycles of its MFMAs, and two barriers: matrix units 41-45 % busy at 2.0-2.2 GHz
+//   (8 experts of 4096 / 14336 with 4096 tokens of 2: gate/up 1.01 ms with E8M0 scales and
+//   1.07 ms with fp32 ones, down 0.52 ms; one dense expert of 8192 rows, 14336 -> 4096 2460-2600
+//   and 2370-2450 TFLOP/s).
 //   128 rows: between the two, 85 flop per loaded byte, three stages.
 #include <algorithm>
 

@@ -16,10 +16,13 @@
 //     once fall into different banks.
 //   - Sums are fp32 (fp32 operands: fp32 MFMA), in the order of p, rounded once at the end.
 // Bounds and measurements (bf16): many rows, the matrix units and the LDS reads that feed them
-// (dgrad of 8191 rows, 14336 -> 4096, 8 experts 0.82 ms; wgrad of 32767 rows, 32 experts of 2048 x
-// 7168 0.95 to 1.04 ms, 16 stages a tile, so that its first loads and its stores weigh more; one
-// dense matrix of 4096 x 14336 and 8192 rows 1420 and 1270 TFLOP/s); few rows, HBM (86 rows, 32
-// experts of 13824 x 3328: dgrad reads the weights at 6.6 TB/s, wgrad writes them at 5.0).
+// (dgrad of 8191 rows, 14336 -> 4096, 8 experts 0.81 to 0.85 ms between cards, matrix units 65 %
+// busy at 1.6 GHz; wgrad of 32767 rows, 32 experts of 2048 x 7168 0.95 to 1.27 ms, 40 % busy: 16
+// stages a tile, so that its first loads and its stores weigh more; one dense matrix of 4096 x
+// 14336 and 8192 rows 1380 and 1240 TFLOP/s); few rows, HBM (86 rows, 32 experts of 13824 x 3328:
+// dgrad reads the weights at 6.6 TB/s, wgrad writes them at 5.0).  fp32 (8192 rows, 8 experts of
+// 1024 x 4096): dgrad 0.63 ms, matrix units 73 % busy; wgrad 0.67 to 0.91, 44 %.  Where tiles are
+// fewer than CUs, fp32 and wgrad leave the others idle: their reductions are not cut.
 #include <algorithm>
 
 #include "gemm_common.h"
@@ -408,9 +411,10 @@ GroupPlan dgrad_plan(int64_t R, int64_t E, int elt) {
   return p;
 }
 
-int64_t group_max_blocks(int64_t R, int64_t E, int64_t N, int64_t K, int elt) {
-  // row operands: at most (R + 63 E) / 64 row tiles by ceil(columns / 128), and up to 2048 blocks
-  // where few blocks are split further; wgrad: every tile of every expert's weight
+int64_t group_max_tiles(int64_t R, int64_t E, int64_t N, int64_t K, int elt) {
+  // row operands: at most (R + 63 E) / 64 row tiles by ceil(columns / 128), at most 2048 blocks of
+  // fewer columns in the few-tiles form of the 8-bit product, and a tail's pieces; wgrad: every
+  // tile of every expert's weight
   const int64_t rows = (R + E * 63) / 64 * (std::max(N, K) / 128) + 2048 + kSplitCUs;
   const int64_t b = elt == 2 ? 256 : 128;
   return std::max(rows, E * ((N + b - 1) / b) * ((K + b - 1) / b)) + 8;

@@ -189,8 +189,8 @@ hipError_t launch_dgrad(int dtype, const void* dy, const int32_t* offsets,
                         int64_t E, int64_t N, int64_t K, hipStream_t s);
 hipError_t launch_wgrad(int dtype, const void* dy, const void* x, const int32_t* offsets,
                         void* dw, int64_t R, int64_t E, int64_t N, int64_t K, hipStream_t s);
-// Upper bound on the blocks (512 threads each) of the grouped launches above.
-int64_t group_max_blocks(int64_t R, int64_t E, int64_t N, int64_t K, int elt);
+// Upper bound on the tiles and pieces that the grouped launches above number.
+int64_t group_max_tiles(int64_t R, int64_t E, int64_t N, int64_t K, int elt);
 
 // S8
 hipError_t launch_combine(int dtype, const void* y_perm, const int32_t* dest_row,

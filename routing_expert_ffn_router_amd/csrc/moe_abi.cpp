@@ -496,7 +496,8 @@ int moe_layer(const moe_shape* s, const void* x, const void* w_router, const flo
 // ------------------------------------------------------------------------------------------
 namespace {
 
-constexpr int64_t kMaxBlocks = (int64_t)1 << 23;  // 512 threads each: within 2^32 threads
+// tiles and pieces, numbered with 32 bits on the device and a block each in the few-tiles form
+constexpr int64_t kMaxTiles = (int64_t)1 << 23;
 
 int scale_bytes(int scale_type) { return scale_type == MOE_SCALE_E8M0 ? 1 : 4; }
 
@@ -515,7 +516,7 @@ int check_group(const moe_group_shape* g) {
   if (g->E > kMaxE || g->rows >= ((int64_t)1 << 31)) return MOE_ERR_UNSUPPORTED;
   if (g->N % 128 != 0 || g->K % 128 != 0) return MOE_ERR_UNSUPPORTED;
   if (g->N > ((int64_t)1 << 20) || g->K > ((int64_t)1 << 20)) return MOE_ERR_UNSUPPORTED;
-  if (moe::group_max_blocks(g->rows, g->E, g->N, g->K, elt_bytes(g->dtype)) >= kMaxBlocks)
+  if (moe::group_max_tiles(g->rows, g->E, g->N, g->K, elt_bytes(g->dtype)) >= kMaxTiles)
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
@@ -580,8 +581,8 @@ int check_fp8_shape(const moe_shape* s, int scale_type) {
   if (x_rows > 0 && (!product_within(x_rows, s->d, (int64_t)1 << 37) ||
                      !product_within(x_rows, s->F, (int64_t)1 << 37)))
     return MOE_ERR_UNSUPPORTED;
-  // both products' grids (either orientation)
-  if (moe::group_max_blocks(R, s->E, s->F, s->d, 2) >= kMaxBlocks) return MOE_ERR_UNSUPPORTED;
+  // both products' tiles (either orientation)
+  if (moe::group_max_tiles(R, s->E, s->F, s->d, 2) >= kMaxTiles) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

@@ -5,7 +5,7 @@
 // not depend on how the division is carried out.  Bound by HBM: each value is read once and a
 // byte written; a thread holds its values in registers between the maximum and the conversion
 // (8191 x 4096 fp32 rows 31 us, 5.4 TB/s; eight weights of 14336 x 4096 bf16 246 us, 5.7 TB/s;
-// 256 x 7168 bf16 rows 4.8 us, latency).
+// 256 x 7168 bf16 rows 3.0 us, latency).
 #include <algorithm>
 
 #include "fp8_common.h"
@@ -137,9 +137,9 @@ static hipError_t run_quantize(int64_t rows, int64_t K, int64_t block_rows, int 
     return hipGetLastError();
   }
   const int64_t groups = rows * kblocks;
-  // sixteen groups per block and step: one step where the blocks are few (256 x 7168 bf16 2.5
-  // against 3.4 us, 1024 x 4096 3.4 against 3.8; 2048 x 4096 the same), else four in flight (8192 x
-  // 4096 18.0 against 19.8 us)
+  // sixteen groups per block and step: one step where the blocks are few (256 x 7168 bf16 3.0
+  // against 3.9 us, 1024 x 4096 3.9 against 4.4; 2048 x 4096 the same), else four in flight (8192 x
+  // 4096 17.9 against 20.2 us)
   if (groups <= 32768)
     quantize_rows_kernel<T, 1><<<(unsigned)((groups + 15) / 16), 256, 0, s>>>(
         x, groups, scale_type, q, scale);
