@@ -248,7 +248,9 @@ def test_nan_stays_in_its_row_and_column(rows, kind):
     ([24, 7], 256, 384),                       # the reduction over a block's waves
     ([20, 32, 9], 16512, 384),                 # tiles of 64, 128 and 256 rows
     ([70, 90], 384, 640), ([200, 300, 65], 256, 512),
-    ([65, 100, 90], 384, 6272)])               # a reduction in pieces
+    ([65, 100, 90], 384, 6272),                # a reduction in pieces
+    # blocks that go on from a tile computed twice to others, 64, 128 and 256 rows high
+    ([20, 64, 9], 25728, 384), ([66, 100, 90], 25728, 256), ([300, 129, 400], 16768, 256)])
 def test_fp32_scales_whose_product_is_past_the_range(counts, N, K):
     c = _product_case(counts, N, K, "f32", seed=N + K)
     clean = _run_product(c)
