@@ -12,9 +12,9 @@
 //     dot product may be 0 or small, a tile is computed again with the exponents given to the
 //     instruction, which adds them in a wider range, and only what is left of each scale, 1 <= m
 //     < 4, multiplied in fp32 (a product where every tile is: 530 -> 1243 us, 638 -> 1297; that
-//     form alone in place of the usual one costs 8 to 17 % of every product).  The few-tiles form
-//     below always takes it: its loads hide the difference (16 rows, K = 4096, N = 16384 21.1 and
-//     21.3 us).
+//     form alone in place of the usual one costs 8 to 17 % of every product; the check costs 1 to
+//     2 % of gate/up in 256-row tiles and nothing elsewhere).  The few-tiles form below always
+//     takes it: its loads hide the difference (16 rows, K = 4096, N = 16384 21.1 and 21.3 us).
 // The order of the 128 values within a step is free (both operands use one order and the scale is
 // the same for all), so a lane takes the 16-byte pieces g and g + 4 of its row's 128 bytes (g
 // = lane / 16).  The weight fragment goes first: a lane then holds one row's four consecutive
