@@ -360,7 +360,7 @@ __device__ __attribute__((always_inline)) inline void fp8_body(
   if (issuer) __builtin_amdgcn_s_setprio(3);
 
   for (;;) {
-    // (what the last round left, in scalar registers again)
+    // (what the last tile left, in scalar registers again)
     base_a = uniform_u64(base_a);
     base_xs = uniform_u64(base_xs);
     wt.b = uniform_u64(wt.b);
