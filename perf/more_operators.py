@@ -360,8 +360,7 @@ def _own(s):
             s["workspace"] = torch.empty(moe.grad_workspace_size(len(s["grads"])),
                                          dtype=torch.uint8, device="cuda")
             s["norm"] = torch.empty(1, dtype=torch.float32, device="cuda")
-        moe.grad_norm(s["grads"], s["workspace"], s["norm"])
-        moe.grad_clip(s["grads"], s["max_norm"], s["norm"], s["out"])
+        moe.clip_grad_norm(s["grads"], s["max_norm"], s["workspace"], s["norm"], s["out"])
         return {"norm": s["norm"], **s["flat"]}
     dt = moe.MOE_BF16 if s["dtype"] == "bf16" else moe.MOE_F32
     if op == "few":
