@@ -523,6 +523,81 @@ int moe_grouped_wgrad(const moe_group_shape* shape, const void* dy, const void* 
                       const int32_t* expert_offsets, void* workspace, size_t workspace_bytes,
                       void* dw, hipStream_t stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Linear layers with a bias, an activation and a residual, their backward pass up to the
+ * products, and the clipping of gradients.
+ * ------------------------------------------------------------------------------------------ */
+
+/* Activations.  gelu is z P(z), P the normal distribution; gelu_tanh its form with a tanh,
+ * z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2.  relu(0) and its slope there are 0. */
+typedef enum {
+  MOE_ACT_NONE = 0,
+  MOE_ACT_RELU = 1,
+  MOE_ACT_SILU = 2,
+  MOE_ACT_GELU = 3,
+  MOE_ACT_GELU_TANH = 4
+} moe_activation;
+
+/* Bytes of device workspace of moe_grouped_linear and moe_grouped_linear_grad (the same size
+ * serves both); 0 for an invalid shape.  Host function. */
+size_t moe_linear_workspace_size(const moe_group_shape* shape);
+
+/*
+ * moe_grouped_linear_grad -- backward pass of moe_grouped_linear up to its product, from the
+ * gradient dy of y and the z that the forward pass kept:
+ *   dz[r, n] = dy[r, n] * act'(z[r, n]),   dbias[e, n] = sum of dz[r, n] over the rows r of expert e
+ * in fp32, dz rounded once to dtype, dbias the sum of the unrounded values (0 for an expert without
+ * rows).  moe_grouped_dgrad and moe_grouped_wgrad go on from dz; the residual's gradient is dy.
+ * K of the shape is not used.  Rows outside [expert_offsets[0], expert_offsets[E]) of dy and z are
+ * not read, and those of dz not written.
+ *   dy     [rows, N] dtype in
+ *   z      [rows, N] dtype in; may be NULL with MOE_ACT_NONE
+ *   dz     [rows, N] dtype out, nullable; may be dy itself
+ *   dbias  [E, N] float out, nullable
+ *   expert_offsets as in moe_grouped_gemm_fp8; workspace moe_linear_workspace_size() bytes,
+ *   256-byte aligned
+ */
+int moe_grouped_linear_grad(const moe_group_shape* shape, int activation, const void* dy,
+                            const void* z, const int32_t* expert_offsets, void* workspace,
+                            size_t workspace_bytes, void* dz, float* dbias, hipStream_t stream);
+
+/* A gradient: n values of a dtype, contiguous, aligned to their type.  out is where moe_grad_clip
+ * puts them, grad itself for clipping in place (moe_grad_norm ignores it). */
+typedef struct {
+  const void* grad;
+  void* out;
+  int64_t n;     /* 0 <= n < 2^36; pointers may be NULL when 0 */
+  int64_t dtype; /* moe_dtype */
+} moe_grad;
+
+/* Bytes of device workspace of moe_grad_norm over `count` gradients; 0 for a count outside
+ * [0, 2^20].  Host function. */
+size_t moe_grad_workspace_size(int64_t count);
+
+/*
+ * moe_grad_norm -- the 2-norm over all values of all gradients, sqrt(sum of squares): squares and
+ * sums in 64 bits, added in an order that depends on the lengths alone.  A NaN or an infinity among
+ * the values makes the norm NaN or infinite.
+ *   grads      host array [count], read before the call returns
+ *   workspace  moe_grad_workspace_size() bytes, 256-byte aligned
+ *   norm       [1] float out (0 without gradients)
+ */
+int moe_grad_norm(int64_t count, const moe_grad* grads, void* workspace, size_t workspace_bytes,
+                  float* norm, hipStream_t stream);
+
+/*
+ * moe_grad_clip -- out = grad * (max_norm / norm) where norm > max_norm, and out = grad otherwise,
+ * also where the norm is infinite or NaN.  The factor is an fp32 number, the product rounded to fp32
+ * and then to the gradient's type.  The norm is read on the device: moe_grad_norm's, or one that the
+ * caller made of several.
+ * No out may overlap another gradient's memory, or its own grad unless it is the same.
+ *   grads  host array [count], read before the call returns
+ *   norm   [1] float in
+ * max_norm is finite and at least 0.
+ */
+int moe_grad_clip(int64_t count, const moe_grad* grads, float max_norm, const float* norm,
+                  hipStream_t stream);
+
 /* Bytes of device workspace for moe_expert_ffn_fp8 and moe_layer_fp8 (the same size serves
  * both); 0 for an invalid shape or scale type, or a dtype other than MOE_BF16.  Host function. */
 size_t moe_fp8_workspace_size(const moe_shape* shape, int scale_type);

@@ -7,6 +7,7 @@ and streams.  If libmoe.so is missing, loading fails with an error: there is no 
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import re
@@ -30,6 +31,12 @@ MOE_BF16 = 1
 
 MOE_SCALE_F32 = 0
 MOE_SCALE_E8M0 = 1
+
+MOE_ACT_NONE = 0
+MOE_ACT_RELU = 1
+MOE_ACT_SILU = 2
+MOE_ACT_GELU = 3
+MOE_ACT_GELU_TANH = 4
 
 MOE_FLAG_PAD_TO_CAPACITY = 1
 MOE_FLAG_SLOT_MAJOR = 2
@@ -146,6 +153,11 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_grouped_gemm_fp8": (i32, [_G, _P, _P, _P, _P, _P, _P, sz, _P, _P]),
         "moe_grouped_dgrad": (i32, [_G, _P, _P, _P, _P, sz, _P, _P]),
         "moe_grouped_wgrad": (i32, [_G, _P, _P, _P, _P, sz, _P, _P]),
+        "moe_linear_workspace_size": (sz, [_G]),
+        "moe_grouped_linear_grad": (i32, [_G, i32, _P, _P, _P, _P, sz, _P, _P, _P]),
+        "moe_grad_workspace_size": (sz, [i64]),
+        "moe_grad_norm": (i32, [i64, _P, _P, sz, _P, _P]),
+        "moe_grad_clip": (i32, [i64, _P, ctypes.c_float, _P, _P]),
         "moe_fp8_workspace_size": (sz, [_S, i32]),
         "moe_fp8_workspace_layout": (i32, [_S, i32, ctypes.POINTER(i64)]),
         "moe_expert_ffn_fp8": (i32, [_S, i32, _P, _P, _P, _W, _W, _W, _P, sz, _P, _P]),
@@ -711,6 +723,105 @@ class MoELayerFp8:
                   self.workspace, self.out, self.routed_counts, self.tokens_per_expert,
                   self.drops, self.status, stream)
         return self.out
+
+
+# -------------------------------------------------------------------- linear layers, clipping
+def linear_workspace_size(g: MoeGroupShape) -> int:
+    return int(load_library().moe_linear_workspace_size(ctypes.byref(g)))
+
+
+def grouped_linear_grad(g: MoeGroupShape, activation: int, dy, z, expert_offsets, workspace,
+                        dz=None, dbias=None, stream=None) -> None:
+    """moe_grouped_linear_grad: dz = dy * act'(z) and the sums of dz over each expert's rows.
+    z may be None without an activation, dz and dbias where they are not wanted."""
+    ty, gpu = _begin()
+    R, E, N = g.rows, g.E, g.N
+    dt = _group_act(ty, g)
+    ws, nbytes = _workspace_arg(workspace, gpu)
+    _check("moe_grouped_linear_grad", load_library().moe_grouped_linear_grad(
+        ctypes.byref(g), activation, _arg(dy, "dy", dt, (R, N), gpu),
+        _optional(z, "z", dt, (R, N), gpu),
+        _optional(expert_offsets, "expert_offsets", ty.i32, (E + 1,), gpu), ws, nbytes,
+        _optional(dz, "dz", dt, (R, N), gpu), _optional(dbias, "dbias", ty.f32, (E, N), gpu),
+        _stream(stream)))
+
+
+def grad_workspace_size(count: int) -> int:
+    return int(load_library().moe_grad_workspace_size(count))
+
+
+def _grad_table(grads, out, ty: _Types, gpu: int):
+    """moe_grad of each gradient, as 64-bit words of an array, and their number."""
+    if out is None:
+        out = grads
+    elif len(out) != len(grads):
+        raise ValueError(f"{len(out)} outputs for {len(grads)} gradients")
+    words, acts = [], ty.acts
+    for i, (g, o) in enumerate(zip(grads, out)):
+        dt = acts.get(g.dtype, -1)
+        if dt < 0 or g.get_device() != gpu or not g.is_contiguous():
+            _arg(g, f"gradient {i}", tuple(acts), g.shape, gpu)
+        if o is not g and (o.dtype != g.dtype or o.numel() != g.numel()
+                           or o.get_device() != gpu or not o.is_contiguous()):
+            _arg(o, f"output {i}", (g.dtype,), g.shape, gpu)
+            raise ValueError(f"output {i} has {o.numel()} values for {g.numel()}")
+        words += (g.data_ptr(), o.data_ptr(), g.numel(), dt)
+    return array.array("q", words), len(words) // 4
+
+
+def _check_apart(table, count: int) -> None:
+    """No output overlaps another gradient or output, or its own gradient in part."""
+    spans = []
+    for i in range(count):
+        g, o, n, dt = table[4 * i:4 * i + 4]
+        if n:
+            size = n * (2 if dt == MOE_BF16 else 4)
+            spans.append((o, o + size, True))
+            if g != o:
+                spans.append((g, g + size, False))
+    spans.sort()
+    end = out_end = 0  # the furthest end so far, and that of the outputs
+    for a, b, is_out in spans:
+        if a < out_end or (is_out and a < end):
+            raise ValueError("an output overlaps another gradient")
+        end = max(end, b)
+        if is_out:
+            out_end = max(out_end, b)
+
+
+def grad_norm(grads, workspace, norm, stream=None) -> None:
+    """moe_grad_norm: norm [1] of all values of a list of gradients (contiguous bf16 or fp32
+    tensors of any shapes)."""
+    ty, gpu = _begin()
+    table, count = _grad_table(grads, None, ty, gpu)
+    ws, nbytes = _workspace_arg(workspace, gpu)
+    _check("moe_grad_norm", load_library().moe_grad_norm(
+        count, table.buffer_info()[0], ws, nbytes, _arg(norm, "norm", ty.f32, (1,), gpu),
+        _stream(stream)))
+
+
+def grad_clip(grads, max_norm: float, norm, out=None, stream=None) -> None:
+    """moe_grad_clip: every gradient times max_norm / norm where norm > max_norm, in place or into
+    the tensors of `out`."""
+    ty, gpu = _begin()
+    table, count = _grad_table(grads, out, ty, gpu)
+    _check_apart(table, count)
+    _check("moe_grad_clip", load_library().moe_grad_clip(
+        count, table.buffer_info()[0], max_norm, _arg(norm, "norm", ty.f32, (1,), gpu),
+        _stream(stream)))
+
+
+def clip_grad_norm(grads, max_norm: float, workspace, norm, out=None, stream=None) -> None:
+    """grad_norm, then grad_clip by it."""
+    ty, gpu = _begin()
+    table, count = _grad_table(grads, out, ty, gpu)
+    _check_apart(table, count)
+    ws, nbytes = _workspace_arg(workspace, gpu)
+    norm_ptr, s, lib = _arg(norm, "norm", ty.f32, (1,), gpu), _stream(stream), load_library()
+    _check("moe_grad_norm", lib.moe_grad_norm(count, table.buffer_info()[0], ws, nbytes, norm_ptr,
+                                              s))
+    _check("moe_grad_clip", lib.moe_grad_clip(count, table.buffer_info()[0], max_norm, norm_ptr,
+                                              s))
 
 
 # ------------------------------------------------------------------------------ calibration

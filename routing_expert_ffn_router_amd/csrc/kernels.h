@@ -192,6 +192,37 @@ hipError_t launch_wgrad(int dtype, const void* dy, const void* x, const int32_t*
 // Upper bound on the tiles and pieces that the grouped launches above number.
 int64_t group_max_tiles(int64_t R, int64_t E, int64_t N, int64_t K, int elt);
 
+// ---------------------------------------------------------------------------------------
+// linear layers of the experts and clipping of gradients
+// ---------------------------------------------------------------------------------------
+// dz = dy * act'(z) and db[e] = sum of dz over the rows of expert e.  partial: rows of N sums, one
+// for each of linear_grad_slots() row tiles (with db only).  dz and z may be null without an
+// activation.
+constexpr int kGradRows = 64;
+inline int64_t linear_grad_slots(int64_t R, int64_t E) { return R / kGradRows + E; }
+hipError_t launch_linear_grad(int dtype, int act, const void* dy, const void* z,
+                              const int32_t* offsets, void* dz, float* db, float* partial,
+                              int64_t R, int64_t E, int64_t N, hipStream_t s);
+
+struct GradTensor {  // moe_grad
+  const void* grad;
+  void* out;
+  int64_t n;
+  int64_t dtype;
+};
+// Tensors of one launch: what 4 KB of kernel arguments hold.
+constexpr int kNormTensors = 192, kClipTensors = 136;
+// Blocks of a launch: eight of 256 threads for each of the 256 CUs.
+constexpr int kNormBlocks = 2048, kClipBlocks = 2048;
+// Sums that launch_grad_norm may leave in partial: those of each launch's blocks.
+inline int64_t grad_norm_sums(int64_t count) {
+  return (count + kNormTensors - 1) / kNormTensors * kNormBlocks;
+}
+hipError_t launch_grad_norm(int64_t count, const GradTensor* g, double* partial, float* norm,
+                            hipStream_t s);
+hipError_t launch_grad_clip(int64_t count, const GradTensor* g, float max_norm,
+                            const float* norm, hipStream_t s);
+
 // S8
 hipError_t launch_combine(int dtype, const void* y_perm, const int32_t* dest_row,
                           const float* topk_w, void* out, int64_t T, int64_t d, int64_t k,

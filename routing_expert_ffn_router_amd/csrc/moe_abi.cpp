@@ -834,3 +834,96 @@ int moe_layer_fp8(const moe_shape* s, int scale_type, const void* x, const void*
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------------------------------------------
+// linear layers and clipping
+// ------------------------------------------------------------------------------------------
+namespace {
+
+constexpr int64_t kMaxGrads = (int64_t)1 << 20;
+static_assert(sizeof(moe_grad) == sizeof(moe::GradTensor), "one layout");
+
+bool known_activation(int act) { return act >= MOE_ACT_NONE && act <= MOE_ACT_GELU_TANH; }
+
+// The sums of dz by row tiles.
+int64_t linear_workspace(const moe_group_shape* g) {
+  return align_up(moe::linear_grad_slots(g->rows, g->E) * g->N * 4);
+}
+
+int check_linear_call(const moe_group_shape* g, int act, const int32_t* offsets, const void* ws,
+                      size_t ws_bytes) {
+  const int rc = check_group(g);
+  if (rc != MOE_OK) return rc;
+  if (!known_activation(act)) return MOE_ERR_UNSUPPORTED;
+  if (!offsets && g->E != 1) return MOE_ERR_INVALID_ARG;
+  if (!ws || (int64_t)ws_bytes < linear_workspace(g)) return MOE_ERR_WORKSPACE;
+  if (((uintptr_t)ws & (kAlign - 1)) != 0) return MOE_ERR_ALIGNMENT;
+  return MOE_OK;
+}
+
+int check_grads(int64_t count, const moe_grad* g, bool out) {
+  if (count < 0 || (count > 0 && !g)) return MOE_ERR_INVALID_ARG;
+  if (count > kMaxGrads) return MOE_ERR_UNSUPPORTED;
+  for (int64_t i = 0; i < count; ++i) {
+    if (g[i].n < 0) return MOE_ERR_INVALID_ARG;
+    if (g[i].dtype != MOE_F32 && g[i].dtype != MOE_BF16) return MOE_ERR_UNSUPPORTED;
+    if (g[i].n >= ((int64_t)1 << 36)) return MOE_ERR_UNSUPPORTED;
+    if (g[i].n == 0) continue;
+    if (!g[i].grad || (out && !g[i].out)) return MOE_ERR_INVALID_ARG;
+    const uintptr_t mask = (uintptr_t)elt_bytes((int32_t)g[i].dtype) - 1;
+    if (((uintptr_t)g[i].grad & mask) != 0 || (out && ((uintptr_t)g[i].out & mask) != 0))
+      return MOE_ERR_ALIGNMENT;
+  }
+  return MOE_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_linear_workspace_size(const moe_group_shape* g) {
+  if (check_group(g) != MOE_OK) return 0;
+  return (size_t)linear_workspace(g);
+}
+
+int moe_grouped_linear_grad(const moe_group_shape* g, int act, const void* dy, const void* z,
+                            const int32_t* expert_offsets, void* ws, size_t ws_bytes, void* dz,
+                            float* dbias, hipStream_t st) {
+  const int rc = check_linear_call(g, act, expert_offsets, ws, ws_bytes);
+  if (rc != MOE_OK) return rc;
+  // without rows every sum is zero: dy and z may be null
+  if (g->rows > 0 && (!dy || (!z && act != MOE_ACT_NONE))) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(dy) || !aligned16(z) || !aligned16(dz) || !aligned16(dbias))
+    return MOE_ERR_ALIGNMENT;
+  return hip_status(moe::launch_linear_grad(g->dtype, act, dy, z, expert_offsets, dz, dbias,
+                                            static_cast<float*>(ws), g->rows, g->E, g->N, st));
+}
+
+size_t moe_grad_workspace_size(int64_t count) {
+  if (count < 0 || count > kMaxGrads) return 0;
+  return (size_t)align_up((moe::grad_norm_sums(count) + 1) * 8);
+}
+
+int moe_grad_norm(int64_t count, const moe_grad* grads, void* ws, size_t ws_bytes, float* norm,
+                  hipStream_t st) {
+  const int rc = check_grads(count, grads, false);
+  if (rc != MOE_OK) return rc;
+  if (!norm) return MOE_ERR_INVALID_ARG;
+  if (!aligned4(norm)) return MOE_ERR_ALIGNMENT;
+  if (!ws || ws_bytes < moe_grad_workspace_size(count)) return MOE_ERR_WORKSPACE;
+  if (((uintptr_t)ws & (kAlign - 1)) != 0) return MOE_ERR_ALIGNMENT;
+  return hip_status(moe::launch_grad_norm(count, reinterpret_cast<const moe::GradTensor*>(grads),
+                                          static_cast<double*>(ws), norm, st));
+}
+
+int moe_grad_clip(int64_t count, const moe_grad* grads, float max_norm, const float* norm,
+                  hipStream_t st) {
+  const int rc = check_grads(count, grads, true);
+  if (rc != MOE_OK) return rc;
+  if (!norm || !(max_norm >= 0) || !isfinite(max_norm)) return MOE_ERR_INVALID_ARG;
+  if (!aligned4(norm)) return MOE_ERR_ALIGNMENT;
+  return hip_status(moe::launch_grad_clip(
+      count, reinterpret_cast<const moe::GradTensor*>(grads), max_norm, norm, st));
+}
+
+}  // extern "C"
