@@ -543,6 +543,25 @@ typedef enum {
 size_t moe_linear_workspace_size(const moe_group_shape* shape);
 
 /*
+ * moe_grouped_linear -- linear layer grouped by expert, for the rows r of expert e:
+ *   z[r, n] = (sum over k of x[r, k] * w[e, n, k]) + bias[e, n],   y[r, n] = act(z[r, n]) + residual[r, n]
+ * summed and evaluated in fp32, y rounded once to dtype (act is applied to the unrounded z), and z,
+ * where the caller keeps it for the backward pass, rounded once.  Rows outside [expert_offsets[0],
+ * expert_offsets[E]) of x and residual are not used, and those of y and z not written.
+ *   x         [rows, K] dtype in; w [E, N, K] dtype in
+ *   bias      [E, N] float in, nullable
+ *   residual  [rows, N] dtype in, nullable; may be y itself
+ *   z         [rows, N] dtype out, nullable
+ *   y         [rows, N] dtype out
+ *   expert_offsets as in moe_grouped_gemm_fp8; workspace moe_linear_workspace_size() bytes,
+ *   256-byte aligned
+ */
+int moe_grouped_linear(const moe_group_shape* shape, int activation, const void* x,
+                       const int32_t* expert_offsets, const void* w, const float* bias,
+                       const void* residual, void* workspace, size_t workspace_bytes, void* z,
+                       void* y, hipStream_t stream);
+
+/*
  * moe_grouped_linear_grad -- backward pass of moe_grouped_linear up to its product, from the
  * gradient dy of y and the z that the forward pass kept:
  *   dz[r, n] = dy[r, n] * act'(z[r, n]),   dbias[e, n] = sum of dz[r, n] over the rows r of expert e

@@ -154,6 +154,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_grouped_dgrad": (i32, [_G, _P, _P, _P, _P, sz, _P, _P]),
         "moe_grouped_wgrad": (i32, [_G, _P, _P, _P, _P, sz, _P, _P]),
         "moe_linear_workspace_size": (sz, [_G]),
+        "moe_grouped_linear": (i32, [_G, i32, _P, _P, _P, _P, _P, _P, sz, _P, _P, _P]),
         "moe_grouped_linear_grad": (i32, [_G, i32, _P, _P, _P, _P, sz, _P, _P, _P]),
         "moe_grad_workspace_size": (sz, [i64]),
         "moe_grad_norm": (i32, [i64, _P, _P, sz, _P, _P]),
@@ -728,6 +729,22 @@ class MoELayerFp8:
 # -------------------------------------------------------------------- linear layers, clipping
 def linear_workspace_size(g: MoeGroupShape) -> int:
     return int(load_library().moe_linear_workspace_size(ctypes.byref(g)))
+
+
+def grouped_linear(g: MoeGroupShape, activation: int, x, expert_offsets, w, bias, residual,
+                   workspace, y, z=None, stream=None) -> None:
+    """moe_grouped_linear: y = act(x w[e]^T + bias[e]) + residual; bias, residual and z (what act
+    takes, for the backward pass) may be None."""
+    ty, gpu = _begin()
+    R, E, N, K = g.rows, g.E, g.N, g.K
+    dt = _group_act(ty, g)
+    ws, nbytes = _workspace_arg(workspace, gpu)
+    _check("moe_grouped_linear", load_library().moe_grouped_linear(
+        ctypes.byref(g), activation, _arg(x, "x", dt, (R, K), gpu),
+        _optional(expert_offsets, "expert_offsets", ty.i32, (E + 1,), gpu),
+        _arg(w, "w", dt, (E, N, K), gpu), _optional(bias, "bias", ty.f32, (E, N), gpu),
+        _optional(residual, "residual", dt, (R, N), gpu), ws, nbytes,
+        _optional(z, "z", dt, (R, N), gpu), _arg(y, "y", dt, (R, N), gpu), _stream(stream)))
 
 
 def grouped_linear_grad(g: MoeGroupShape, activation: int, dy, z, expert_offsets, workspace,

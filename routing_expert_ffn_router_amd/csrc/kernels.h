@@ -195,6 +195,24 @@ int64_t group_max_tiles(int64_t R, int64_t E, int64_t N, int64_t K, int elt);
 // ---------------------------------------------------------------------------------------
 // linear layers of the experts and clipping of gradients
 // ---------------------------------------------------------------------------------------
+// y = act(x W[e]^T + bias[e]) + residual, z what act takes.
+struct LinearArgs {
+  int dtype, act;
+  const void* x;           // [R, K]
+  const void* w;           // [E, N, K]
+  const int32_t* offsets;  // [E+1], nullable: one expert holds all rows
+  const int32_t* table;    // launch_tile_table of linear_plan(R, E), or null (group_needs_table)
+  const float* bias;       // [E, N], nullable
+  const void* residual;    // [R, N], nullable
+  void* z;                 // [R, N], nullable
+  void* y;                 // [R, N]
+  void* partial;           // linear_split().bytes
+  int64_t R, E, N, K;
+};
+GroupPlan linear_plan(int64_t R, int64_t E);
+GroupSplit linear_split(int64_t R, int64_t E, int64_t N, int64_t K, int elt);
+hipError_t launch_linear(const LinearArgs& a, hipStream_t s);
+
 // dz = dy * act'(z) and db[e] = sum of dz over the rows of expert e.  partial: rows of N sums, one
 // for each of linear_grad_slots() row tiles (with db only).  dz and z may be null without an
 // activation.

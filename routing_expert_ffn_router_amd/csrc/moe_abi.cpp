@@ -845,9 +845,16 @@ static_assert(sizeof(moe_grad) == sizeof(moe::GradTensor), "one layout");
 
 bool known_activation(int act) { return act >= MOE_ACT_NONE && act <= MOE_ACT_GELU_TANH; }
 
-// The sums of dz by row tiles.
+int64_t linear_table_bytes(const moe_group_shape* g) {
+  return align_up(moe::group_table_ints(moe::linear_plan(g->rows, g->E)) * 4);
+}
+// Forward: the tile table, then the partial sums of split tiles; backward: the sums of dz by row
+// tiles.
 int64_t linear_workspace(const moe_group_shape* g) {
-  return align_up(moe::linear_grad_slots(g->rows, g->E) * g->N * 4);
+  const int64_t a = linear_table_bytes(g) +
+                    moe::linear_split(g->rows, g->E, g->N, g->K, elt_bytes(g->dtype)).bytes;
+  const int64_t b = align_up(moe::linear_grad_slots(g->rows, g->E) * g->N * 4);
+  return a > b ? a : b;
 }
 
 int check_linear_call(const moe_group_shape* g, int act, const int32_t* offsets, const void* ws,
@@ -884,6 +891,39 @@ extern "C" {
 size_t moe_linear_workspace_size(const moe_group_shape* g) {
   if (check_group(g) != MOE_OK) return 0;
   return (size_t)linear_workspace(g);
+}
+
+int moe_grouped_linear(const moe_group_shape* g, int act, const void* x,
+                       const int32_t* expert_offsets, const void* w, const float* bias,
+                       const void* residual, void* ws, size_t ws_bytes, void* z, void* y,
+                       hipStream_t st) {
+  int rc = check_linear_call(g, act, expert_offsets, ws, ws_bytes);
+  if (rc != MOE_OK) return rc;
+  if (g->rows == 0) return MOE_OK;
+  if (!x || !w || !y) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w) || !aligned16(bias) || !aligned16(residual) ||
+      !aligned16(z) || !aligned16(y))
+    return MOE_ERR_ALIGNMENT;
+  moe::LinearArgs a = {};
+  int32_t* table = nullptr;
+  rc = group_table(g, moe::linear_plan(g->rows, g->E), expert_offsets, ws, &table, st);
+  if (rc != MOE_OK) return rc;
+  a.dtype = g->dtype;
+  a.act = act;
+  a.x = x;
+  a.w = w;
+  a.offsets = expert_offsets;
+  a.table = table;
+  a.bias = bias;
+  a.residual = residual;
+  a.z = z;
+  a.y = y;
+  a.partial = static_cast<char*>(ws) + linear_table_bytes(g);
+  a.R = g->rows;
+  a.E = g->E;
+  a.N = g->N;
+  a.K = g->K;
+  return hip_status(moe::launch_linear(a, st));
 }
 
 int moe_grouped_linear_grad(const moe_group_shape* g, int act, const void* dy, const void* z,

@@ -1,5 +1,5 @@
-"""Argument checks, workspace sizes and refusals of the linear layers' backward pass and of gradient
-clipping on the host.  Nothing here launches a kernel: every call is refused before the first HIP
+"""Argument checks, workspace sizes and refusals of the linear layers and of gradient clipping on
+the host.  Nothing here launches a kernel: every call is refused before the first HIP
 call."""
 import ctypes
 
@@ -19,6 +19,14 @@ def group(**kw):
     return moe.MoeGroupShape(**a)
 
 
+def linear(g, **kw):
+    a = dict(act=moe.MOE_ACT_GELU, x=P, off=P, w=P, bias=P, res=P, work=P, n=1 << 40, z=P, y=P)
+    a.update(kw)
+    return lib.moe_grouped_linear(None if g is None else ctypes.byref(g), a["act"], a["x"],
+                                  a["off"], a["w"], a["bias"], a["res"], a["work"], a["n"],
+                                  a["z"], a["y"], None)
+
+
 def linear_grad(g, **kw):
     a = dict(act=moe.MOE_ACT_GELU, dy=P, z=P, off=P, work=P, n=1 << 40, dz=P, db=P)
     a.update(kw)
@@ -36,18 +44,30 @@ BAD_CALLS = [
     (dict(work=None), WORKSPACE), (dict(n=0), WORKSPACE), (dict(work=P + 128), ALIGNMENT)]
 
 
-@pytest.mark.parametrize("call", [linear_grad])
+@pytest.mark.parametrize("call", [linear, linear_grad])
 @pytest.mark.parametrize("kw,want", BAD_GROUPS)
 def test_group_shapes_are_refused(call, kw, want):
     assert call(group(**kw)) == want
     assert moe.linear_workspace_size(group(**kw)) == 0
 
 
-@pytest.mark.parametrize("call", [linear_grad])
+@pytest.mark.parametrize("call", [linear, linear_grad])
 @pytest.mark.parametrize("kw,want", BAD_CALLS)
 def test_calls_are_refused(call, kw, want):
     assert call(group(), **kw) == want
     assert call(None) == INVALID
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(x=None), INVALID), (dict(w=None), INVALID), (dict(y=None), INVALID),
+    (dict(x=P + 8), ALIGNMENT), (dict(w=P + 8), ALIGNMENT), (dict(bias=P + 4), ALIGNMENT),
+    (dict(res=P + 2), ALIGNMENT), (dict(z=P + 8), ALIGNMENT), (dict(y=P + 8), ALIGNMENT)])
+def test_linear_operands(kw, want):
+    assert linear(group(), **kw) == want
+
+
+def test_linear_of_no_rows_needs_no_operands():
+    assert linear(group(rows=0), x=None, w=None, y=None) == moe.MOE_OK
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -63,6 +83,7 @@ def test_workspace_is_what_the_call_asks_for():
         n = moe.linear_workspace_size(g)
         assert n > 0 and n % 256 == 0
         assert linear_grad(g, n=n - 1) == WORKSPACE
+        assert linear(g, n=n - 1) == WORKSPACE
 
 
 def grads(*items):
