@@ -667,6 +667,48 @@ int moe_layer_fp8(const moe_shape* shape, int scale_type, const void* x, const v
                   int32_t* tokens_per_expert, int32_t* drops, int32_t* status,
                   hipStream_t stream);
 
+/* ------------------------------------------------------------------------------------------
+ * The whole layer for a few tokens: a step of one chat, of some drafted tokens, of a small batch.
+ * ------------------------------------------------------------------------------------------ */
+#define MOE_FEW_MAX_TOKENS 16
+
+/* Bytes of device workspace of moe_layer_few and moe_layer_few_fp8 (the same size serves both);
+ * 0 for an invalid shape, T > MOE_FEW_MAX_TOKENS, T * k > 512 or T * k * F values of h past 2^31
+ * bytes.  Host function. */
+size_t moe_few_workspace_size(const moe_shape* shape);
+
+/*
+ * moe_layer_few -- moe_layer for at most MOE_FEW_MAX_TOKENS tokens, which is bound by reading the
+ * chosen experts' weights once: no rows are packed and no row tiles filled.  The same layer as
+ * moe_layer's, with these differences in its roundings: router logits are summed in 64 bits and
+ * rounded once to fp32, so that the selection is the exact logits'; an expert's outputs are not
+ * rounded before they are weighted and added (in fp32, by expert).  h is rounded to dtype.
+ * MOE_FLAG_PAD_TO_CAPACITY changes nothing: there are no row slots.
+ *   workspace  moe_few_workspace_size() bytes, 256-byte aligned
+ *   routed_counts, tokens_per_expert [E], drops [k+2], status [1] int32 out, all nullable, as in
+ *              moe_layer
+ * Other arguments as in moe_layer.  MOE_ERR_UNSUPPORTED outside moe_few_workspace_size's limits.
+ */
+int moe_layer_few(const moe_shape* shape, const void* x, const void* w_router,
+                  const float* b_router, const void* w_gate, const void* w_up,
+                  const void* w_down, void* workspace, size_t workspace_bytes, void* out,
+                  int32_t* routed_counts, int32_t* tokens_per_expert, int32_t* drops,
+                  int32_t* status, hipStream_t stream);
+
+/*
+ * moe_layer_few_fp8 -- moe_layer_few with 8-bit expert weights.  x and h stay in bf16: a weight's
+ * value e4m3 * scale is exact, its products with bf16 are summed in fp32 over each block of 128 and
+ * then scaled, so the result is that of the weights as they are, without the quantization of x and h
+ * that moe_layer_fp8 has.
+ * Arguments as in moe_layer_few and moe_expert_ffn_fp8; shape->dtype must be MOE_BF16.
+ */
+int moe_layer_few_fp8(const moe_shape* shape, int scale_type, const void* x,
+                      const void* w_router, const float* b_router,
+                      const moe_fp8_tensor* w_gate, const moe_fp8_tensor* w_up,
+                      const moe_fp8_tensor* w_down, void* workspace, size_t workspace_bytes,
+                      void* out, int32_t* routed_counts, int32_t* tokens_per_expert,
+                      int32_t* drops, int32_t* status, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -24,6 +24,7 @@ MOE_ERR_ALIGNMENT = -3
 MOE_ERR_WORKSPACE = -4
 MOE_ERR_HIP = -5
 MOE_ERR_SCRATCH = -6
+FEW_MAX_TOKENS = 16  # MOE_FEW_MAX_TOKENS
 DISPATCH_SCRATCH_BYTES = 8 << 20  # MOE_DISPATCH_SCRATCH_BYTES
 
 MOE_F32 = 0
@@ -153,6 +154,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_grouped_gemm_fp8": (i32, [_G, _P, _P, _P, _P, _P, _P, sz, _P, _P]),
         "moe_grouped_dgrad": (i32, [_G, _P, _P, _P, _P, sz, _P, _P]),
         "moe_grouped_wgrad": (i32, [_G, _P, _P, _P, _P, sz, _P, _P]),
+        "moe_few_workspace_size": (sz, [_S]),
+        "moe_layer_few": (i32, [_S, _P, _P, _P, _P, _P, _P, _P, sz, _P, _P, _P, _P, _P, _P]),
+        "moe_layer_few_fp8": (i32, [_S, i32, _P, _P, _P, _W, _W, _W, _P, sz, _P, _P, _P, _P, _P,
+                                    _P]),
         "moe_linear_workspace_size": (sz, [_G]),
         "moe_grouped_linear": (i32, [_G, i32, _P, _P, _P, _P, _P, _P, sz, _P, _P, _P]),
         "moe_grouped_linear_grad": (i32, [_G, i32, _P, _P, _P, _P, sz, _P, _P, _P]),
@@ -839,6 +844,59 @@ def clip_grad_norm(grads, max_norm: float, workspace, norm, out=None, stream=Non
                                               s))
     _check("moe_grad_clip", lib.moe_grad_clip(count, table.buffer_info()[0], max_norm, norm_ptr,
                                               s))
+
+
+# -------------------------------------------------------------------- a few tokens
+def few_workspace_size(s: MoeShape) -> int:
+    return int(load_library().moe_few_workspace_size(ctypes.byref(s)))
+
+
+def _few_common(ty: _Types, gpu: int, s: MoeShape, act: tuple, x, w_router, b_router):
+    return (_arg(x, "x", act, (s.T, s.d), gpu), _arg(w_router, "w_router", act, (s.E, s.d), gpu),
+            _optional(b_router, "b_router", ty.f32, (s.E,), gpu))
+
+
+def _few_outputs(ty: _Types, gpu: int, s: MoeShape, act: tuple, out, routed_counts,
+                 tokens_per_expert, drops, status, stream):
+    return (_arg(out, "out", act, (s.T, s.d), gpu),
+            _optional(routed_counts, "routed_counts", ty.i32, (s.E,), gpu),
+            _optional(tokens_per_expert, "tokens_per_expert", ty.i32, (s.E,), gpu),
+            _optional(drops, "drops", ty.i32, (s.k + 2,), gpu),
+            _optional(status, "status", ty.i32, (1,), gpu), _stream(stream))
+
+
+def layer_few(s: MoeShape, x, w_router, b_router, w_gate, w_up, w_down, workspace, out,
+              routed_counts=None, tokens_per_expert=None, drops=None, status=None,
+              stream=None) -> None:
+    """moe_layer_few: the whole layer for at most FEW_MAX_TOKENS tokens."""
+    ty, gpu = _begin()
+    if s.dtype not in ty.act:
+        raise ValueError(f"unknown dtype {s.dtype}")
+    E, d, F, act = s.E, s.d, s.F, ty.act[s.dtype]
+    ws, nbytes = _workspace_arg(workspace, gpu)
+    _check("moe_layer_few", load_library().moe_layer_few(
+        ctypes.byref(s), *_few_common(ty, gpu, s, act, x, w_router, b_router),
+        _arg(w_gate, "w_gate", act, (E, F, d), gpu), _arg(w_up, "w_up", act, (E, F, d), gpu),
+        _arg(w_down, "w_down", act, (E, d, F), gpu), ws, nbytes,
+        *_few_outputs(ty, gpu, s, act, out, routed_counts, tokens_per_expert, drops, status,
+                      stream)))
+
+
+def layer_few_fp8(s: MoeShape, scale_type: int, x, w_router, b_router, w_gate, w_up, w_down,
+                  workspace, out, routed_counts=None, tokens_per_expert=None, drops=None,
+                  status=None, stream=None) -> None:
+    """moe_layer_few_fp8; each expert weight is a pair (e4m3 values, scales)."""
+    ty, gpu = _begin()
+    E, d, F, act = s.E, s.d, s.F, ty.act[MOE_BF16]
+    wg = _fp8_weight(w_gate, "w_gate", ty, scale_type, E, F, d, gpu)
+    wu = _fp8_weight(w_up, "w_up", ty, scale_type, E, F, d, gpu)
+    wd = _fp8_weight(w_down, "w_down", ty, scale_type, E, d, F, gpu)
+    ws, nbytes = _workspace_arg(workspace, gpu)
+    _check("moe_layer_few_fp8", load_library().moe_layer_few_fp8(
+        ctypes.byref(s), scale_type, *_few_common(ty, gpu, s, act, x, w_router, b_router),
+        ctypes.byref(wg), ctypes.byref(wu), ctypes.byref(wd), ws, nbytes,
+        *_few_outputs(ty, gpu, s, act, out, routed_counts, tokens_per_expert, drops, status,
+                      stream)))
 
 
 # ------------------------------------------------------------------------------ calibration

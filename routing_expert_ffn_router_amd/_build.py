@@ -20,8 +20,8 @@ LIB = os.path.join(PKG, "libmoe.so")
 STAMP = os.path.join(OBJ, "libmoe.sha256")
 
 SOURCES = ["route.hip", "dispatch.hip", "expert_ffn.hip", "combine.hip", "noalloc.hip",
-           "quantize.hip", "fp8_gemm.hip", "grad_gemm.hip", "linear.hip", "linear_grad.hip", "clip.hip",
-           "moe_abi.cpp", "stats.cpp"]
+           "quantize.hip", "fp8_gemm.hip", "grad_gemm.hip", "few.hip", "linear.hip",
+           "linear_grad.hip", "clip.hip", "moe_abi.cpp", "stats.cpp"]
 # the MFMA-rate calibration for the measurement harness, in a library of its own
 CALIB_SOURCES = ["calib.hip"]
 CALIB_LIB = os.path.join(PKG, "libmoe_calib.so")

@@ -222,6 +222,31 @@ hipError_t launch_linear_grad(int dtype, int act, const void* dy, const void* z,
                               const int32_t* offsets, void* dz, float* db, float* partial,
                               int64_t R, int64_t E, int64_t N, hipStream_t s);
 
+// ---------------------------------------------------------------------------------------
+// the whole layer for a few tokens
+// ---------------------------------------------------------------------------------------
+constexpr int64_t kFewTokens = 16, kFewPairs = 512;
+struct FewArgs {
+  int dtype, scale_type;  // scale_type < 0: weights of dtype
+  const void* x;          // [T, d]
+  const void* w_router;   // [E, d]
+  const float* bias;      // [E], nullable: of the logits
+  const float* sel_bias;  // [E], nullable: of the selection alone
+  const void* w[3];       // gate, up [E, F, d], down [E, d, F]
+  const void* w_scale[3];
+  float* logits;          // [T, E]
+  void* h;                // [T k, F]
+  void* out;              // [T, d]
+  int32_t* routed;        // nullable, as the three below
+  int32_t* kept;
+  int32_t* drops;
+  int32_t* status;
+  int64_t T, d, E, k, F, C;
+  int n_groups, topk_groups;  // 1, 1: no limit
+  bool slot_major;
+};
+hipError_t launch_few(const FewArgs& a, hipStream_t s);
+
 struct GradTensor {  // moe_grad
   const void* grad;
   void* out;

@@ -967,3 +967,112 @@ int moe_grad_clip(int64_t count, const moe_grad* grads, float max_norm, const fl
 }
 
 }  // extern "C"
+
+// ------------------------------------------------------------------------------------------
+// the whole layer for a few tokens
+// ------------------------------------------------------------------------------------------
+namespace {
+
+int check_few_shape(const moe_shape* s) {
+  const int rc = check_shape(s);
+  if (rc != MOE_OK) return rc;
+  if (s->T > MOE_FEW_MAX_TOKENS || s->T * s->k > moe::kFewPairs) return MOE_ERR_UNSUPPORTED;
+  // h is read with 32-bit offsets
+  if (s->T * s->k * s->F * elt_bytes(s->dtype) >= ((int64_t)1 << 31) - 4096)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+struct FewLayout {
+  int64_t h, total;  // the logits come first
+};
+FewLayout few_layout(const moe_shape* s) {
+  FewLayout L;
+  L.h = align_up(s->T * s->E * 4);
+  L.total = L.h + align_up(s->T * s->k * s->F * elt_bytes(s->dtype));
+  if (L.total == 0) L.total = kAlign;  // a size of 0 says that the shape is invalid
+  return L;
+}
+
+// The launches over checked weights.
+int few_layer(const moe_shape* s, int scale_type, const void* x, const void* w_router,
+              const float* b_router, const void* const (&w)[3], const void* const (&w_scale)[3],
+              void* ws, size_t ws_bytes, void* out, int32_t* routed_counts,
+              int32_t* tokens_per_expert, int32_t* drops, int32_t* status, hipStream_t st) {
+  if (!w_router) return MOE_ERR_INVALID_ARG;
+  if (s->T > 0 && (!x || !out)) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(w_router) || !aligned16(out)) return MOE_ERR_ALIGNMENT;
+  const FewLayout L = few_layout(s);
+  if (!ws || (int64_t)ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+  if (((uintptr_t)ws & (kAlign - 1)) != 0) return MOE_ERR_ALIGNMENT;
+  const bool sel_only = (s->flags & MOE_FLAG_BIAS_SELECTION_ONLY) != 0;
+  moe::FewArgs a = {};
+  a.dtype = s->dtype;
+  a.scale_type = scale_type;
+  a.x = x;
+  a.w_router = w_router;
+  a.bias = sel_only ? nullptr : b_router;
+  a.sel_bias = sel_only ? b_router : nullptr;
+  for (int i = 0; i < 3; ++i) {
+    a.w[i] = w[i];
+    a.w_scale[i] = w_scale[i];
+  }
+  a.logits = static_cast<float*>(ws);
+  a.h = static_cast<char*>(ws) + L.h;
+  a.out = out;
+  a.routed = routed_counts;
+  a.kept = tokens_per_expert;
+  a.drops = drops;
+  a.status = status;
+  a.T = s->T;
+  a.d = s->d;
+  a.E = s->E;
+  a.k = s->k;
+  a.F = s->F;
+  a.C = eff_capacity(s);
+  a.n_groups = grouped(s) ? s->n_groups : 1;
+  a.topk_groups = grouped(s) ? s->topk_groups : 1;
+  a.slot_major = (s->flags & MOE_FLAG_SLOT_MAJOR) != 0;
+  return hip_status(moe::launch_few(a, st));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_few_workspace_size(const moe_shape* s) {
+  if (check_few_shape(s) != MOE_OK) return 0;
+  return (size_t)few_layout(s).total;
+}
+
+int moe_layer_few(const moe_shape* s, const void* x, const void* w_router, const float* b_router,
+                  const void* w_gate, const void* w_up, const void* w_down, void* ws,
+                  size_t ws_bytes, void* out, int32_t* routed_counts, int32_t* tokens_per_expert,
+                  int32_t* drops, int32_t* status, hipStream_t st) {
+  const int rc = check_few_shape(s);
+  if (rc != MOE_OK) return rc;
+  if (!w_gate || !w_up || !w_down) return MOE_ERR_INVALID_ARG;
+  if (!aligned16(w_gate) || !aligned16(w_up) || !aligned16(w_down)) return MOE_ERR_ALIGNMENT;
+  const void* const w[3] = {w_gate, w_up, w_down};
+  const void* const none[3] = {nullptr, nullptr, nullptr};
+  return few_layer(s, -1, x, w_router, b_router, w, none, ws, ws_bytes, out, routed_counts,
+                   tokens_per_expert, drops, status, st);
+}
+
+int moe_layer_few_fp8(const moe_shape* s, int scale_type, const void* x, const void* w_router,
+                      const float* b_router, const moe_fp8_tensor* w_gate,
+                      const moe_fp8_tensor* w_up, const moe_fp8_tensor* w_down, void* ws,
+                      size_t ws_bytes, void* out, int32_t* routed_counts,
+                      int32_t* tokens_per_expert, int32_t* drops, int32_t* status,
+                      hipStream_t st) {
+  int rc = check_few_shape(s);
+  if (rc != MOE_OK) return rc;
+  if (s->dtype != MOE_BF16 || !known_scale(scale_type)) return MOE_ERR_UNSUPPORTED;
+  if ((rc = check_fp8_weights(w_gate, w_up, w_down, scale_type)) != MOE_OK) return rc;
+  const void* const w[3] = {w_gate->q, w_up->q, w_down->q};
+  const void* const scale[3] = {w_gate->scale, w_up->scale, w_down->scale};
+  return few_layer(s, scale_type, x, w_router, b_router, w, scale, ws, ws_bytes, out,
+                   routed_counts, tokens_per_expert, drops, status, st);
+}
+
+}  // extern "C"
