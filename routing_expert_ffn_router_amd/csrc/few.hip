@@ -64,7 +64,10 @@ struct FewKern {
   int32_t* kept;
   int32_t* drops;
   int32_t* status;
-  int T, d, E, k, F, C, n_groups, topk_groups, slot_major;
+  float* partial;     // [chunks][T, d]
+  int32_t* counters;  // tickets and what is done, zero
+  int32_t* tile_done; // [column tiles], zero
+  int T, d, E, k, F, C, n_groups, topk_groups, slot_major, chunks, tickets, tp, lds;
 };
 
 // ---------------------------------------------------------------------------------------
@@ -75,7 +78,13 @@ struct FewKern {
 template <class T, int TT>
 __global__ void __launch_bounds__(256)
 few_logits_kernel(const T* __restrict__ x, const T* __restrict__ w, const float* __restrict__ b,
-                  float* __restrict__ logits, int tokens, int d, int E) {
+                  float* __restrict__ logits, int tokens, int d, int E, int32_t* __restrict__ zero,
+                  int zeros) {
+  if (blockIdx.x == 0 && blockIdx.y == 0)  // the experts' counters
+    for (int i = threadIdx.x; i < zeros; i += 256) zero[i] = 0;
+  x += (int64_t)blockIdx.y * TT * d;
+  logits += (int64_t)blockIdx.y * TT * E;
+  tokens -= blockIdx.y * TT;
   constexpr int V = 16 / sizeof(T);
   typedef T tx __attribute__((ext_vector_type(V)));
   __shared__ double part[4][TT];
@@ -83,18 +92,29 @@ few_logits_kernel(const T* __restrict__ x, const T* __restrict__ w, const float*
   double sum[TT];
 #pragma unroll
   for (int t = 0; t < TT; ++t) sum[t] = 0.0;
-  for (int i = tid * V; i < d; i += 256 * V) {
-    const tx wv = *reinterpret_cast<const tx*>(w + (int64_t)e * d + i);
-    tx xv[TT];
+  constexpr int U = TT == 1 ? 4 : 2;  // pieces under way
+  for (int i0 = tid * V; i0 < d; i0 += U * 256 * V) {
+    tx wv[U], xv[U][TT];
 #pragma unroll
-    for (int t = 0; t < TT; ++t)
-      if (t < tokens) xv[t] = *reinterpret_cast<const tx*>(x + (int64_t)t * d + i);
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * 256 * V;
+      if (i < d) {
+        wv[u] = *reinterpret_cast<const tx*>(w + (int64_t)e * d + i);
 #pragma unroll
-    for (int j = 0; j < V; ++j) {
-      const double wd = (double)Elt<T>::to_f32(wv[j]);
+        for (int t = 0; t < TT; ++t)
+          if (t < tokens) xv[u][t] = *reinterpret_cast<const tx*>(x + (int64_t)t * d + i);
+      }
+    }
 #pragma unroll
-      for (int t = 0; t < TT; ++t)
-        if (t < tokens) sum[t] = fma(wd, (double)Elt<T>::to_f32(xv[t][j]), sum[t]);
+    for (int u = 0; u < U; ++u) {
+      if (i0 + u * 256 * V >= d) break;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const double wd = (double)Elt<T>::to_f32(wv[u][j]);
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
+          if (t < tokens) sum[t] = fma(wd, (double)Elt<T>::to_f32(xv[u][t][j]), sum[t]);
+      }
     }
   }
 #pragma unroll
@@ -119,16 +139,14 @@ few_logits_kernel(const T* __restrict__ x, const T* __restrict__ w, const float*
 struct Routing {
   uint8_t* slot;     // [E][16]: 1 + the slot in which a token chose an expert and was kept, or 0
   float* gate_of;    // [T k]
-  float* gates;      // [active][16]: a token's gate, -1 where it did not choose the expert
   uint16_t* active;  // experts with tokens, in order
   int count;
 };
 
 __host__ __device__ inline int few_active_max(int T, int k, int E) { return min(E, T * k); }
-// slot, gate_of, gates, active and what their making needs (selected experts, group keys, scans)
+// slot, gate_of, active and the selected experts
 __host__ __device__ inline int few_routing_bytes(int T, int k, int E) {
-  const int a = few_active_max(T, k, E);
-  const int bytes = E * 16 + T * k * 4 + a * 64 + (a * 2 + 15) / 16 * 16 + (T * k * 2 + 15) / 16 * 16;
+  const int bytes = E * 16 + T * k * 4 + few_active_max(T, k, E) * 2 + T * k * 2;
   return (bytes + 15) / 16 * 16;
 }
 
@@ -156,10 +174,11 @@ __device__ inline uint32_t wave_max_u32(uint32_t v) {
 
 // A token's k experts, slot j on lane j: value descending, index ascending, as moe_route selects.
 // Returns whether a logit is not finite (such a logit is not selected).
+// V: logits a lane holds.
+template <int V>
 __device__ inline bool few_select(const float* __restrict__ row, const float* __restrict__ sel_bias,
                                   int E, int k, int n_groups, int topk_groups, uint32_t* group_key,
                                   int* slot_e) {
-  constexpr int V = 1024 / kWave;
   const int lane = lane_id();
   uint32_t key[V];
   bool bad = false;
@@ -189,6 +208,7 @@ __device__ inline bool few_select(const float* __restrict__ row, const float* __
     __builtin_amdgcn_wave_barrier();
     uint32_t mine = *(volatile uint32_t*)&group_key[lane];
     uint64_t chosen = 0;
+#pragma unroll 1
     for (int r = 0; r < topk_groups; ++r) {
       const uint32_t best = wave_max_u32(mine);
       if (best == 0) break;  // only tokens with non-finite logits get here
@@ -204,6 +224,7 @@ __device__ inline bool few_select(const float* __restrict__ row, const float* __
     }
   }
   int picked = 0;
+#pragma unroll 1
   for (int j = 0; j < k; ++j) {
     uint32_t best = 0;
 #pragma unroll
@@ -242,18 +263,21 @@ __device__ inline Routing few_routing(const FewKern& a, char* smem, bool report)
   Routing r;
   r.slot = reinterpret_cast<uint8_t*>(smem);
   r.gate_of = reinterpret_cast<float*>(smem + E * 16);
-  r.gates = r.gate_of + pairs;
-  r.active = reinterpret_cast<uint16_t*>(r.gates + most * 16);
-  uint16_t* sel = r.active + (most * 2 + 15) / 16 * 8;
+  r.active = reinterpret_cast<uint16_t*>(r.gate_of + pairs);
+  uint16_t* sel = r.active + most;
   u32x4* slot4 = reinterpret_cast<u32x4*>(smem);
   for (int e = tid; e < E; e += kThreads) slot4[e] = u32x4{0, 0, 0, 0};
   if (tid < 67) tally[tid] = 0;
   __syncthreads();
+#pragma unroll 1
   for (int t = wave; t < T; t += kWaves) {
     int e;
     const float* row = a.logits + (int64_t)t * E;
-    const bool bad = few_select(row, a.sel_bias, E, k, a.n_groups, a.topk_groups,
-                                group_key[wave], &e);
+    const bool bad =
+        E <= 256 ? few_select<4>(row, a.sel_bias, E, k, a.n_groups, a.topk_groups,
+                                 group_key[wave], &e)
+                 : few_select<16>(row, a.sel_bias, E, k, a.n_groups, a.topk_groups,
+                                  group_key[wave], &e);
     // gates: softmax over the selection
     const float l = lane < k ? row[e] : -__builtin_huge_valf();
     float m = l;
@@ -274,6 +298,7 @@ __device__ inline Routing few_routing(const FewKern& a, char* smem, bool report)
   if (report && a.routed) {
     for (int e = tid; e < E; e += kThreads) {
       int n = 0;
+#pragma unroll 1
       for (int t = 0; t < T; ++t) n += r.slot[e * 16 + t] != 0;
       a.routed[e] = n;
     }
@@ -284,6 +309,7 @@ __device__ inline Routing few_routing(const FewKern& a, char* smem, bool report)
     if (tid < pairs) {
       int before = 0;
       const int e = sel[tid];
+#pragma unroll 1
       for (int o = 0; o < T; ++o) {
         const int s = r.slot[e * 16 + o];
         if (s && (a.slot_major ? s - 1 < j || (s - 1 == j && o < t) : o < t)) ++before;
@@ -300,6 +326,7 @@ __device__ inline Routing few_routing(const FewKern& a, char* smem, bool report)
     __syncthreads();
     if (report && tid < T) {
       bool none = true;
+#pragma unroll 1
       for (int i = 0; i < k; ++i) none = none && sel[tid * k + i] == 0xffff;
       if (none) atomicAdd(&tally[k + 1], 1);
     }
@@ -309,6 +336,7 @@ __device__ inline Routing few_routing(const FewKern& a, char* smem, bool report)
     if (a.kept)
       for (int e = tid; e < E; e += kThreads) {
         int n = 0;
+#pragma unroll 1
         for (int t = 0; t < T; ++t) n += r.slot[e * 16 + t] != 0;
         a.kept[e] = n;
       }
@@ -330,11 +358,6 @@ __device__ inline Routing few_routing(const FewKern& a, char* smem, bool report)
     count += total;
   }
   __syncthreads();
-  for (int i = tid; i < count * kTokens; i += kThreads) {
-    const int t = i & 15, s = r.slot[r.active[i >> 4] * 16 + t];
-    r.gates[i] = s ? r.gate_of[t * k + s - 1] : -1.f;
-  }
-  __syncthreads();
   r.count = __builtin_amdgcn_readfirstlane(count);
   return r;
 }
@@ -342,8 +365,6 @@ __device__ inline Routing few_routing(const FewKern& a, char* smem, bool report)
 // ---------------------------------------------------------------------------------------
 // the experts
 // ---------------------------------------------------------------------------------------
-typedef bf16 bf16x2 __attribute__((ext_vector_type(2)));
-
 // Eight e4m3 values as bf16 (exact).
 __device__ inline u32x4 e4m3_to_bf16(uint32_t lo, uint32_t hi) {
   u32x4 r;
@@ -359,249 +380,487 @@ __device__ inline float e8m0_value(uint32_t v) {
   return __uint_as_float(v == 0 ? 0x00400000u : v == 255 ? 0x7fc00000u : v << 23);
 }
 
-// TP: tokens' rows that are loaded (8 or 16); RT: MFMA tiles of 16 weight rows an item has; G: units
-// of a group.
-template <class W, int TP_, int RT_, int G_>
-struct FewTile {
-  static constexpr int TP = TP_, RT = RT_, G = G_;
-  static constexpr int kWLoads = 2 * RT;                     // of 1024 bytes, per unit
-  static constexpr int kXLoads = TP * W::kXBytes / 1024;
-  static constexpr int kSlot = RT * 2048 + TP * W::kXBytes;  // a wave's LDS
-  static constexpr int kSums = 2 * kWaves * RT * 1024;       // two items' sums
-  static constexpr int kLds = kWaves * kSlot + kSums;
-};
+// Waits until `count` tickets are done, or long enough that something must be wrong with the
+// workspace (another call's, say): then the results are unspecified, but the kernel ends.
+__device__ inline void wait_for(const int32_t* done, int count) {
+#pragma unroll 1
+  for (int i = 0; i < (1 << 20); ++i) {
+    if (__hip_atomic_load(done, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) >= count) break;
+    __builtin_amdgcn_s_sleep(2);
+  }
+}
 
-template <class W, class P, bool DOWN>
-__global__ void __launch_bounds__(kThreads) few_kernel(const FewKern a) {
-  extern __shared__ __attribute__((aligned(1024))) char smem_dyn[];
+// LDS accesses that the compiler does not order behind the direct loads under way: it would wait for
+// all of those before each.  Each waits for itself.
+__device__ inline uint32_t lds_address(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) char*)p;
+}
+__device__ inline uint32_t lds_u8(uint32_t at) {
+  uint32_t v;
+  asm volatile("ds_read_u8 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(v) : "v"(at) : "memory");
+  return v;
+}
+__device__ inline uint32_t lds_u16(uint32_t at) {
+  uint32_t v;
+  asm volatile("ds_read_u16 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(v) : "v"(at) : "memory");
+  return v;
+}
+__device__ inline uint32_t lds_u32(uint32_t at) {
+  uint32_t v;
+  asm volatile("ds_read_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(v) : "v"(at) : "memory");
+  return v;
+}
+__device__ inline float lds_f32(uint32_t at) { return __uint_as_float(lds_u32(at)); }
+__device__ inline void lds_write32(uint32_t at, uint32_t v) {
+  asm volatile("ds_write_b32 %0, %1" ::"v"(at), "v"(v) : "memory");
+}
+__device__ inline void lds_write(uint32_t at, const f32x4& v) {
+  asm volatile("ds_write_b128 %0, %1" ::"v"(at), "v"(v) : "memory");
+}
+// N pieces
+template <int N>
+__device__ inline void lds_read(u32x4 (&v)[N], const uint32_t (&at)[N]) {
+  static_assert(N == 2 || N == 4 || N == 6, "pieces");
+  if constexpr (N == 2)
+    asm volatile(
+        "ds_read_b128 %0, %2\n\tds_read_b128 %1, %3\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1])
+        : "v"(at[0]), "v"(at[1])
+        : "memory");
+  if constexpr (N == 4)
+    asm volatile(
+        "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_b128 %2, %6\n\t"
+        "ds_read_b128 %3, %7\n\ts_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3])
+        : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3])
+        : "memory");
+  if constexpr (N == 6)
+    asm volatile(
+        "ds_read_b128 %0, %6\n\tds_read_b128 %1, %7\n\tds_read_b128 %2, %8\n\t"
+        "ds_read_b128 %3, %9\n\tds_read_b128 %4, %10\n\tds_read_b128 %5, %11\n\t"
+        "s_waitcnt lgkmcnt(0)"
+        : "=&v"(v[0]), "=&v"(v[1]), "=&v"(v[2]), "=&v"(v[3]), "=&v"(v[4]), "=&v"(v[5])
+        : "v"(at[0]), "v"(at[1]), "v"(at[2]), "v"(at[3]), "v"(at[4]), "v"(at[5])
+        : "memory");
+}
+template <int N>
+__device__ inline void wait_loads() {
+  static_assert(N >= 0 && N < 64, "vmcnt immediate");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
+// How a block divides an item.  ALONG the reduction: every wave takes its part of the units of 16
+// weight rows, with a ring of its own for weights and rows; ACROSS the columns (more than eight
+// tokens, whose rows would be half of all loads): every wave takes 16 weight rows of its own through
+// all units, and the block shares the rows.
+constexpr bool kAlong = false, kAcross = true;
+
+// LDS of one stage of the ring, of one wave (along) or of the block (across): weight rows of one unit,
+// tp tokens' rows, scales (a word for gate or down and one for up).
+template <class W, bool ACROSS>
+__host__ __device__ constexpr int stage_bytes(int tp) {
+  return ACROSS ? kWaves * (2048 + (W::kScale ? 16 : 0)) + tp * W::kXBytes
+                : 2048 + (W::kScale ? 16 : 0) + tp * W::kXBytes;
+}
+template <class W, bool ACROSS>
+__host__ __device__ constexpr int ring_bytes(int tp, int stages) {
+  return (ACROSS ? 1 : kWaves) * stages * stage_bytes<W, ACROSS>(tp);
+}
+constexpr int kSumBytes = 2 * kWaves * 1024;  // along: two items' sums
+// columns of an item: gate and up rows of the same columns make up the sixteen
+__host__ __device__ constexpr int few_columns(bool down, bool across) {
+  return (down ? 16 : 8) * (across ? kWaves : 1);
+}
+
+// Items first, first + stride, ... of gate/up or of down.  ready(): called once, when the first
+// weights are under way and before h is read.
+template <class W, int S, bool ACROSS, bool DOWN, class Ready>
+__device__ __attribute__((always_inline)) inline void few_items(const FewKern& a, const Routing& r,
+                                                                char* smem, int items, int first,
+                                                                int stride, int chunks,
+                                                                Ready&& ready) {
   typedef typename W::X X;
-  constexpr int RT = P::RT, G = P::G, NW = P::kWLoads, NX = P::kXLoads, ES = W::kScale;
-  constexpr int kScales = !W::kScale ? 0 : DOWN || RT == 1 ? 1 : 2;
-  const Routing r = few_routing(a, smem_dyn + P::kLds, !DOWN && blockIdx.x == 0);
+  typedef X x4 __attribute__((ext_vector_type(4)));
+  constexpr int ES = W::kScale, NX = W::kXBytes / 128;
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int c = lane & 15, g = lane >> 4;
-  lds_char* slot = (lds_char*)smem_dyn + wave * P::kSlot;
-  lds_char* sums = (lds_char*)smem_dyn + kWaves * P::kSlot;
+  const uint32_t slot_tab = lds_address(r.slot), gate_tab = lds_address(r.gate_of),
+                 active_tab = lds_address(r.active);
 
-  // Items and, of each, this wave's units [u0, u1): the reduction's units (down: of every chosen
-  // expert, one behind the other).
-  const int K = DOWN ? a.F : a.d, N = DOWN ? a.d : a.F;
-  constexpr int kCols = DOWN ? 16 * RT : 8 * RT;  // columns of an item
+  const int K = DOWN ? a.F : a.d, N = DOWN ? a.d : a.F, tp = a.tp;
+  constexpr int kCols = few_columns(DOWN, ACROSS);
   const int per_k = K * W::kElt / 128, tiles = N / kCols;
-  const int items = DOWN ? tiles : r.count * tiles;
   const int units = DOWN ? r.count * per_k : per_k;
-  const int u0 = (int)((int64_t)wave * units / kWaves), u1 = (int)((int64_t)(wave + 1) * units / kWaves);
-  const uint32_t pitch = (uint32_t)K * W::kElt;
-  const uint32_t vw = (uint32_t)(lane >> 3) * pitch + (uint32_t)(lane & 7) * 16;
-  const uint32_t x_pitch = (uint32_t)K * (uint32_t)sizeof(X);
-  const auto rx = bounded_rsrc(uniform_u64(DOWN ? a.h : a.x),
-                               (int64_t)(DOWN ? a.T * a.k : a.T) * x_pitch);
-  constexpr uint32_t kNone = 0x7fffff00u;  // past the resource's end: loads as zeros
-  // x load i: 128-byte part i * 8 / TP of the unit's row, tokens (i * 8) % TP + L / 8
-  auto x_token = [&](int i) { return (i * 8) % P::TP + (lane >> 3); };
+  const uint32_t pitch = (uint32_t)K * W::kElt, x_pitch = (uint32_t)K * (uint32_t)sizeof(X);
   const int64_t matrix = (int64_t)N * pitch;
+  constexpr uint32_t kNone = 0x80000000u;  // past a resource's end: loads as zeros
 
-  struct Group {
-    u32x4 w[G][NW], x[G][NX];
-    uint32_t s[G][kScales ? kScales : 1];
-  };
-  // unit u of item q: where its expert stands in the list, and the unit of the row
-  struct Unit {
-    int at, k;
-  };
-  auto unit_of = [&](int q, int u) {
-    if constexpr (DOWN) return Unit{u / per_k, u % per_k};
-    return Unit{q / tiles, u};
-  };
-  auto load = [&](Group& o, int q, int u) {
-    const int col0 = (DOWN ? q : q % tiles) * kCols;
+  // A stage: this wave's weight rows, then (along: its, across: the block's) tokens' rows and scales.
+  // Load i brings eight rows of 128 bytes; the 16-byte piece p of row n lies in slot p ^ ((n >> 1) & 7),
+  // which keeps a fragment's reads free of bank conflicts.
+  const int stage = stage_bytes<W, ACROSS>(tp);
+  lds_char* const ring = (lds_char*)smem + (ACROSS ? 0 : wave * S * stage);
+  const int w_at = ACROSS ? wave * 2048 : 0, x_at = ACROSS ? kWaves * 2048 : 2048;
+  const int s_at = x_at + tp * W::kXBytes + (ACROSS ? wave * 16 : 0);
+  const uint32_t ring_lds = lds_address(smem) + (ACROSS ? 0 : wave * S * stage);
+  uint32_t vw[2];
 #pragma unroll
-    for (int i = 0; i < G; ++i) {
-      if (u + i >= u1) break;
-      const Unit v = unit_of(q, u + i);
-      const int e = __builtin_amdgcn_readfirstlane((int)r.active[v.at]);
-      const int64_t first = (int64_t)e * matrix + (int64_t)col0 * pitch;
-      const auto r0 = buffer_rsrc(uniform_u64((DOWN ? a.down.q : a.gate.q) + first));
-      const auto r1 = buffer_rsrc(uniform_u64((DOWN ? a.down.q : a.up.q) + first));
+  for (int i = 0; i < 2; ++i)
+    vw[i] = (uint32_t)(lane >> 3) * pitch + (uint32_t)(((lane & 7) ^ (4 * i + (lane >> 4))) * 16);
+  // the tokens' rows in parts of 128 bytes, a load each: along, the wave's own; across, an eighth
+  const int x_lanes = ACROSS ? tp : tp * 8, x_piece = (ACROSS ? wave * tp : 0) + lane;
+  const int x_row = x_piece >> 3;
+  const uint32_t x_col = (uint32_t)(((x_piece & 7) ^ ((x_row >> 1) & 7)) * 16);
+  const int x_dst = x_at + (ACROSS ? wave * tp * 16 : 0);
+  // fragments: weights' row c, pieces g and g + 4; the same values of token c's row
+  constexpr int kFrags = 2 + 2 * NX;
+  uint32_t frag[kFrags];
+  {
+    auto piece = [&](int row, int p) { return (uint32_t)(row * 128 + ((p ^ ((row >> 1) & 7)) << 4)); };
+    const int xr = c & (tp - 1);
 #pragma unroll
-      for (int n = 0; n < NW; ++n) {
-        const bool second = !DOWN && n >= RT;  // the up rows
-        const uint32_t row = (uint32_t)(second ? n - RT : n) * 8u * pitch;
-        o.w[i][n] = __builtin_bit_cast(
-            u32x4, __builtin_amdgcn_raw_buffer_load_b128(second ? r1 : r0, vw,
-                                                         row + (uint32_t)v.k * 128u, 2));
-      }
+    for (int ks = 0; ks < 2; ++ks) {
+      frag[ks] = ring_lds + w_at + piece(c, ks * 4 + g);
+      if constexpr (NX == 1)
+        frag[2 + ks] = ring_lds + x_at + piece(xr, ks * 4 + g);
+      else
 #pragma unroll
-      for (int n = 0; n < NX; ++n) {
-        const int t = x_token(n);
-        uint32_t off = kNone;
-        if constexpr (DOWN) {
-          const int s = r.slot[e * 16 + t];
-          if (s) off = (uint32_t)(t * a.k + s - 1) * x_pitch;
-        } else {
-          if (t < a.T) off = (uint32_t)t * x_pitch;
-        }
-        if (off != kNone) off += (uint32_t)(lane & 7) * 16 + (uint32_t)(n * 8 / P::TP) * 128u;
-        o.x[i][n] = __builtin_bit_cast(
-            u32x4, __builtin_amdgcn_raw_buffer_load_b128(rx, off, (uint32_t)v.k * W::kXBytes, 0));
-      }
-      if constexpr (kScales > 0) {
-        const int kb = K / 128, row = (int)((int64_t)col0 / 128);
-        const int64_t at = ((int64_t)e * (N / 128) + row) * kb + v.k;
-        auto scale = [&](const char* p) -> uint32_t {
-          if constexpr (ES == 4) return *reinterpret_cast<const uint32_t*>(p + at * 4);
-          return *reinterpret_cast<const uint8_t*>(p + at);
-        };
-        if constexpr (DOWN) {
-          o.s[i][0] = scale(a.down.scale);
-        } else if constexpr (RT == 1) {
-          o.s[i][0] = scale(g < 2 ? a.gate.scale : a.up.scale);
-        } else {
-          o.s[i][0] = scale(a.gate.scale);
-          o.s[i][1] = scale(a.up.scale);
-        }
-      }
+        for (int h = 0; h < 2; ++h)
+          frag[2 + 2 * ks + h] = ring_lds + x_at + ks * tp * 128 + piece(xr, 2 * g + h);
     }
+  }
+
+  // Along, each wave takes every eighth unit: together they read a kilobyte of each row at a time.
+  constexpr int kStep = ACROSS ? 1 : kWaves;
+  auto item_units = [&](int q, int* u0) {  // how many this wave has, and the first
+    int from = 0, len = units;
+    if constexpr (DOWN) {  // (at most 2^24 units and 32 chunks)
+      const uint32_t n = (uint32_t)q / (uint32_t)tiles;
+      from = (int)(n * (uint32_t)units / (uint32_t)chunks);
+      len = (int)((n + 1) * (uint32_t)units / (uint32_t)chunks) - from;
+    }
+    if constexpr (!ACROSS) {
+      from += wave;
+      len = max(len - wave + kWaves - 1, 0) / kWaves;
+    }
+    *u0 = from;
+    return len;
   };
 
-  f32x4 acc[RT];
-#pragma unroll
-  for (int i = 0; i < RT; ++i) acc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto lds_at = [&](int row, int piece) { return row * 128 + ((piece ^ ((row >> 1) & 7)) << 4); };
-  lds_char* xs = slot + RT * 2048;
-  auto multiply = [&](const Group& o, int q, int u) {
-#pragma unroll
-    for (int i = 0; i < G; ++i) {
-      if (u + i >= u1) break;
-#pragma unroll
-      for (int n = 0; n < NW; ++n)
-        *reinterpret_cast<lds_u32x4*>(slot + lds_at(n * 8 + (lane >> 3), lane & 7)) = o.w[i][n];
-#pragma unroll
-      for (int n = 0; n < NX; ++n)  // parts of TP rows of 128 bytes
-        *reinterpret_cast<lds_u32x4*>(xs + (n * 8 / P::TP) * (P::TP * 128) +
-                                      lds_at(x_token(n), lane & 7)) = o.x[i][n];
-      __builtin_amdgcn_wave_barrier();
-      f32x4 p[RT];
-#pragma unroll
-      for (int t = 0; t < RT; ++t) p[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-      const int xr = c & (P::TP - 1);
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        u32x4 w[RT];
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
-          w[t] = *reinterpret_cast<const lds_u32x4*>(slot + lds_at(t * 16 + c, ks * 4 + g));
-        if constexpr (W::kElt == 1) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const u32x4 x = *reinterpret_cast<const lds_u32x4*>(xs + ks * (P::TP * 128) +
-                                                                lds_at(xr, 2 * g + h));
-#pragma unroll
-            for (int t = 0; t < RT; ++t)
-              mma_chunk(p[t], e4m3_to_bf16(w[t][2 * h], w[t][2 * h + 1]), x, bf16());
-          }
-        } else {
-          const u32x4 x = *reinterpret_cast<const lds_u32x4*>(xs + lds_at(xr, ks * 4 + g));
-#pragma unroll
-          for (int t = 0; t < RT; ++t) mma_chunk(p[t], w[t], x, X());
-        }
-      }
-      __builtin_amdgcn_wave_barrier();
-      float f[RT];
-#pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        f[t] = 1.f;
-        if constexpr (kScales > 0) {
-          const uint32_t s = o.s[i][kScales == 2 ? t : 0];
-          f[t] = ES == 4 ? __uint_as_float(s) : e8m0_value(s);
-        }
-      }
-      if constexpr (DOWN) {
-        const float gate = r.gates[unit_of(q, u + i).at * kTokens + c];
-        // a token that did not choose the expert takes nothing of it, be it infinite or NaN
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          const float v = f[t] * gate;
-#pragma unroll
-          for (int b = 0; b < 4; ++b) acc[t][b] = gate < 0.f ? acc[t][b] : fmaf(p[t][b], v, acc[t][b]);
-        }
-      } else {
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
-#pragma unroll
-          for (int b = 0; b < 4; ++b) acc[t][b] = fmaf(p[t][b], f[t], acc[t][b]);
-      }
-    }
+  // The unit that is loaded next: of item q, `left` units to go, unit k of the rows of the at-th
+  // expert, to stage `slot`.  Past the last item there is none: its loads go nowhere and give zeros,
+  // so that every step issues as many loads and the waits count a constant.
+  struct Load {
+    int q, left, k, at, slot;
   };
-
-  // The item's end: this wave's sums to LDS, and one wave adds and finishes.
-  auto finish = [&](int q, int nth) {
-    lds_char* buf = sums + (nth & 1) * (kWaves * RT * 1024);
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      *reinterpret_cast<lds_f32x4*>(buf + (wave * RT + t) * 1024 + lane * 16) = acc[t];
-      acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  const Load start = {first - stride, 0, 0, 0, 0};
+  Load l = start;
+  uint64_t base0 = 0, base1 = 0;
+  int64_t scale_at = 0;
+  uint32_t vx = kNone;
+  auto find = [&] {  // the expert's matrices and rows, of another item or expert
+    while (l.left == 0 && l.q < items) {
+      l.q += stride;
+      if (l.q >= items) return;
+      int u0;
+      l.left = item_units(l.q, &u0);
+      l.at = DOWN ? (int)((uint32_t)u0 / (uint32_t)per_k) : (int)((uint32_t)l.q / (uint32_t)tiles);
+      l.k = DOWN ? u0 - l.at * per_k : u0;
     }
-    // (the loads under way stay under way)
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    if (wave != (nth & (kWaves - 1))) return;
-    f32x4 v[RT];
-#pragma unroll
-    for (int t = 0; t < RT; ++t) {
-      v[t] = *reinterpret_cast<const lds_f32x4*>(buf + t * 1024 + lane * 16);
-#pragma unroll
-      for (int w = 1; w < kWaves; ++w) {
-        const f32x4 o = *reinterpret_cast<const lds_f32x4*>(buf + (w * RT + t) * 1024 + lane * 16);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) v[t][b] += o[b];
-      }
+    while (DOWN && l.k >= per_k) {
+      l.k -= per_k;
+      ++l.at;
     }
-    // lane (c, g): token c, weight rows 4 g .. 4 g + 3 of each tile
-    typedef X x4 __attribute__((ext_vector_type(4)));
+    const int e = __builtin_amdgcn_readfirstlane((int)lds_u16(active_tab + l.at * 2));
+    const int col0 = (int)((uint32_t)l.q % (uint32_t)tiles) * kCols;
+    const int64_t to = (int64_t)e * matrix +
+                       (int64_t)(col0 + (ACROSS ? wave * few_columns(DOWN, false) : 0)) * pitch;
+    base0 = uniform_u64((DOWN ? a.down.q : a.gate.q) + to);
+    if constexpr (!DOWN) base1 = uniform_u64(a.up.q + to);
+    if constexpr (ES > 0) scale_at = ((int64_t)e * (N / 128) + col0 / 128) * (K / 128);
     if constexpr (DOWN) {
-      if (c < a.T) {
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
-          *reinterpret_cast<x4*>(static_cast<X*>(a.out) + (int64_t)c * N + q * kCols + t * 16 +
-                                 4 * g) =
-              x4{Elt<X>::from_f32(v[t][0]), Elt<X>::from_f32(v[t][1]), Elt<X>::from_f32(v[t][2]),
-                 Elt<X>::from_f32(v[t][3])};
-      }
+      const int s = (int)lds_u8(slot_tab + e * 16 + min(x_row, kTokens - 1));
+      vx = s ? (uint32_t)(x_row * a.k + s - 1) * x_pitch + x_col : kNone;
     } else {
-      const int e = r.active[q / tiles], s = c < a.T ? r.slot[e * 16 + c] : 0;
+      vx = x_row < a.T ? (uint32_t)x_row * x_pitch + x_col : kNone;
+    }
+  };
+  auto load_w = [&] {
+    const int64_t most = l.q < items ? 0x7fffffff : 0;
+    const uint32_t koff = (uint32_t)l.k * 128u;
+    lds_char* to = ring + l.slot + w_at;
+    // each line is read once: past the caches
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(bounded_rsrc(base0, most), to, 16, vw[0], koff, 0, 2);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(bounded_rsrc(DOWN ? base0 : base1, most), to + 1024, 16,
+                                             vw[1], DOWN ? koff + 8u * pitch : koff, 0, 2);
+  };
+  const int64_t x_bytes = (int64_t)(DOWN ? a.T * a.k : a.T) * x_pitch;
+  const uint64_t x_base = uniform_u64(DOWN ? a.h : a.x);
+  auto load_x = [&] {
+    if (lane < x_lanes) {
+      const auto rx = bounded_rsrc(x_base, l.q < items ? x_bytes : 0);
+#pragma unroll
+      for (int n = 0; n < NX; ++n)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, ring + l.slot + x_dst + n * tp * 128, 16, vx,
+                                                 (uint32_t)l.k * W::kXBytes + n * 128u, 0, 0);
+    }
+    if constexpr (ES > 0) {
+      if (lane < 2) {  // lane 0 gate or down, lane 1 up
+        const char* p = DOWN ? a.down.scale : lane == 0 ? a.gate.scale : a.up.scale;
+        p += (l.q < items ? scale_at + l.k : 0) * ES;
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) char*)p,
+                                         ring + l.slot + s_at, ES, 0, 0);
+      }
+    }
+  };
+  constexpr int kLoads = 2 + NX + (ES ? 1 : 0);
+
+  // The item's end.  Along: this wave's sums to LDS, and one wave, another one each time, adds them and
+  // finishes.  lane (c, g): token c, weight rows 4 g .. 4 g + 3.
+  f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
+  const uint32_t sums = lds_address(smem) + (ACROSS ? 1 : kWaves) * S * stage;
+  auto finish = [&](int q, int nth) {
+    f32x4 v = acc;
+    acc = f32x4{0.f, 0.f, 0.f, 0.f};
+    if constexpr (!ACROSS) {
+      const uint32_t buf = sums + (nth & 1) * (kWaves * 1024) + lane * 16;
+      lds_write(buf + wave * 1024, v);
+      // (the loads under way stay under way)
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      if (wave != (nth & (kWaves - 1))) return;
+      v = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int w = 0; w < kWaves; w += 4) {
+        u32x4 o[4];
+        const uint32_t at[4] = {buf + w * 1024, buf + (w + 1) * 1024, buf + (w + 2) * 1024,
+                                buf + (w + 3) * 1024};
+        lds_read<4>(o, at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int b = 0; b < 4; ++b) v[b] += __uint_as_float(o[i][b]);
+      }
+    }
+    const int n = (int)((uint32_t)q / (uint32_t)tiles), tile = q - n * tiles;
+    if constexpr (DOWN) {
+      const int col = tile * kCols + (ACROSS ? wave * 16 : 0) + 4 * g;
+      if (chunks > 1) {
+        // the chunk's sums to the workspace; the columns' last chunk adds them in order.  (One wave's
+        // release and acquire are the block's, as at the kernel's end.)
+        float* at = a.partial + (int64_t)c * N + col;
+        const int64_t chunk = (int64_t)a.T * N;
+        if (c < a.T) *reinterpret_cast<f32x4*>(at + n * chunk) = v;
+        auto arrive = [&] {
+          int before = 0;
+          __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+          if (lane == 0)
+            before = __hip_atomic_fetch_add(a.tile_done + tile, 1, __ATOMIC_RELAXED,
+                                            __HIP_MEMORY_SCOPE_AGENT);
+          before = __builtin_amdgcn_readfirstlane(before);
+          if (before == chunks - 1) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+          return before;
+        };
+        int before;
+        if constexpr (ACROSS) {
+          // (the ring's loads end with the stores: an item is the block's last, or nearly)
+          asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+          if (wave == 0) lds_write32(sums, (uint32_t)arrive());
+          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+          before = (int)lds_u32(sums);
+        } else {
+          before = arrive();
+        }
+        if (__builtin_amdgcn_readfirstlane(before) != chunks - 1) return;
+        if (c < a.T) {
+          v = *reinterpret_cast<const f32x4*>(at);
+#pragma unroll 4
+          for (int i = 1; i < chunks; ++i) {
+            const f32x4 o = *reinterpret_cast<const f32x4*>(at + i * chunk);
+#pragma unroll
+            for (int b = 0; b < 4; ++b) v[b] += o[b];
+          }
+        }
+      }
+      if (c < a.T)
+        *reinterpret_cast<x4*>(static_cast<X*>(a.out) + (int64_t)c * N + col) =
+            x4{Elt<X>::from_f32(v[0]), Elt<X>::from_f32(v[1]), Elt<X>::from_f32(v[2]),
+               Elt<X>::from_f32(v[3])};
+    } else {
+      const int e = __builtin_amdgcn_readfirstlane((int)lds_u16(active_tab + n * 2));
+      const int s = (int)lds_u8(slot_tab + e * 16 + c);
       x4 o;
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        // one tile: gate rows 0..7, up rows 8..15, on the lane 32 further
-        const float up = RT == 1 ? __shfl_xor(v[0][b], 32, kWave) : v[RT - 1][b];
-        o[b] = Elt<X>::from_f32(silu_f32(v[0][b]) * up);
-      }
-      if (s && (RT == 2 || g < 2))
+      for (int b = 0; b < 4; ++b)  // gate rows 0..7, up rows 8..15 on the lane 32 further
+        o[b] = Elt<X>::from_f32(silu_f32(v[b]) * __shfl_xor(v[b], 32, kWave));
+      if (s && g < 2)
         *reinterpret_cast<x4*>(static_cast<X*>(a.h) + (int64_t)(c * a.k + s - 1) * N +
-                               (q % tiles) * kCols + 4 * g) = o;
+                               tile * kCols + (ACROSS ? wave * 8 : 0) + 4 * g) = o;
     }
   };
 
-  Group ga, gb;
-  int q = blockIdx.x, u = u0, nth = 0;
-  if (q >= items) return;
-  load(ga, q, u);
+  // The unit that is multiplied: of item q, `todo` to go; down: unit k of the at-th expert.
+  int q = first, nth = 0, todo = 0, k = 0, at = 0;
+  uint32_t slot = 0;
+  float gate = 1.f;
+  bool begun = false;
+  // One loop, so that there is one copy of everything: a block runs much of its code once, and what
+  // it has to fetch it waits for.  First the S - 1 first units' weights, then, h being ready, their
+  // rows, then a step for each unit.
+  enum { kWeights, kRows, kSteps };
+  int phase = kWeights, count = S - 1;
+  // loads behind stage u's at step u: those of S - 1 (across: S - 2) stages; at first fewer, since
+  // the first stages' rows follow all of their weights
+  constexpr int kBehind = ACROSS ? S - 2 : S - 1;
+#pragma unroll 1
   for (;;) {
-    // (both halves alike: the group that is multiplied, and the next one under way)
-    auto half = [&](Group& now, Group& next) -> bool {
-      const bool last = u + G >= u1;
-      const int nq = last ? q + (int)gridDim.x : q, nu = last ? u0 : u + G;
-      if (nq < items) load(next, nq, nu);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(now, q, u);
-      if (last) finish(q, nth++);
-      q = nq;
-      u = nu;
-      return nq < items;
-    };
-    if (!half(ga, gb)) break;
-    if (!half(gb, ga)) break;
+    if (phase == kSteps) {
+#pragma unroll 1
+      while (todo == 0) {
+        if (begun) {
+          finish(q, nth++);
+          q += stride;
+        }
+        begun = true;
+        if (q >= items) break;
+        int u0;
+        todo = item_units(q, &u0);
+        if constexpr (DOWN) {
+          at = (int)((uint32_t)u0 / (uint32_t)per_k) - 1;
+          k = u0 - at * per_k;  // (as if behind the expert before)
+        }
+      }
+      if (q >= items) break;
+      if constexpr (DOWN) {
+        if (k >= per_k) {
+          while (k >= per_k) {
+            k -= per_k;
+            ++at;
+          }
+          const int e = __builtin_amdgcn_readfirstlane((int)lds_u16(active_tab + at * 2));
+          const int s = (int)lds_u8(slot_tab + e * 16 + c);
+          // a token that did not choose the expert takes nothing of it, be it infinite or NaN
+          gate = s ? lds_f32(gate_tab + (s ? c * a.k + s - 1 : 0) * 4) : -1.f;
+        }
+      }
+      if constexpr (ACROSS) {
+        if (count > 0)
+          wait_loads<(S - 2) * (kLoads - 2)>();
+        else
+          wait_loads<kBehind * kLoads>();
+        // everyone's part has landed, and everyone is done with the stage that is loaded again
+        asm volatile("s_barrier" ::: "memory");
+      }
+    }
+    if (l.q < items && (l.left == 0 || (DOWN && l.k >= per_k))) find();
+    if (phase != kRows) load_w();
+    if (phase != kWeights) load_x();
+    l.slot = l.slot == (S - 1) * stage ? 0 : l.slot + stage;
+    if (l.q < items) {
+      l.k += kStep;
+      --l.left;
+    }
+    if (phase != kSteps) {
+      if (--count == 0) {
+        count = S - 1;
+        if (phase++ == kWeights) {
+          l = start;
+          ready();
+        }
+      }
+      continue;
+    }
+    if constexpr (!ACROSS) {
+      if (count > 0)
+        wait_loads<(S - 2) * (kLoads - 2) + kLoads>();
+      else
+        wait_loads<kBehind * kLoads>();
+    }
+    if (count > 0) --count;
+    u32x4 f[kFrags];
+    uint32_t from[kFrags];
+#pragma unroll
+    for (int i = 0; i < kFrags; ++i) from[i] = frag[i] + slot;
+    lds_read<kFrags>(f, from);
+    f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+      if constexpr (W::kElt == 1) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          mma_chunk(v, e4m3_to_bf16(f[ks][2 * h], f[ks][2 * h + 1]), f[2 + 2 * ks + h], bf16());
+      } else {
+        mma_chunk(v, f[ks], f[2 + ks], X());
+      }
+    }
+    float factor = gate;
+    if constexpr (ES > 0) {
+      const float s = lds_f32(ring_lds + slot + s_at + (DOWN || g < 2 ? 0 : 4));
+      factor *= ES == 4 ? s : e8m0_value(__float_as_uint(s) & 255u);
+    }
+#pragma unroll
+    for (int b = 0; b < 4; ++b) acc[b] = gate < 0.f ? acc[b] : fmaf(v[b], factor, acc[b]);
+    slot = slot == (uint32_t)((S - 1) * stage) ? 0 : slot + stage;
+    --todo;
+    k += kStep;
+  }
+  // what is under way goes nowhere, but must not be when the LDS is used again
+  wait_loads<0>();
+  if constexpr (ACROSS) asm volatile("s_barrier" ::: "memory");
+}
+
+// The experts' network: gate/up, then down.  Blocks take tickets, each a run of items, and wait for
+// h only when no gate/up ticket is left: all of those are then done or held by blocks that run and
+// wait for nothing, so every wait ends, however few of the blocks are on the GPU at once.
+template <class W, int S, bool ACROSS>
+__global__ void __launch_bounds__(kThreads) few_kernel(const FewKern a) {
+  extern __shared__ __attribute__((aligned(1024))) char smem_dyn[];
+  __shared__ int ticket;
+  const int tid = threadIdx.x;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  int32_t* const take_up = a.counters;
+  int32_t* const done_up = a.counters + 32;
+  int32_t* const take_down = a.counters + 64;
+  auto take = [&](int32_t* p) {
+    return __hip_atomic_fetch_add(p, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  };
+  int mine = 0, down = 0;
+  if (tid == 0) {
+    mine = take(take_up);
+    down = take(take_down);
+  }
+  const Routing r = few_routing(a, smem_dyn + a.lds, blockIdx.x == 0);
+  const int up_items = r.count * (a.F / few_columns(false, ACROSS));
+  const int down_items = r.count > 0 ? a.d / few_columns(true, ACROSS) * a.chunks : 0;
+  const int up_tickets = min(up_items, a.tickets), down_tickets = min(down_items, a.tickets);
+  auto share = [&](int t) {  // thread 0's ticket, to all threads
+    __syncthreads();
+    if (tid == 0) ticket = t;
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(ticket);
+  };
+  for (int t = share(mine); t < up_tickets; t = share(mine)) {
+    few_items<W, S, ACROSS, false>(a, r, smem_dyn, up_items, t, up_tickets, 1, [] {});
+    if (tid == 0) mine = take(take_up);
+    // every wave's part of h has left it
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (tid == 0) {
+      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+      __hip_atomic_fetch_add(done_up, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+  }
+  for (int t = share(down); t < down_tickets; t = share(down)) {
+    few_items<W, S, ACROSS, true>(a, r, smem_dyn, down_items, t, down_tickets, a.chunks, [&] {
+      // (one wave's acquire is the block's: the others come behind it by the barrier, on the same L1;
+      // an acquire drops the XCD's whole L2, and one of every wave took 12 us)
+      if (wave == 0) {
+        if (tid == 0) wait_for(done_up, up_tickets);
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+      }
+      asm volatile("s_barrier" ::: "memory");
+    });
+    if (tid == 0) down = take(take_down);
   }
 }
 
@@ -610,53 +869,61 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewKern a) {
 // ---------------------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------------------
-template <class T>
+template <class T, int TT>
 static hipError_t run_logits(const FewArgs& a, hipStream_t s) {
-  const T* x = (const T*)a.x;
-  const T* w = (const T*)a.w_router;
-  const int n = (int)a.T, d = (int)a.d, E = (int)a.E;
-  const unsigned grid = (unsigned)a.E;
-  if (n <= 1)
-    few_logits_kernel<T, 1><<<grid, 256, 0, s>>>(x, w, a.bias, a.logits, n, d, E);
-  else if (n <= 4)
-    few_logits_kernel<T, 4><<<grid, 256, 0, s>>>(x, w, a.bias, a.logits, n, d, E);
-  else
-    few_logits_kernel<T, 16><<<grid, 256, 0, s>>>(x, w, a.bias, a.logits, n, d, E);
+  const dim3 grid((unsigned)a.E, (unsigned)std::max<int64_t>(1, (a.T + TT - 1) / TT));
+  few_logits_kernel<T, TT><<<grid, 256, 0, s>>>(
+      (const T*)a.x, (const T*)a.w_router, a.bias, a.logits, (int)a.T, (int)a.d, (int)a.E,
+      a.counters, kFewCounters + (int)(a.d / 16));
   return hipGetLastError();
 }
 
-template <class W, class P, bool DOWN>
-static hipError_t run_half(const FewKern& k, hipStream_t s) {
-  const int lds = P::kLds + few_routing_bytes(k.T, k.k, k.E);
-  hipError_t e = hipFuncSetAttribute((const void*)few_kernel<W, P, DOWN>,
+template <class W, int S, bool ACROSS>
+static hipError_t run_few(FewKern k, hipStream_t s) {
+  k.lds = ring_bytes<W, ACROSS>(k.tp, S) + (ACROSS ? 16 : kSumBytes);
+  const int lds = k.lds + few_routing_bytes(k.T, k.k, k.E);
+  hipError_t e = hipFuncSetAttribute((const void*)few_kernel<W, S, ACROSS>,
                                      hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;
-  constexpr int cols = DOWN ? 16 * P::RT : 8 * P::RT;
-  const int64_t items = DOWN ? k.d / cols
-                             : (int64_t)few_active_max(k.T, k.k, k.E) * (k.F / cols);
+  // Down's column tiles are cut along the reduction where they are too few for the CUs, or leave
+  // many idle in a last round; each wave keeps two units at least.
+  const int tiles = k.d / few_columns(true, ACROSS);
+  const int most = std::min<int>(
+      kFewChunks, std::max(1, k.k * (k.F * W::kElt / 128) / (2 * (ACROSS ? 4 : kWaves))));
+  auto busy = [&](int n) {
+    const int rounds = (tiles * n + kSplitCUs - 1) / kSplitCUs;
+    return (double)(tiles * n) / (rounds * kSplitCUs);
+  };
+  k.chunks = 1;
+  for (int n = 2; n <= most && busy(k.chunks) < 0.85; ++n)
+    if (busy(n) > busy(k.chunks)) k.chunks = n;
+  const int64_t up =
+      (int64_t)few_active_max(k.T, k.k, k.E) * (k.F / few_columns(false, ACROSS));
+  const int64_t items = std::max<int64_t>(up, (int64_t)tiles * k.chunks);
+  k.tickets = kSplitCUs;
   const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(items, kSplitCUs));
-  few_kernel<W, P, DOWN><<<grid, kThreads, lds, s>>>(k);
+  few_kernel<W, S, ACROSS><<<k.T ? grid : 1, kThreads, lds, s>>>(k);
   return hipGetLastError();
 }
 
-template <class W, class P>
-static hipError_t run_few(const FewKern& k, hipStream_t s) {
-  const hipError_t e = run_half<W, P, false>(k, s);
-  return e != hipSuccess || k.T == 0 ? e : run_half<W, P, true>(k, s);
-}
-
-template <class W, int G8, int G16>
-static hipError_t run_few_tokens(const FewKern& k, hipStream_t s) {
-  // more than eight tokens: two weight tiles share the rows they are multiplied with
-  if (k.T <= 8) return run_few<W, FewTile<W, 8, 1, G8>>(k, s);
-  return run_few<W, FewTile<W, 16, 2, G16>>(k, s);
+template <class W>
+static hipError_t run_few_tokens(FewKern k, hipStream_t s) {
+  k.tp = k.T <= 1 ? 1 : k.T <= 2 ? 2 : k.T <= 4 ? 4 : k.T <= 8 ? 8 : 16;
+  if (k.T > 8) return run_few<W, 6, kAcross>(k, s);
+  // the deepest ring that a CU's LDS holds
+  const int room = 160 * 1024 - 4096 - kSumBytes - few_routing_bytes(k.T, k.k, k.E);
+  if (ring_bytes<W, kAlong>(k.tp, 6) <= room) return run_few<W, 6, kAlong>(k, s);
+  if (ring_bytes<W, kAlong>(k.tp, 5) <= room) return run_few<W, 5, kAlong>(k, s);
+  if (ring_bytes<W, kAlong>(k.tp, 4) <= room) return run_few<W, 4, kAlong>(k, s);
+  return run_few<W, 3, kAlong>(k, s);
 }
 
 hipError_t launch_few(const FewArgs& a, hipStream_t s) {
-  if (a.T > 0) {
-    const hipError_t e = a.dtype == 1 ? run_logits<bf16>(a, s) : run_logits<float>(a, s);
-    if (e != hipSuccess) return e;
-  }
+  const bool one = a.T <= 1;
+  const hipError_t e = a.dtype == 1 ? one ? run_logits<bf16, 1>(a, s) : run_logits<bf16, 4>(a, s)
+                       : one        ? run_logits<float, 1>(a, s)
+                                    : run_logits<float, 4>(a, s);
+  if (e != hipSuccess) return e;
   FewKern k = {};
   k.x = a.x;
   k.logits = a.logits;
@@ -679,10 +946,13 @@ hipError_t launch_few(const FewArgs& a, hipStream_t s) {
   k.n_groups = a.n_groups;
   k.topk_groups = a.topk_groups;
   k.slot_major = a.slot_major;
-  if (a.scale_type == kScaleF32) return run_few_tokens<W8<4>, 4, 3>(k, s);
-  if (a.scale_type == kScaleE8M0) return run_few_tokens<W8<1>, 4, 3>(k, s);
-  if (a.dtype == 1) return run_few_tokens<W16, 8, 4>(k, s);
-  return run_few_tokens<W32, 8, 4>(k, s);
+  k.partial = a.partial;
+  k.counters = a.counters;
+  k.tile_done = a.counters + kFewCounters;
+  if (a.scale_type == kScaleF32) return run_few_tokens<W8<4>>(k, s);
+  if (a.scale_type == kScaleE8M0) return run_few_tokens<W8<1>>(k, s);
+  if (a.dtype == 1) return run_few_tokens<W16>(k, s);
+  return run_few_tokens<W32>(k, s);
 }
 
 }  // namespace moe

@@ -226,6 +226,9 @@ hipError_t launch_linear_grad(int dtype, int act, const void* dy, const void* z,
 // the whole layer for a few tokens
 // ---------------------------------------------------------------------------------------
 constexpr int64_t kFewTokens = 16, kFewPairs = 512;
+// counters of tickets, each in a line of its own, before those of the column tiles; the most
+// chunks of the down product's reduction
+constexpr int kFewCounters = 96, kFewChunks = 32;
 struct FewArgs {
   int dtype, scale_type;  // scale_type < 0: weights of dtype
   const void* x;          // [T, d]
@@ -236,6 +239,8 @@ struct FewArgs {
   const void* w_scale[3];
   float* logits;          // [T, E]
   void* h;                // [T k, F]
+  float* partial;         // [kFewChunks][T, d]
+  int32_t* counters;      // kFewCounters + d / 16
   void* out;              // [T, d]
   int32_t* routed;        // nullable, as the three below
   int32_t* kept;

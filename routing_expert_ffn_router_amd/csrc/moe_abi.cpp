@@ -984,13 +984,14 @@ int check_few_shape(const moe_shape* s) {
 }
 
 struct FewLayout {
-  int64_t h, total;  // the logits come first
+  int64_t counters, h, partial, total;  // the logits come first
 };
 FewLayout few_layout(const moe_shape* s) {
   FewLayout L;
-  L.h = align_up(s->T * s->E * 4);
-  L.total = L.h + align_up(s->T * s->k * s->F * elt_bytes(s->dtype));
-  if (L.total == 0) L.total = kAlign;  // a size of 0 says that the shape is invalid
+  L.counters = align_up(s->T * s->E * 4);
+  L.h = L.counters + align_up((moe::kFewCounters + s->d / 16) * 4);
+  L.partial = L.h + align_up(s->T * s->k * s->F * elt_bytes(s->dtype));
+  L.total = L.partial + align_up(moe::kFewChunks * s->T * s->d * 4);
   return L;
 }
 
@@ -1019,6 +1020,8 @@ int few_layer(const moe_shape* s, int scale_type, const void* x, const void* w_r
   }
   a.logits = static_cast<float*>(ws);
   a.h = static_cast<char*>(ws) + L.h;
+  a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + L.partial);
+  a.counters = reinterpret_cast<int32_t*>(static_cast<char*>(ws) + L.counters);
   a.out = out;
   a.routed = routed_counts;
   a.kept = tokens_per_expert;
