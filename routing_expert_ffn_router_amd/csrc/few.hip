@@ -256,7 +256,7 @@ __device__ inline bool few_select(const float* __restrict__ row, const float* __
 // counts.
 __device__ inline Routing few_routing(const FewKern& a, char* smem, bool report) {
   __shared__ uint32_t group_key[kWaves][kWave];
-  __shared__ int scan[17];
+  __shared__ uint64_t masks[1024 / kWave];
   __shared__ int tally[66 + 1];  // drops, then status
   const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
   const int T = a.T, E = a.E, k = a.k, pairs = T * k, most = few_active_max(T, k, E);
@@ -343,19 +343,28 @@ __device__ inline Routing few_routing(const FewKern& a, char* smem, bool report)
     if (a.drops && tid < k + 2) a.drops[tid] = tally[tid];
     if (a.status && tid == 0) *a.status = tally[66];
   }
-  // experts with tokens, in order
-  int count = 0;
-  for (int e0 = 0; e0 < E; e0 += kThreads) {
-    const int e = e0 + tid;
+  // experts with tokens, in order: a mask of each 64 experts
+  constexpr int kMasks = 1024 / kWave;
+#pragma unroll
+  for (int m = wave; m < kMasks; m += kWaves) {
+    const int e = m * kWave + lane;
     bool any = false;
     if (e < E) {
       const u32x4 v = slot4[e];
       any = (v[0] | v[1] | v[2] | v[3]) != 0;
     }
-    int total;
-    const int at = count + block_exclusive_scan(any ? 1 : 0, scan, &total);
-    if (any) r.active[at] = (uint16_t)e;
-    count += total;
+    const uint64_t mask = __ballot(any);
+    if (lane == 0) masks[m] = mask;
+  }
+  __syncthreads();
+  int count = 0;
+#pragma unroll 1
+  for (int m = 0; m * kWave < E; ++m) {
+    const uint64_t mask = masks[m];
+    if (m % kWaves == wave && ((mask >> lane) & 1))
+      r.active[count + __builtin_popcountll(mask & ((1ull << lane) - 1))] =
+          (uint16_t)(m * kWave + lane);
+    count += __builtin_popcountll(mask);
   }
   __syncthreads();
   r.count = __builtin_amdgcn_readfirstlane(count);
@@ -455,16 +464,16 @@ __device__ inline void wait_loads() {
 // all units, and the block shares the rows.
 constexpr bool kAlong = false, kAcross = true;
 
-// LDS of one stage of the ring, of one wave (along) or of the block (across): weight rows of one unit,
-// tp tokens' rows, scales (a word for gate or down and one for up).
-template <class W, bool ACROSS>
+// A unit is U * 128 bytes of each of 16 weight rows.  LDS of one stage of the ring, of one wave (along)
+// or of the block (across): weight rows of one unit, tp tokens' rows, scales (a word for each 128
+// bytes of gate or down, and of up).
+template <class W, int U, bool ACROSS>
 __host__ __device__ constexpr int stage_bytes(int tp) {
-  return ACROSS ? kWaves * (2048 + (W::kScale ? 16 : 0)) + tp * W::kXBytes
-                : 2048 + (W::kScale ? 16 : 0) + tp * W::kXBytes;
+  return (ACROSS ? kWaves : 1) * (U * 2048 + (W::kScale ? 16 : 0)) + U * tp * W::kXBytes;
 }
-template <class W, bool ACROSS>
+template <class W, int U, bool ACROSS>
 __host__ __device__ constexpr int ring_bytes(int tp, int stages) {
-  return (ACROSS ? 1 : kWaves) * stages * stage_bytes<W, ACROSS>(tp);
+  return (ACROSS ? 1 : kWaves) * stages * stage_bytes<W, U, ACROSS>(tp);
 }
 constexpr int kSumBytes = 2 * kWaves * 1024;  // along: two items' sums
 // columns of an item: gate and up rows of the same columns make up the sixteen
@@ -474,11 +483,10 @@ __host__ __device__ constexpr int few_columns(bool down, bool across) {
 
 // Items first, first + stride, ... of gate/up or of down.  ready(): called once, when the first
 // weights are under way and before h is read.
-template <class W, int S, bool ACROSS, bool DOWN, class Ready>
+template <class W, int U, int S, bool ACROSS, bool DOWN, class Ready>
 __device__ __attribute__((always_inline)) inline void few_items(const FewKern& a, const Routing& r,
                                                                 char* smem, int items, int first,
-                                                                int stride, int chunks,
-                                                                Ready&& ready) {
+                                                                int stride, Ready&& ready) {
   typedef typename W::X X;
   typedef X x4 __attribute__((ext_vector_type(4)));
   constexpr int ES = W::kScale, NX = W::kXBytes / 128;
@@ -488,21 +496,21 @@ __device__ __attribute__((always_inline)) inline void few_items(const FewKern& a
   const uint32_t slot_tab = lds_address(r.slot), gate_tab = lds_address(r.gate_of),
                  active_tab = lds_address(r.active);
 
-  const int K = DOWN ? a.F : a.d, N = DOWN ? a.d : a.F, tp = a.tp;
+  const int K = DOWN ? a.F : a.d, N = DOWN ? a.d : a.F, tp = a.tp, chunks = DOWN ? a.chunks : 1;
   constexpr int kCols = few_columns(DOWN, ACROSS);
-  const int per_k = K * W::kElt / 128, tiles = N / kCols;
+  const int per_k = (int)((uint32_t)K * W::kElt / (128u * U)), tiles = (int)((uint32_t)N / kCols);
   const int units = DOWN ? r.count * per_k : per_k;
   const uint32_t pitch = (uint32_t)K * W::kElt, x_pitch = (uint32_t)K * (uint32_t)sizeof(X);
   const int64_t matrix = (int64_t)N * pitch;
   constexpr uint32_t kNone = 0x80000000u;  // past a resource's end: loads as zeros
 
   // A stage: this wave's weight rows, then (along: its, across: the block's) tokens' rows and scales.
-  // Load i brings eight rows of 128 bytes; the 16-byte piece p of row n lies in slot p ^ ((n >> 1) & 7),
-  // which keeps a fragment's reads free of bank conflicts.
-  const int stage = stage_bytes<W, ACROSS>(tp);
+  // A weight load brings eight rows of 128 bytes; the 16-byte piece p of row n lies in slot
+  // p ^ ((n >> 1) & 7), which keeps a fragment's reads free of bank conflicts.
+  const int stage = stage_bytes<W, U, ACROSS>(tp);
   lds_char* const ring = (lds_char*)smem + (ACROSS ? 0 : wave * S * stage);
-  const int w_at = ACROSS ? wave * 2048 : 0, x_at = ACROSS ? kWaves * 2048 : 2048;
-  const int s_at = x_at + tp * W::kXBytes + (ACROSS ? wave * 16 : 0);
+  const int w_at = ACROSS ? wave * (U * 2048) : 0, x_at = (ACROSS ? kWaves : 1) * (U * 2048);
+  const int s_at = x_at + U * tp * W::kXBytes + (ACROSS ? wave * 16 : 0);
   const uint32_t ring_lds = lds_address(smem) + (ACROSS ? 0 : wave * S * stage);
   uint32_t vw[2];
 #pragma unroll
@@ -531,9 +539,9 @@ __device__ __attribute__((always_inline)) inline void few_items(const FewKern& a
     }
   }
 
-  // Along, each wave takes every eighth unit: together they read a kilobyte of each row at a time.
+  // Along, each wave takes every eighth unit: together they read whole kilobytes of each row.
   constexpr int kStep = ACROSS ? 1 : kWaves;
-  auto item_units = [&](int q, int* u0) {  // how many this wave has, and the first
+  auto item_units = [&](int q, int* u0) __attribute__((always_inline)) {  // how many this wave has, and the first
     int from = 0, len = units;
     if constexpr (DOWN) {  // (at most 2^24 units and 32 chunks)
       const uint32_t n = (uint32_t)q / (uint32_t)tiles;
@@ -544,83 +552,120 @@ __device__ __attribute__((always_inline)) inline void few_items(const FewKern& a
       from += wave;
       len = max(len - wave + kWaves - 1, 0) / kWaves;
     }
-    *u0 = from;
-    return len;
+    // (in scalar registers: a quotient is not)
+    *u0 = __builtin_amdgcn_readfirstlane(from);
+    return __builtin_amdgcn_readfirstlane(len);
+  };
+  // A place in the stream of units: item q, `left` units to go when the run began, unit k of the rows
+  // of the at-th expert there; a run ends with the item or the expert.
+  struct Place {
+    int q, left, run, at, k;
+  };
+  // from the end of a run to the next one; false: no item has units any more.  done(q): item q ended
+  auto next_run = [&](Place& p, auto&& done) __attribute__((always_inline)) {
+    p.left -= p.run;
+    p.k += p.run * kStep;
+#pragma unroll 1
+    while (p.left == 0) {
+      done(p.q);
+      p.q += stride;
+      if (p.q >= items) return false;
+      int u0;
+      p.left = item_units(p.q, &u0);
+      p.at = __builtin_amdgcn_readfirstlane(
+          (int)(DOWN ? (uint32_t)u0 / (uint32_t)per_k : (uint32_t)p.q / (uint32_t)tiles));
+      p.k = DOWN ? u0 - p.at * per_k : u0;
+    }
+    if constexpr (DOWN) {
+#pragma unroll 1
+      while (p.k >= per_k) {
+        p.k -= per_k;
+        ++p.at;
+      }
+      p.run = min(p.left, (int)((uint32_t)(per_k - p.k + kStep - 1) / kStep));
+    } else {
+      p.run = p.left;
+    }
+    return true;
   };
 
-  // The unit that is loaded next: of item q, `left` units to go, unit k of the rows of the at-th
-  // expert, to stage `slot`.  Past the last item there is none: its loads go nowhere and give zeros,
-  // so that every step issues as many loads and the waits count a constant.
-  struct Load {
-    int q, left, k, at, slot;
+  // Loading.  Past the last item the loads go nowhere and give zeros, so that every step issues as
+  // many loads and the waits count a constant.
+  const Place start = {first - stride, 0, 0, 0, 0};
+  Place l = start;
+  int l_todo = 0, l_slot = 0;  // units of the run to go; the stage
+  uint32_t l_off = 0;          // 128 bytes for each 128 of the rows
+  auto rsrc = [](uint64_t base, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(base), 0, (int)bytes, 0x00020000);
   };
-  const Load start = {first - stride, 0, 0, 0, 0};
-  Load l = start;
-  uint64_t base0 = 0, base1 = 0;
-  int64_t scale_at = 0;
-  uint32_t vx = kNone;
-  auto find = [&] {  // the expert's matrices and rows, of another item or expert
-    while (l.left == 0 && l.q < items) {
-      l.q += stride;
-      if (l.q >= items) return;
-      int u0;
-      l.left = item_units(l.q, &u0);
-      l.at = DOWN ? (int)((uint32_t)u0 / (uint32_t)per_k) : (int)((uint32_t)l.q / (uint32_t)tiles);
-      l.k = DOWN ? u0 - l.at * per_k : u0;
-    }
-    while (DOWN && l.k >= per_k) {
-      l.k -= per_k;
-      ++l.at;
-    }
+  const uint64_t x_base = uniform_u64(DOWN ? a.h : a.x);
+  // (below 2^31)
+  const uint32_t x_bytes = (uint32_t)(DOWN ? a.T * a.k : a.T) * x_pitch;
+  const auto rx = rsrc(x_base, x_bytes);
+  auto r0 = rx, r1 = rx;
+  const char *scale0 = nullptr, *scale1 = nullptr;
+  uint32_t v0 = kNone, v1 = kNone, vx = kNone;
+  auto find = [&]() __attribute__((always_inline)) {
+    const bool live = next_run(l, [](int) {});
+    l_todo = live ? l.run : 0x7fffffff;
+    l_off = live ? (uint32_t)l.k * (U * 128u) : 0u;
+    // (none: offsets past the resources' ends)
     const int e = __builtin_amdgcn_readfirstlane((int)lds_u16(active_tab + l.at * 2));
-    const int col0 = (int)((uint32_t)l.q % (uint32_t)tiles) * kCols;
+    const int col0 =
+        __builtin_amdgcn_readfirstlane((int)((uint32_t)l.q % (uint32_t)tiles)) * kCols;
     const int64_t to = (int64_t)e * matrix +
                        (int64_t)(col0 + (ACROSS ? wave * few_columns(DOWN, false) : 0)) * pitch;
-    base0 = uniform_u64((DOWN ? a.down.q : a.gate.q) + to);
-    if constexpr (!DOWN) base1 = uniform_u64(a.up.q + to);
-    if constexpr (ES > 0) scale_at = ((int64_t)e * (N / 128) + col0 / 128) * (K / 128);
+    // sixteen rows of down, or eight of gate and eight of up
+    const uint64_t base0 = uniform_u64((DOWN ? a.down.q : a.gate.q) + to);
+    r0 = rsrc(base0, 0x7fffffff);
+    r1 = rsrc(DOWN ? base0 + 8u * pitch : uniform_u64(a.up.q + to), 0x7fffffff);
+    v0 = live ? vw[0] : kNone;
+    v1 = live ? vw[1] : kNone;
+    if constexpr (ES > 0) {
+      const int64_t at = live ? ((int64_t)e * (N / 128) + col0 / 128) * (K / 128) * ES : 0;
+      scale0 = (DOWN ? a.down.scale : a.gate.scale) + at;
+      scale1 = (DOWN ? a.down.scale : a.up.scale) + at;
+    }
     if constexpr (DOWN) {
       const int s = (int)lds_u8(slot_tab + e * 16 + min(x_row, kTokens - 1));
-      vx = s ? (uint32_t)(x_row * a.k + s - 1) * x_pitch + x_col : kNone;
+      vx = s && live ? (uint32_t)(x_row * a.k + s - 1) * x_pitch + x_col : kNone;
     } else {
-      vx = x_row < a.T ? (uint32_t)x_row * x_pitch + x_col : kNone;
+      vx = x_row < a.T && live ? (uint32_t)x_row * x_pitch + x_col : kNone;
     }
   };
-  auto load_w = [&] {
-    const int64_t most = l.q < items ? 0x7fffffff : 0;
-    const uint32_t koff = (uint32_t)l.k * 128u;
-    lds_char* to = ring + l.slot + w_at;
-    // each line is read once: past the caches
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(bounded_rsrc(base0, most), to, 16, vw[0], koff, 0, 2);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(bounded_rsrc(DOWN ? base0 : base1, most), to + 1024, 16,
-                                             vw[1], DOWN ? koff + 8u * pitch : koff, 0, 2);
-  };
-  const int64_t x_bytes = (int64_t)(DOWN ? a.T * a.k : a.T) * x_pitch;
-  const uint64_t x_base = uniform_u64(DOWN ? a.h : a.x);
-  auto load_x = [&] {
-    if (lane < x_lanes) {
-      const auto rx = bounded_rsrc(x_base, l.q < items ? x_bytes : 0);
+  auto load_w = [&]() __attribute__((always_inline)) {
+    const uint32_t off = __builtin_amdgcn_readfirstlane(l_off);
+    lds_char* to = ring + l_slot + w_at;
 #pragma unroll
-      for (int n = 0; n < NX; ++n)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, ring + l.slot + x_dst + n * tp * 128, 16, vx,
-                                                 (uint32_t)l.k * W::kXBytes + n * 128u, 0, 0);
+    for (int u = 0; u < U; ++u) {
+      // each line is read once: past the caches
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r0, to + u * 2048, 16, v0, off + u * 128u, 0, 2);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r1, to + u * 2048 + 1024, 16, v1, off + u * 128u, 0, 2);
+    }
+  };
+  auto load_x = [&]() __attribute__((always_inline)) {
+    const uint32_t off = __builtin_amdgcn_readfirstlane(l_off);
+    if (lane < x_lanes) {
+#pragma unroll
+      for (int n = 0; n < U * NX; ++n)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, ring + l_slot + x_dst + n * tp * 128, 16, vx,
+                                                 off * NX + n * 128u, 0, 0);
     }
     if constexpr (ES > 0) {
-      if (lane < 2) {  // lane 0 gate or down, lane 1 up
-        const char* p = DOWN ? a.down.scale : lane == 0 ? a.gate.scale : a.up.scale;
-        p += (l.q < items ? scale_at + l.k : 0) * ES;
+      if (lane < 2 * U) {  // gate or down, up; of each 128 bytes
+        const char* p = (lane & 1 ? scale1 : scale0) + (off / 128 + (lane >> 1)) * ES;
         __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) char*)p,
-                                         ring + l.slot + s_at, ES, 0, 0);
+                                         ring + l_slot + s_at, W::kScale == 1 ? 1 : 4, 0, 0);
       }
     }
   };
-  constexpr int kLoads = 2 + NX + (ES ? 1 : 0);
+  constexpr int kXLoads = U * NX + (ES ? 1 : 0), kLoads = 2 * U + kXLoads;
 
   // The item's end.  Along: this wave's sums to LDS, and one wave, another one each time, adds them and
   // finishes.  lane (c, g): token c, weight rows 4 g .. 4 g + 3.
   f32x4 acc = f32x4{0.f, 0.f, 0.f, 0.f};
   const uint32_t sums = lds_address(smem) + (ACROSS ? 1 : kWaves) * S * stage;
-  auto finish = [&](int q, int nth) {
+  auto finish = [&](int q, int nth) __attribute__((always_inline)) {
     f32x4 v = acc;
     acc = f32x4{0.f, 0.f, 0.f, 0.f};
     if constexpr (!ACROSS) {
@@ -699,11 +744,11 @@ __device__ __attribute__((always_inline)) inline void few_items(const FewKern& a
     }
   };
 
-  // The unit that is multiplied: of item q, `todo` to go; down: unit k of the at-th expert.
-  int q = first, nth = 0, todo = 0, k = 0, at = 0;
-  uint32_t slot = 0;
+  // The unit that is multiplied.
+  Place m = start;
+  int m_todo = 0, nth = 0;
+  uint32_t m_slot = 0;
   float gate = 1.f;
-  bool begun = false;
   // One loop, so that there is one copy of everything: a block runs much of its code once, and what
   // it has to fetch it waits for.  First the S - 1 first units' weights, then, h being ready, their
   // rows, then a step for each unit.
@@ -715,56 +760,41 @@ __device__ __attribute__((always_inline)) inline void few_items(const FewKern& a
 #pragma unroll 1
   for (;;) {
     if (phase == kSteps) {
-#pragma unroll 1
-      while (todo == 0) {
-        if (begun) {
-          finish(q, nth++);
-          q += stride;
-        }
-        begun = true;
-        if (q >= items) break;
-        int u0;
-        todo = item_units(q, &u0);
+      if (m_todo == 0) {
+        if (!next_run(m, [&](int q) {
+              if (q >= 0) finish(q, nth++);
+            }))
+          break;
+        m_todo = m.run;
         if constexpr (DOWN) {
-          at = (int)((uint32_t)u0 / (uint32_t)per_k) - 1;
-          k = u0 - at * per_k;  // (as if behind the expert before)
-        }
-      }
-      if (q >= items) break;
-      if constexpr (DOWN) {
-        if (k >= per_k) {
-          while (k >= per_k) {
-            k -= per_k;
-            ++at;
-          }
-          const int e = __builtin_amdgcn_readfirstlane((int)lds_u16(active_tab + at * 2));
+          const int e = __builtin_amdgcn_readfirstlane((int)lds_u16(active_tab + m.at * 2));
           const int s = (int)lds_u8(slot_tab + e * 16 + c);
           // a token that did not choose the expert takes nothing of it, be it infinite or NaN
           gate = s ? lds_f32(gate_tab + (s ? c * a.k + s - 1 : 0) * 4) : -1.f;
         }
       }
+      --m_todo;
       if constexpr (ACROSS) {
         if (count > 0)
-          wait_loads<(S - 2) * (kLoads - 2)>();
+          wait_loads<(S - 2) * kXLoads>();
         else
           wait_loads<kBehind * kLoads>();
         // everyone's part has landed, and everyone is done with the stage that is loaded again
         asm volatile("s_barrier" ::: "memory");
       }
     }
-    if (l.q < items && (l.left == 0 || (DOWN && l.k >= per_k))) find();
+    if (l_todo == 0) find();
+    --l_todo;
     if (phase != kRows) load_w();
     if (phase != kWeights) load_x();
-    l.slot = l.slot == (S - 1) * stage ? 0 : l.slot + stage;
-    if (l.q < items) {
-      l.k += kStep;
-      --l.left;
-    }
+    l_slot = l_slot == (S - 1) * stage ? 0 : l_slot + stage;
+    l_off += l.left ? kStep * U * 128u : 0u;
     if (phase != kSteps) {
       if (--count == 0) {
         count = S - 1;
         if (phase++ == kWeights) {
           l = start;
+          l_todo = l_slot = 0;
           ready();
         }
       }
@@ -772,37 +802,40 @@ __device__ __attribute__((always_inline)) inline void few_items(const FewKern& a
     }
     if constexpr (!ACROSS) {
       if (count > 0)
-        wait_loads<(S - 2) * (kLoads - 2) + kLoads>();
+        wait_loads<(S - 2) * kXLoads + kLoads>();
       else
         wait_loads<kBehind * kLoads>();
     }
     if (count > 0) --count;
-    u32x4 f[kFrags];
-    uint32_t from[kFrags];
+    unroll_steps<U>([&](auto UI) {
+      constexpr int u = decltype(UI)::value;
+      u32x4 f[kFrags];
+      uint32_t from[kFrags];
 #pragma unroll
-    for (int i = 0; i < kFrags; ++i) from[i] = frag[i] + slot;
-    lds_read<kFrags>(f, from);
-    f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < kFrags; ++i)
+        from[i] = frag[i] + m_slot + (i < 2 ? u * 2048 : u * NX * tp * 128);
+      lds_read<kFrags>(f, from);
+      f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int ks = 0; ks < 2; ++ks) {
-      if constexpr (W::kElt == 1) {
+      for (int ks = 0; ks < 2; ++ks) {
+        if constexpr (W::kElt == 1) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          mma_chunk(v, e4m3_to_bf16(f[ks][2 * h], f[ks][2 * h + 1]), f[2 + 2 * ks + h], bf16());
-      } else {
-        mma_chunk(v, f[ks], f[2 + ks], X());
+          for (int h = 0; h < 2; ++h)
+            mma_chunk(v, e4m3_to_bf16(f[ks][2 * h], f[ks][2 * h + 1]), f[2 + 2 * ks + h], bf16());
+        } else {
+          mma_chunk(v, f[ks], f[2 + ks], X());
+        }
       }
-    }
-    float factor = gate;
-    if constexpr (ES > 0) {
-      const float s = lds_f32(ring_lds + slot + s_at + (DOWN || g < 2 ? 0 : 4));
-      factor *= ES == 4 ? s : e8m0_value(__float_as_uint(s) & 255u);
-    }
+      float factor = gate;
+      if constexpr (ES > 0) {
+        const float s = lds_f32(ring_lds + m_slot + s_at + u * 8 + (DOWN || g < 2 ? 0 : 4));
+        factor *= ES == 4 ? s : e8m0_value(__float_as_uint(s) & 255u);
+      }
 #pragma unroll
-    for (int b = 0; b < 4; ++b) acc[b] = gate < 0.f ? acc[b] : fmaf(v[b], factor, acc[b]);
-    slot = slot == (uint32_t)((S - 1) * stage) ? 0 : slot + stage;
-    --todo;
-    k += kStep;
+      for (int b = 0; b < 4; ++b)
+        acc[b] = DOWN && gate < 0.f ? acc[b] : fmaf(v[b], factor, acc[b]);
+    });
+    m_slot = m_slot == (uint32_t)((S - 1) * stage) ? 0 : m_slot + stage;
   }
   // what is under way goes nowhere, but must not be when the LDS is used again
   wait_loads<0>();
@@ -812,7 +845,7 @@ __device__ __attribute__((always_inline)) inline void few_items(const FewKern& a
 // The experts' network: gate/up, then down.  Blocks take tickets, each a run of items, and wait for
 // h only when no gate/up ticket is left: all of those are then done or held by blocks that run and
 // wait for nothing, so every wait ends, however few of the blocks are on the GPU at once.
-template <class W, int S, bool ACROSS>
+template <class W, int U, int S, bool ACROSS>
 __global__ void __launch_bounds__(kThreads) few_kernel(const FewKern a) {
   extern __shared__ __attribute__((aligned(1024))) char smem_dyn[];
   __shared__ int ticket;
@@ -840,7 +873,7 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewKern a) {
     return __builtin_amdgcn_readfirstlane(ticket);
   };
   for (int t = share(mine); t < up_tickets; t = share(mine)) {
-    few_items<W, S, ACROSS, false>(a, r, smem_dyn, up_items, t, up_tickets, 1, [] {});
+    few_items<W, U, S, ACROSS, false>(a, r, smem_dyn, up_items, t, up_tickets, [] {});
     if (tid == 0) mine = take(take_up);
     // every wave's part of h has left it
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
@@ -851,7 +884,7 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewKern a) {
     }
   }
   for (int t = share(down); t < down_tickets; t = share(down)) {
-    few_items<W, S, ACROSS, true>(a, r, smem_dyn, down_items, t, down_tickets, a.chunks, [&] {
+    few_items<W, U, S, ACROSS, true>(a, r, smem_dyn, down_items, t, down_tickets, [&] {
       // (one wave's acquire is the block's: the others come behind it by the barrier, on the same L1;
       // an acquire drops the XCD's whole L2, and one of every wave took 12 us)
       if (wave == 0) {
@@ -878,11 +911,11 @@ static hipError_t run_logits(const FewArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <class W, int S, bool ACROSS>
+template <class W, int U, int S, bool ACROSS>
 static hipError_t run_few(FewKern k, hipStream_t s) {
-  k.lds = ring_bytes<W, ACROSS>(k.tp, S) + (ACROSS ? 16 : kSumBytes);
+  k.lds = ring_bytes<W, U, ACROSS>(k.tp, S) + (ACROSS ? 16 : kSumBytes);
   const int lds = k.lds + few_routing_bytes(k.T, k.k, k.E);
-  hipError_t e = hipFuncSetAttribute((const void*)few_kernel<W, S, ACROSS>,
+  hipError_t e = hipFuncSetAttribute((const void*)few_kernel<W, U, S, ACROSS>,
                                      hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;
   // Down's column tiles are cut along the reduction where they are too few for the CUs, or leave
@@ -902,20 +935,28 @@ static hipError_t run_few(FewKern k, hipStream_t s) {
   const int64_t items = std::max<int64_t>(up, (int64_t)tiles * k.chunks);
   k.tickets = kSplitCUs;
   const unsigned grid = (unsigned)std::max<int64_t>(1, std::min<int64_t>(items, kSplitCUs));
-  few_kernel<W, S, ACROSS><<<k.T ? grid : 1, kThreads, lds, s>>>(k);
+  few_kernel<W, U, S, ACROSS><<<k.T ? grid : 1, kThreads, lds, s>>>(k);
   return hipGetLastError();
+}
+
+template <class W, int U>
+static hipError_t run_along(const FewKern& k, hipStream_t s) {
+  // the deepest ring that a CU's LDS holds, eight units of 128 bytes for each wave at most
+  const int room = 160 * 1024 - 4096 - kSumBytes - few_routing_bytes(k.T, k.k, k.E);
+  if constexpr (U == 1) {
+    if (ring_bytes<W, U, kAlong>(k.tp, 6) <= room) return run_few<W, U, 6, kAlong>(k, s);
+    if (ring_bytes<W, U, kAlong>(k.tp, 5) <= room) return run_few<W, U, 5, kAlong>(k, s);
+  }
+  if (ring_bytes<W, U, kAlong>(k.tp, 3) <= room) return run_few<W, U, 3, kAlong>(k, s);
+  return run_few<W, U, 2, kAlong>(k, s);
 }
 
 template <class W>
 static hipError_t run_few_tokens(FewKern k, hipStream_t s) {
   k.tp = k.T <= 1 ? 1 : k.T <= 2 ? 2 : k.T <= 4 ? 4 : k.T <= 8 ? 8 : 16;
-  if (k.T > 8) return run_few<W, 6, kAcross>(k, s);
-  // the deepest ring that a CU's LDS holds
-  const int room = 160 * 1024 - 4096 - kSumBytes - few_routing_bytes(k.T, k.k, k.E);
-  if (ring_bytes<W, kAlong>(k.tp, 6) <= room) return run_few<W, 6, kAlong>(k, s);
-  if (ring_bytes<W, kAlong>(k.tp, 5) <= room) return run_few<W, 5, kAlong>(k, s);
-  if (ring_bytes<W, kAlong>(k.tp, 4) <= room) return run_few<W, 4, kAlong>(k, s);
-  return run_few<W, 3, kAlong>(k, s);
+  if (k.T > 8) return run_few<W, 1, 6, kAcross>(k, s);
+  if (W::kElt > 1 || (k.d % 256 == 0 && k.F % 256 == 0)) return run_along<W, 2>(k, s);
+  return run_along<W, 1>(k, s);
 }
 
 hipError_t launch_few(const FewArgs& a, hipStream_t s) {
