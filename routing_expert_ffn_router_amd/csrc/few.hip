@@ -399,6 +399,35 @@ __device__ inline void wait_for(const int32_t* done, int count) {
   }
 }
 
+// What one block writes for another (h, sums of chunks) goes through all caches to where every XCD sees
+// it, and is read from there; a wave waits for its own stores before the counter that tells of them is
+// raised.  (A release and an acquire instead write back and drop an XCD's whole L2, 3 us of every
+// block one after the other, and with it the weights that were fetched ahead.)
+template <class V>
+__device__ inline void store_shared(V* p, const V& v) {
+  static_assert(sizeof(V) == 8 || sizeof(V) == 16, "whole words of 64 bits");
+  typedef uint64_t words __attribute__((ext_vector_type(2)));
+  if constexpr (sizeof(V) == 8) {
+    __hip_atomic_store(reinterpret_cast<uint64_t*>(p), __builtin_bit_cast(uint64_t, v),
+                       __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  } else {
+    const words w = __builtin_bit_cast(words, v);
+    for (int i = 0; i < 2; ++i)
+      __hip_atomic_store(reinterpret_cast<uint64_t*>(p) + i, w[i], __ATOMIC_RELAXED,
+                         __HIP_MEMORY_SCOPE_AGENT);
+  }
+}
+__device__ inline f32x4 load_shared(const f32x4* p) {
+  typedef uint64_t words __attribute__((ext_vector_type(2)));
+  words w;
+  for (int i = 0; i < 2; ++i)
+    w[i] = __hip_atomic_load(reinterpret_cast<const uint64_t*>(p) + i, __ATOMIC_RELAXED,
+                             __HIP_MEMORY_SCOPE_AGENT);
+  return __builtin_bit_cast(f32x4, w);
+}
+__device__ inline void wait_stores() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+constexpr int kSharedLoad = 16;  // a buffer load's flag for it
+
 // LDS accesses that the compiler does not order behind the direct loads under way: it would wait for
 // all of those before each.  Each waits for itself.
 __device__ inline uint32_t lds_address(const void* p) {
@@ -420,9 +449,6 @@ __device__ inline uint32_t lds_u32(uint32_t at) {
   return v;
 }
 __device__ inline float lds_f32(uint32_t at) { return __uint_as_float(lds_u32(at)); }
-__device__ inline void lds_write32(uint32_t at, uint32_t v) {
-  asm volatile("ds_write_b32 %0, %1" ::"v"(at), "v"(v) : "memory");
-}
 __device__ inline void lds_write(uint32_t at, const f32x4& v) {
   asm volatile("ds_write_b128 %0, %1" ::"v"(at), "v"(v) : "memory");
 }
@@ -643,13 +669,29 @@ __device__ __attribute__((always_inline)) inline void few_items(const FewKern& a
       __builtin_amdgcn_raw_ptr_buffer_load_lds(r1, to + u * 2048 + 1024, 16, v1, off + u * 128u, 0, 2);
     }
   };
+  // While h is not ready: the lines of the next units into the L2, a lane for each line.
+  auto touch = [&]() __attribute__((always_inline)) {
+    if constexpr (!DOWN) return;
+    constexpr int kAhead = 8 / U;  // units
+    const int piece = lane >> 4;
+    u32x4 seen;
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int unit = n * (kAhead / 2) + piece / U;
+      const uint32_t to = (uint32_t)(lane & 15) * pitch + l_off + (uint32_t)(unit * kStep * U * 128) +
+                          (uint32_t)(piece % U) * 128u;
+      seen[n] = __builtin_amdgcn_raw_buffer_load_b32(r0, v0 != kNone && unit < l_todo ? to : kNone, 0, 0);
+    }
+    asm volatile("" ::"v"(seen[0]), "v"(seen[1]));
+  };
   auto load_x = [&]() __attribute__((always_inline)) {
     const uint32_t off = __builtin_amdgcn_readfirstlane(l_off);
     if (lane < x_lanes) {
 #pragma unroll
       for (int n = 0; n < U * NX; ++n)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, ring + l_slot + x_dst + n * tp * 128, 16, vx,
-                                                 off * NX + n * 128u, 0, 0);
+                                                 off * NX + n * 128u, 0,
+                                                 DOWN ? kSharedLoad : 0);
     }
     if constexpr (ES > 0) {
       if (lane < 2 * U) {  // gate or down, up; of each 128 bytes
@@ -691,37 +733,21 @@ __device__ __attribute__((always_inline)) inline void few_items(const FewKern& a
     if constexpr (DOWN) {
       const int col = tile * kCols + (ACROSS ? wave * 16 : 0) + 4 * g;
       if (chunks > 1) {
-        // the chunk's sums to the workspace; the columns' last chunk adds them in order.  (One wave's
-        // release and acquire are the block's, as at the kernel's end.)
-        float* at = a.partial + (int64_t)c * N + col;
-        const int64_t chunk = (int64_t)a.T * N;
-        if (c < a.T) *reinterpret_cast<f32x4*>(at + n * chunk) = v;
-        auto arrive = [&] {
-          int before = 0;
-          __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-          if (lane == 0)
-            before = __hip_atomic_fetch_add(a.tile_done + tile, 1, __ATOMIC_RELAXED,
-                                            __HIP_MEMORY_SCOPE_AGENT);
-          before = __builtin_amdgcn_readfirstlane(before);
-          if (before == chunks - 1) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-          return before;
-        };
-        int before;
-        if constexpr (ACROSS) {
-          // (the ring's loads end with the stores: an item is the block's last, or nearly)
-          asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-          if (wave == 0) lds_write32(sums, (uint32_t)arrive());
-          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-          before = (int)lds_u32(sums);
-        } else {
-          before = arrive();
-        }
+        // the chunk's sums to the workspace; the columns' last chunk adds them in order
+        f32x4* at = reinterpret_cast<f32x4*>(a.partial + (int64_t)c * N + col);
+        const int64_t chunk = (int64_t)a.T * N / 4;
+        if (c < a.T) store_shared(at + n * chunk, v);
+        wait_stores();
+        int before = 0;
+        if (lane == 0)
+          before = __hip_atomic_fetch_add(a.tile_done + col / 16, 1, __ATOMIC_RELAXED,
+                                          __HIP_MEMORY_SCOPE_AGENT);
         if (__builtin_amdgcn_readfirstlane(before) != chunks - 1) return;
         if (c < a.T) {
-          v = *reinterpret_cast<const f32x4*>(at);
+          v = load_shared(at);
 #pragma unroll 4
           for (int i = 1; i < chunks; ++i) {
-            const f32x4 o = *reinterpret_cast<const f32x4*>(at + i * chunk);
+            const f32x4 o = load_shared(at + i * chunk);
 #pragma unroll
             for (int b = 0; b < 4; ++b) v[b] += o[b];
           }
@@ -739,8 +765,9 @@ __device__ __attribute__((always_inline)) inline void few_items(const FewKern& a
       for (int b = 0; b < 4; ++b)  // gate rows 0..7, up rows 8..15 on the lane 32 further
         o[b] = Elt<X>::from_f32(silu_f32(v[b]) * __shfl_xor(v[b], 32, kWave));
       if (s && g < 2)
-        *reinterpret_cast<x4*>(static_cast<X*>(a.h) + (int64_t)(c * a.k + s - 1) * N +
-                               tile * kCols + (ACROSS ? wave * 8 : 0) + 4 * g) = o;
+        store_shared(reinterpret_cast<x4*>(static_cast<X*>(a.h) + (int64_t)(c * a.k + s - 1) * N +
+                                           tile * kCols + (ACROSS ? wave * 8 : 0) + 4 * g),
+                     o);
     }
   };
 
@@ -793,6 +820,7 @@ __device__ __attribute__((always_inline)) inline void few_items(const FewKern& a
       if (--count == 0) {
         count = S - 1;
         if (phase++ == kWeights) {
+          touch();
           l = start;
           l_todo = l_slot = 0;
           ready();
@@ -850,17 +878,16 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewKern a) {
   extern __shared__ __attribute__((aligned(1024))) char smem_dyn[];
   __shared__ int ticket;
   const int tid = threadIdx.x;
-  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   int32_t* const take_up = a.counters;
   int32_t* const done_up = a.counters + 32;
   int32_t* const take_down = a.counters + 64;
   auto take = [&](int32_t* p) {
     return __hip_atomic_fetch_add(p, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   };
-  int mine = 0, down = 0;
+  int mine = 0, mine_down = 0;
   if (tid == 0) {
     mine = take(take_up);
-    down = take(take_down);
+    mine_down = take(take_down);
   }
   const Routing r = few_routing(a, smem_dyn + a.lds, blockIdx.x == 0);
   const int up_items = r.count * (a.F / few_columns(false, ACROSS));
@@ -875,25 +902,17 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewKern a) {
   for (int t = share(mine); t < up_tickets; t = share(mine)) {
     few_items<W, U, S, ACROSS, false>(a, r, smem_dyn, up_items, t, up_tickets, [] {});
     if (tid == 0) mine = take(take_up);
-    // every wave's part of h has left it
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
-    if (tid == 0) {
-      __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
+    wait_stores();
+    __syncthreads();  // every wave's part of h has arrived
+    if (tid == 0)
       __hip_atomic_fetch_add(done_up, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
   }
-  for (int t = share(down); t < down_tickets; t = share(down)) {
+  for (int t = share(mine_down); t < down_tickets; t = share(mine_down)) {
     few_items<W, U, S, ACROSS, true>(a, r, smem_dyn, down_items, t, down_tickets, [&] {
-      // (one wave's acquire is the block's: the others come behind it by the barrier, on the same L1;
-      // an acquire drops the XCD's whole L2, and one of every wave took 12 us)
-      if (wave == 0) {
-        if (tid == 0) wait_for(done_up, up_tickets);
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-      }
+      if (tid == 0) wait_for(done_up, up_tickets);
       asm volatile("s_barrier" ::: "memory");
     });
-    if (tid == 0) down = take(take_down);
+    if (tid == 0) mine_down = take(take_down);
   }
 }
 
@@ -913,7 +932,7 @@ static hipError_t run_logits(const FewArgs& a, hipStream_t s) {
 
 template <class W, int U, int S, bool ACROSS>
 static hipError_t run_few(FewKern k, hipStream_t s) {
-  k.lds = ring_bytes<W, U, ACROSS>(k.tp, S) + (ACROSS ? 16 : kSumBytes);
+  k.lds = ring_bytes<W, U, ACROSS>(k.tp, S) + (ACROSS ? 0 : kSumBytes);
   const int lds = k.lds + few_routing_bytes(k.T, k.k, k.E);
   hipError_t e = hipFuncSetAttribute((const void*)few_kernel<W, U, S, ACROSS>,
                                      hipFuncAttributeMaxDynamicSharedMemorySize, lds);
