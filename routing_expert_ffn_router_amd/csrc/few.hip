@@ -958,24 +958,27 @@ static hipError_t run_few(FewKern k, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <class W, int U>
-static hipError_t run_along(const FewKern& k, hipStream_t s) {
-  // the deepest ring that a CU's LDS holds, eight units of 128 bytes for each wave at most
-  const int room = 160 * 1024 - 4096 - kSumBytes - few_routing_bytes(k.T, k.k, k.E);
-  if constexpr (U == 1) {
-    if (ring_bytes<W, U, kAlong>(k.tp, 6) <= room) return run_few<W, U, 6, kAlong>(k, s);
-    if (ring_bytes<W, U, kAlong>(k.tp, 5) <= room) return run_few<W, U, 5, kAlong>(k, s);
-  }
-  if (ring_bytes<W, U, kAlong>(k.tp, 3) <= room) return run_few<W, U, 3, kAlong>(k, s);
-  return run_few<W, U, 2, kAlong>(k, s);
+// Whether a ring fits a CU's LDS, beside what the kernel holds in static tables.
+template <class W, int U, bool ACROSS>
+static bool ring_fits(const FewKern& k, int stages) {
+  return ring_bytes<W, U, ACROSS>(k.tp, stages) + (ACROSS ? 0 : kSumBytes) +
+             few_routing_bytes(k.T, k.k, k.E) <= 160 * 1024 - 4096;
 }
 
+// The deepest ring that fits.  (Two pieces of 128 bytes a step against one: one token, 8 of 128 experts
+// of 2048 / 768 38 and 41 us; sixteen tokens, 2 of 8 of 4096 / 14336 474 and 482 us.)
 template <class W>
 static hipError_t run_few_tokens(FewKern k, hipStream_t s) {
   k.tp = k.T <= 1 ? 1 : k.T <= 2 ? 2 : k.T <= 4 ? 4 : k.T <= 8 ? 8 : 16;
-  if (k.T > 8) return run_few<W, 1, 6, kAcross>(k, s);
-  if (W::kElt > 1 || (k.d % 256 == 0 && k.F % 256 == 0)) return run_along<W, 2>(k, s);
-  return run_along<W, 1>(k, s);
+  const bool pairs = (int64_t)k.d * W::kElt % 256 == 0 && (int64_t)k.F * W::kElt % 256 == 0;
+  if (k.T > 8) {
+    if (pairs && ring_fits<W, 2, kAcross>(k, 4)) return run_few<W, 2, 4, kAcross>(k, s);
+    return run_few<W, 1, 6, kAcross>(k, s);
+  }
+  if (pairs && ring_fits<W, 2, kAlong>(k, 3)) return run_few<W, 2, 3, kAlong>(k, s);
+  if (ring_fits<W, 1, kAlong>(k, 5)) return run_few<W, 1, 5, kAlong>(k, s);
+  if (ring_fits<W, 1, kAlong>(k, 4)) return run_few<W, 1, 4, kAlong>(k, s);
+  return run_few<W, 1, 3, kAlong>(k, s);
 }
 
 hipError_t launch_few(const FewArgs& a, hipStream_t s) {
