@@ -201,7 +201,7 @@ struct LinearArgs {
   const void* x;           // [R, K]
   const void* w;           // [E, N, K]
   const int32_t* offsets;  // [E+1], nullable: one expert holds all rows
-  const int32_t* table;    // launch_tile_table of linear_plan(R, E), or null (group_needs_table)
+  const int32_t* table;    // launch_tile_table of linear_plan, or null (group_needs_table)
   const float* bias;       // [E, N], nullable
   const void* residual;    // [R, N], nullable
   void* z;                 // [R, N], nullable
@@ -209,7 +209,7 @@ struct LinearArgs {
   void* partial;           // linear_split().bytes
   int64_t R, E, N, K;
 };
-GroupPlan linear_plan(int64_t R, int64_t E);
+GroupPlan linear_plan(int64_t R, int64_t E, int64_t N, int elt);
 GroupSplit linear_split(int64_t R, int64_t E, int64_t N, int64_t K, int elt);
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s);
 

@@ -81,16 +81,20 @@ __device__ inline void finish(const LinearOut<T>& o, const float* bias_row, int6
   *reinterpret_cast<txa*>(o.y + at) = t;
 }
 
-// BM rows x 256 weight rows, 8 waves as 2 x 4, each MT x 4 MFMA tiles of 16 x 16.
-template <int BM_, int STAGES_>
+// BM rows x BN weight rows, 8 waves as WM x WN, each MT x NT MFMA tiles of 16 x 16.
+template <int BM_, int BN_, int WM_, int WN_, int STAGES_>
 struct LinearTile {
-  static constexpr int BM = BM_, BN = 256, MT = BM / 32, NT = 4;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
+  static constexpr int MT = BM / WM / 16, NT = BN / WN / 16;
   static constexpr int kStages = STAGES_;
   static constexpr int kABytes = BM * 128, kBBytes = BN * 128;
   static constexpr int kLds = kStages * (kABytes + kBBytes);
   // direct loads of 1024 bytes (eight rows) per stage and issuing wave (waves 4-7)
   static constexpr int kALoads = BM / 32, kBLoads = BN / 32;
-  static_assert(kStages >= 2 && kStages <= 4 && kLds <= 160 * 1024, "LDS of one CU");
+  // pieces of the reduction have their sums laid out for this one
+  static constexpr bool kSplits = BN == 256 && WM == 2 && WN == 4;
+  static_assert(WM * WN == 8 && MT >= 1 && NT >= 1 && BM % 32 == 0 && BN % 32 == 0, "tile");
+  static_assert(kStages >= 2 && kStages <= 6 && kLds <= 160 * 1024, "LDS of one CU");
 };
 
 // One tile: `rows` rows of x from A on, `cols` weight rows from B on, the reduction's bytes [0,
@@ -101,12 +105,14 @@ __device__ __attribute__((always_inline)) inline void linear_body(
     const T* __restrict__ A, int rows, const T* __restrict__ B, int cols, int64_t pitch, int steps,
     const LinearOut<T>& out, const float* bias_row, int64_t row0, int col0, int N,
     f32x4* __restrict__ slot, lds_char* __restrict__ a0, lds_char* __restrict__ a1,
-    lds_char* __restrict__ a2, lds_char* __restrict__ a3, lds_char* __restrict__ b0,
-    lds_char* __restrict__ b1, lds_char* __restrict__ b2, lds_char* __restrict__ b3) {
+    lds_char* __restrict__ a2, lds_char* __restrict__ a3, lds_char* __restrict__ a4,
+    lds_char* __restrict__ a5, lds_char* __restrict__ b0, lds_char* __restrict__ b1,
+    lds_char* __restrict__ b2, lds_char* __restrict__ b3, lds_char* __restrict__ b4,
+    lds_char* __restrict__ b5) {
   constexpr int MT = G::MT, NT = G::NT, S = G::kStages, nA = G::kALoads, nB = G::kBLoads;
   const int tid = tile_thread(), lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int wm = wave >> 2, wn = wave & 3;
+  const int wm = wave / G::WN, wn = wave % G::WN;
   const int c = lane & 15, g = lane >> 4;
   const bool issuer = wave >= 4;
   const int dslot = wave & 3;
@@ -194,11 +200,11 @@ __device__ __attribute__((always_inline)) inline void linear_body(
   };
   auto buf_a = [&](auto I) -> lds_char* {
     constexpr int j = decltype(I)::value % S;
-    return j == 0 ? a0 : j == 1 ? a1 : j == 2 ? a2 : a3;
+    return j == 0 ? a0 : j == 1 ? a1 : j == 2 ? a2 : j == 3 ? a3 : j == 4 ? a4 : a5;
   };
   auto buf_b = [&](auto I) -> lds_char* {
     constexpr int j = decltype(I)::value % S;
-    return j == 0 ? b0 : j == 1 ? b1 : j == 2 ? b2 : b3;
+    return j == 0 ? b0 : j == 1 ? b1 : j == 2 ? b2 : j == 3 ? b3 : j == 4 ? b4 : b5;
   };
   // Step k: stage k has landed (own loads waited for, then the barrier); A's stage k + S - 1 goes
   // out into the buffer step k - 1 finished with, B's stage k + S once every wave holds this
@@ -228,16 +234,18 @@ __device__ __attribute__((always_inline)) inline void linear_body(
   });
   // drain the loads issued past the last stage before the LDS is used again
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  if (slot) {
-    store_partial(slot, acc, live);
-    return;
+  if constexpr (G::kSplits) {
+    if (slot) {
+      store_partial(slot, acc, live);
+      return;
+    }
   }
   __syncthreads();
 
   // Epilogue through LDS, in passes of the row tiles that fit: B's fragment goes first in the
   // MFMA, so lane (c, g) holds row c of each 16-row tile and columns 4 g .. 4 g + 3.
-  constexpr int kRow = G::BN * 4;
-  constexpr int IP = std::min(MT, G::kLds / (2 * 16 * kRow));  // row tiles of a band per pass
+  constexpr int kRow = G::BN * 4, kMask = std::min(16, kRow / 16) - 1, kEights = G::BN / 8;
+  constexpr int IP = std::min(MT, G::kLds / (G::WM * 16 * kRow));  // row tiles of a band per pass
   static_assert(IP >= 1, "a row tile fits");
 #pragma unroll
   for (int i0 = 0; i0 < MT; i0 += IP) {
@@ -249,13 +257,13 @@ __device__ __attribute__((always_inline)) inline void linear_body(
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         const int piece = (wn * NT + j) * 4 + g;
-        *reinterpret_cast<lds_f32x4*>(a0 + r * kRow + ((piece ^ (r & 15)) << 4)) = acc[i0 + ii][j];
+        *reinterpret_cast<lds_f32x4*>(a0 + r * kRow + ((piece ^ (r & kMask)) << 4)) = acc[i0 + ii][j];
       }
     }
     __syncthreads();
-    // eight columns for each thread: 32 threads a row
-    for (int q = tid; q < 2 * IP * 16 * 32; q += 512) {
-      const int r = q >> 5, p = q & 31;
+    // eight columns for each thread
+    for (int q = tid; q < G::WM * IP * 16 * kEights; q += 512) {
+      const int r = q / kEights, p = q % kEights;
       const int band = r / (IP * 16), i = i0 + (r / 16) % IP;
       const int row = (band * MT + i) * 16 + (r & 15), col = p * 8;
       if (i >= MT || row >= rows || col >= cols) continue;
@@ -263,7 +271,7 @@ __device__ __attribute__((always_inline)) inline void linear_body(
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const f32x4 u = *reinterpret_cast<const lds_f32x4*>(
-            a0 + r * kRow + (((2 * p + h) ^ (r & 15)) << 4));
+            a0 + r * kRow + (((2 * p + h) ^ (r & kMask)) << 4));
 #pragma unroll
         for (int b = 0; b < 4; ++b) v[4 * h + b] = u[b];
       }
@@ -304,8 +312,10 @@ __global__ void __launch_bounds__(512) linear_kernel(const LinearKern<T> a) {
         a.w + ((int64_t)w.rt.e * a.N + col0) * a.K + at, min(a.N - col0, G::BN),
         (int64_t)a.K * sizeof(T), k1 - k0, a.out,
         a.out.bias ? a.out.bias + (int64_t)w.rt.e * a.N : nullptr, w.rt.begin, col0, a.N, slot,
-        base, base + SA, base + (S > 2 ? 2 * SA : 0), base + (S > 3 ? 3 * SA : 0), bb, bb + SB,
-        bb + (S > 2 ? 2 * SB : 0), bb + (S > 3 ? 3 * SB : 0));
+        base, base + SA, base + (S > 2 ? 2 : 0) * SA, base + (S > 3 ? 3 : 0) * SA,
+        base + (S > 4 ? 4 : 0) * SA, base + (S > 5 ? 5 : 0) * SA, bb, bb + SB,
+        bb + (S > 2 ? 2 : 0) * SB, bb + (S > 3 ? 3 : 0) * SB, bb + (S > 4 ? 4 : 0) * SB,
+        bb + (S > 5 ? 5 : 0) * SB);
     // every wave's reads of the LDS are done
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   }
@@ -348,15 +358,31 @@ __global__ void __launch_bounds__(256) linear_sum_kernel(const LinearKern<T> a) 
 // ---------------------------------------------------------------------------------------
 // launches
 // ---------------------------------------------------------------------------------------
-GroupPlan linear_plan(int64_t R, int64_t E) {
+namespace {
+enum LinearForm { kRows64, kRows128, kRows256, kFew, kSmall32 };
+LinearForm linear_form(int64_t R, int64_t E, int64_t N, int elt) {
+  const int64_t columns = (N + 255) / 256;
+  if (elt == 4) {
+    const int64_t tiles = (R + E * 127) / 128 * columns;
+    return tiles < 2 * kSplitCUs ? kSmall32 : kRows128;
+  }
+  if (R <= 32 * E) return (R + E * 63) / 64 * columns < kSplitCUs / 2 ? kFew : kRows64;
+  return R <= 128 * E ? kRows128 : kRows256;
+}
+}  // namespace
+
+GroupPlan linear_plan(int64_t R, int64_t E, int64_t N, int elt) {
+  static const int kRows[] = {64, 128, 256, 64, 64};
   GroupPlan p;
-  p.bm = R <= 32 * E ? 64 : R <= 128 * E ? 128 : 256;
+  p.bm = kRows[linear_form(R, E, N, elt)];
   p.m_max = (R + E * (p.bm - 1)) / p.bm;
   return p;
 }
 
 GroupSplit linear_split(int64_t R, int64_t E, int64_t N, int64_t K, int elt) {
-  return group_split(linear_plan(R, E), E, N, K * elt / 128, 96);
+  const LinearForm f = linear_form(R, E, N, elt);
+  if (f == kFew || f == kSmall32) return GroupSplit{1, 0};
+  return group_split(linear_plan(R, E, N, elt), E, N, K * elt / 128, 96);
 }
 
 template <class T, class G>
@@ -368,13 +394,17 @@ static hipError_t run_linear(LinearKern<T> k, int64_t m_max, hipStream_t s) {
   hipError_t e = hipFuncSetAttribute((const void*)linear_kernel<T, G>,
                                      hipFuncAttributeMaxDynamicSharedMemorySize, G::kLds);
   if (e != hipSuccess) return e;
-  // one block per CU at most, a multiple of the 8 XCDs
+  // one block for each share of a CU's LDS at most, a multiple of the 8 XCDs
   const int64_t tiles = m_max * k.n_tiles + (k.s_max > 1 ? kSplitCUs : 0);
-  const unsigned grid = (unsigned)std::min<int64_t>((tiles + 7) / 8 * 8, kSplitCUs);
+  const unsigned grid =
+      (unsigned)std::min<int64_t>((tiles + 7) / 8 * 8, 160 * 1024 / G::kLds * kSplitCUs);
   linear_kernel<T, G><<<grid, 512, G::kLds, s>>>(k);
   if ((e = hipGetLastError()) != hipSuccess || k.s_max < 2) return e;
-  linear_sum_kernel<T, G::BM><<<dim3(kSplitCUs, 8 * G::MT / 4), 256, 0, s>>>(k);
-  return hipGetLastError();
+  if constexpr (G::kSplits) {
+    linear_sum_kernel<T, G::BM><<<dim3(kSplitCUs, 8 * G::MT / 4), 256, 0, s>>>(k);
+    return hipGetLastError();
+  }
+  return hipErrorInvalidValue;
 }
 
 template <class T>
@@ -390,10 +420,17 @@ static hipError_t run_linear_type(const LinearArgs& a, hipStream_t s) {
   k.E = (int)a.E;
   k.N = (int)a.N;
   k.K = (int)a.K;
-  const GroupPlan p = linear_plan(a.R, a.E);
-  if (p.bm == 64) return run_linear<T, LinearTile<64, 4>>(k, p.m_max, s);
-  if (p.bm == 128) return run_linear<T, LinearTile<128, 3>>(k, p.m_max, s);
-  return run_linear<T, LinearTile<256, 2>>(k, p.m_max, s);
+  const int64_t m_max = linear_plan(a.R, a.E, a.N, sizeof(T)).m_max;
+  const LinearForm form = linear_form(a.R, a.E, a.N, sizeof(T));
+  if constexpr (sizeof(T) == 4) {
+    if (form == kSmall32) return run_linear<T, LinearTile<64, 64, 2, 4, 4>>(k, m_max, s);
+    return run_linear<T, LinearTile<128, 256, 2, 4, 3>>(k, m_max, s);
+  } else {
+    if (form == kFew) return run_linear<T, LinearTile<64, 32, 4, 2, 6>>(k, m_max, s);
+    if (form == kRows64) return run_linear<T, LinearTile<64, 256, 2, 4, 4>>(k, m_max, s);
+    if (form == kRows128) return run_linear<T, LinearTile<128, 256, 2, 4, 3>>(k, m_max, s);
+    return run_linear<T, LinearTile<256, 256, 2, 4, 2>>(k, m_max, s);
+  }
 }
 
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s) {

@@ -846,7 +846,9 @@ static_assert(sizeof(moe_grad) == sizeof(moe::GradTensor), "one layout");
 bool known_activation(int act) { return act >= MOE_ACT_NONE && act <= MOE_ACT_GELU_TANH; }
 
 int64_t linear_table_bytes(const moe_group_shape* g) {
-  return align_up(moe::group_table_ints(moe::linear_plan(g->rows, g->E)) * 4);
+  return align_up(moe::group_table_ints(
+                      moe::linear_plan(g->rows, g->E, g->N, elt_bytes(g->dtype))) *
+                  4);
 }
 // Forward: the tile table, then the partial sums of split tiles; backward: the sums of dz by row
 // tiles.
@@ -906,7 +908,7 @@ int moe_grouped_linear(const moe_group_shape* g, int act, const void* x,
     return MOE_ERR_ALIGNMENT;
   moe::LinearArgs a = {};
   int32_t* table = nullptr;
-  rc = group_table(g, moe::linear_plan(g->rows, g->E), expert_offsets, ws, &table, st);
+  rc = group_table(g, moe::linear_plan(g->rows, g->E, g->N, elt_bytes(g->dtype)), expert_offsets, ws, &table, st);
   if (rc != MOE_OK) return rc;
   a.dtype = g->dtype;
   a.act = act;
