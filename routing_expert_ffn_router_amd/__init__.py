@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import operator
 import os
 import re
 from typing import Optional
@@ -523,6 +524,7 @@ class _Types:
         self.scale = {MOE_SCALE_F32: self.f32,
                       MOE_SCALE_E8M0: (torch.uint8, torch.float8_e8m0fnu)}
         self.device = torch.cuda.current_device
+        self.tensor = torch.Tensor
 
 
 _types = None
@@ -773,42 +775,50 @@ def grad_workspace_size(count: int) -> int:
 
 
 def _grad_table(grads, out, ty: _Types, gpu: int):
-    """moe_grad of each gradient, as 64-bit words of an array, and their number."""
+    """moe_grad of each gradient, as 64-bit words of an array, and their number.  Checked list by
+    list, since there may be many small tensors; what is amiss is looked for afterwards."""
+    tensor, dtype_of = ty.tensor, operator.attrgetter("dtype")
+    n, acts = len(grads), ty.acts
+    table = array.array("q", bytes(32 * n))
+    lists = [grads] if out is None else [grads, out]
+    if out is not None and len(out) != n:
+        raise ValueError(f"{len(out)} outputs for {n} gradients")
+    sizes, types = list(map(tensor.numel, grads)), list(map(dtype_of, grads))
+    for i, ts in enumerate(lists):
+        if not (all(map(tensor.is_contiguous, ts)) and set(map(tensor.get_device, ts)) <= {gpu}
+                and acts.keys() >= set(types)
+                and (i == 0 or (list(map(tensor.numel, ts)) == sizes
+                                and list(map(dtype_of, ts)) == types))):
+            for j, (g, t) in enumerate(zip(grads, ts)):
+                _arg(t, f"{'output' if i else 'gradient'} {j}",
+                     (g.dtype,) if i else tuple(acts), t.shape, gpu)
+                if t.numel() != g.numel():
+                    raise ValueError(f"output {j} has {t.numel()} values, not {g.numel()}")
+        table[i::4] = array.array("q", map(tensor.data_ptr, ts))
     if out is None:
-        out = grads
-    elif len(out) != len(grads):
-        raise ValueError(f"{len(out)} outputs for {len(grads)} gradients")
-    words, acts = [], ty.acts
-    for i, (g, o) in enumerate(zip(grads, out)):
-        dt = acts.get(g.dtype, -1)
-        if dt < 0 or g.get_device() != gpu or not g.is_contiguous():
-            _arg(g, f"gradient {i}", tuple(acts), g.shape, gpu)
-        if o is not g and (o.dtype != g.dtype or o.numel() != g.numel()
-                           or o.get_device() != gpu or not o.is_contiguous()):
-            _arg(o, f"output {i}", (g.dtype,), g.shape, gpu)
-            raise ValueError(f"output {i} has {o.numel()} values for {g.numel()}")
-        words += (g.data_ptr(), o.data_ptr(), g.numel(), dt)
-    return array.array("q", words), len(words) // 4
+        table[1::4] = table[0::4]
+    table[2::4] = array.array("q", sizes)
+    table[3::4] = array.array("q", map(acts.__getitem__, types))
+    return table, n
 
 
-def _check_apart(table, count: int) -> None:
+def _check_apart(table) -> None:
     """No output overlaps another gradient or output, or its own gradient in part."""
-    spans = []
-    for i in range(count):
-        g, o, n, dt = table[4 * i:4 * i + 4]
-        if n:
-            size = n * (2 if dt == MOE_BF16 else 4)
-            spans.append((o, o + size, True))
-            if g != o:
-                spans.append((g, g + size, False))
-    spans.sort()
-    end = out_end = 0  # the furthest end so far, and that of the outputs
-    for a, b, is_out in spans:
-        if a < out_end or (is_out and a < end):
-            raise ValueError("an output overlaps another gradient")
-        end = max(end, b)
-        if is_out:
-            out_end = max(out_end, b)
+    import numpy as np
+
+    t = np.frombuffer(table, dtype=np.int64).reshape(-1, 4)
+    t = t[t[:, 2] > 0]
+    size = t[:, 2] * np.where(t[:, 3] == MOE_BF16, 2, 4)
+    apart = t[:, 0] != t[:, 1]  # gradients that are not their own outputs
+    first = np.concatenate([t[:, 1], t[apart, 0]])
+    end = first + np.concatenate([size, size[apart]])
+    is_out = np.arange(first.size) < t.shape[0]
+    order = np.argsort(first, kind="stable")
+    first, end, is_out = first[order], end[order], is_out[order]
+    before = np.maximum.accumulate(end)[:-1]
+    out_before = np.maximum.accumulate(np.where(is_out, end, 0))[:-1]
+    if np.any((first[1:] < out_before) | (is_out[1:] & (first[1:] < before))):
+        raise ValueError("an output overlaps another gradient")
 
 
 def grad_norm(grads, workspace, norm, stream=None) -> None:
@@ -827,7 +837,7 @@ def grad_clip(grads, max_norm: float, norm, out=None, stream=None) -> None:
     the tensors of `out`."""
     ty, gpu = _begin()
     table, count = _grad_table(grads, out, ty, gpu)
-    _check_apart(table, count)
+    _check_apart(table)
     _check("moe_grad_clip", load_library().moe_grad_clip(
         count, table.buffer_info()[0], max_norm, _arg(norm, "norm", ty.f32, (1,), gpu),
         _stream(stream)))
@@ -837,7 +847,7 @@ def clip_grad_norm(grads, max_norm: float, workspace, norm, out=None, stream=Non
     """grad_norm, then grad_clip by it."""
     ty, gpu = _begin()
     table, count = _grad_table(grads, out, ty, gpu)
-    _check_apart(table, count)
+    _check_apart(table)
     ws, nbytes = _workspace_arg(workspace, gpu)
     norm_ptr, s, lib = _arg(norm, "norm", ty.f32, (1,), gpu), _stream(stream), load_library()
     _check("moe_grad_norm", lib.moe_grad_norm(count, table.buffer_info()[0], ws, nbytes, norm_ptr,

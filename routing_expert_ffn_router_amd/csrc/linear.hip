@@ -32,19 +32,20 @@ struct LinearOut {
   int act;
 };
 
-// act(z) by the activation's number, the same for all lanes
-__device__ inline float act_any(int act, float z) {
+// f(tag of the activation); the same for all lanes, so that one of the copies runs.
+template <class F>
+__device__ __attribute__((always_inline)) inline void by_act(int act, F&& f) {
   switch (act) {
-    case kActRelu: return act_value<kActRelu>(z);
-    case kActSilu: return act_value<kActSilu>(z);
-    case kActGelu: return act_value<kActGelu>(z);
-    case kActGeluTanh: return act_value<kActGeluTanh>(z);
-    default: return z;
+    case kActRelu: return f(IntC<kActRelu>{});
+    case kActSilu: return f(IntC<kActSilu>{});
+    case kActGelu: return f(IntC<kActGelu>{});
+    case kActGeluTanh: return f(IntC<kActGeluTanh>{});
+    default: return f(IntC<kActNone>{});
   }
 }
 
 // C consecutive outputs (4 or 8) of row `row` from column `col` on, from their sums.
-template <class T, int C>
+template <int ACT, class T, int C>
 __device__ inline void finish(const LinearOut<T>& o, const float* bias_row, int64_t row, int N,
                               int col, const float (&sum)[C]) {
   typedef T tx __attribute__((ext_vector_type(C)));
@@ -65,12 +66,10 @@ __device__ inline void finish(const LinearOut<T>& o, const float* bias_row, int6
   if (o.z) {
 #pragma unroll
     for (int i = 0; i < C; ++i) t[i] = Elt<T>::from_f32(v[i]);
-    *reinterpret_cast<txa*>(o.z + at) = t;
+    __builtin_nontemporal_store(t, reinterpret_cast<txa*>(o.z + at));
   }
-  if (o.act != kActNone) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) v[i] = act_any(o.act, v[i]);
-  }
+  for (int i = 0; i < C; ++i) v[i] = act_value<ACT>(v[i]);
   if (o.residual) {
     const tx r = *reinterpret_cast<const txa*>(o.residual + at);
 #pragma unroll
@@ -186,7 +185,7 @@ __device__ __attribute__((always_inline)) inline void linear_body(
         for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
           for (int j = 0; j < NT; ++j) mma_chunk(acc[i][j], fb[ks][j], fa[i % RING][ks], T());
-        if constexpr (i == std::min(3, LIVE - 1)) mid();
+        if constexpr (i == std::min(1, LIVE - 1)) mid();
         if constexpr (sizeof(T) == 2) {  // the next tile's reads between this one's MFMAs
           constexpr int R = i + 2 < LIVE ? 2 : 0, M = 2 * NT;
           unroll_steps<M>([&](auto MI) {
@@ -262,21 +261,23 @@ __device__ __attribute__((always_inline)) inline void linear_body(
     }
     __syncthreads();
     // eight columns for each thread
-    for (int q = tid; q < G::WM * IP * 16 * kEights; q += 512) {
-      const int r = q / kEights, p = q % kEights;
-      const int band = r / (IP * 16), i = i0 + (r / 16) % IP;
-      const int row = (band * MT + i) * 16 + (r & 15), col = p * 8;
-      if (i >= MT || row >= rows || col >= cols) continue;
-      float v[8];
+    by_act(out.act, [&](auto act) __attribute__((always_inline)) {
+      for (int q = tid; q < G::WM * IP * 16 * kEights; q += 512) {
+        const int r = q / kEights, p = q % kEights;
+        const int band = r / (IP * 16), i = i0 + (r / 16) % IP;
+        const int row = (band * MT + i) * 16 + (r & 15), col = p * 8;
+        if (i >= MT || row >= rows || col >= cols) continue;
+        float v[8];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const f32x4 u = *reinterpret_cast<const lds_f32x4*>(
-            a0 + r * kRow + (((2 * p + h) ^ (r & kMask)) << 4));
+        for (int h = 0; h < 2; ++h) {
+          const f32x4 u = *reinterpret_cast<const lds_f32x4*>(
+              a0 + r * kRow + (((2 * p + h) ^ (r & kMask)) << 4));
 #pragma unroll
-        for (int b = 0; b < 4; ++b) v[4 * h + b] = u[b];
+          for (int b = 0; b < 4; ++b) v[4 * h + b] = u[b];
+        }
+        finish<decltype(act)::value>(out, bias_row, row0 + row, N, col0 + col, v);
       }
-      finish<T, 8>(out, bias_row, row0 + row, N, col0 + col, v);
-    }
+    });
   }
 }
 
@@ -351,7 +352,10 @@ __global__ void __launch_bounds__(256) linear_sum_kernel(const LinearKern<T> a) 
 #pragma unroll
       for (int q = 0; q < 4; ++q) v[q] += u[q];
     }
-    if (row < live) finish<T, 4>(a.out, bias_row, rt.begin + row, a.N, col + 4 * (lane >> 4), v);
+    if (row < live)
+      by_act(a.out.act, [&](auto act) {
+        finish<decltype(act)::value>(a.out, bias_row, rt.begin + row, a.N, col + 4 * (lane >> 4), v);
+      });
   }
 }
 
@@ -359,15 +363,21 @@ __global__ void __launch_bounds__(256) linear_sum_kernel(const LinearKern<T> a) 
 // launches
 // ---------------------------------------------------------------------------------------
 namespace {
+// bf16: 64, 128 or 256 rows by 256 columns by the mean rows of an expert; where 64 rows by 32 columns
+// give no more blocks than the CUs hold at once, two each, that (rows, K -> N of one expert, us in
+// 64 x 32 tiles and in the best other: 1, 4096 -> 4096 11.3 and 21.0; 33, 2048 -> 7168 9.9 and 19.4;
+// 64, 4096 -> 14336 24.3 and 32.5; 128, 4096 -> 4096 15.4 and 27.5; 64, 14336 -> 4096 39.5 and 37.4;
+// eight experts, 512 rows, 2048 -> 1408 14.5 and 22.7; 128 rows, 4096 -> 14336, where the rule takes 64
+// x 256, 186 and 185).  fp32: 128 x 256, or 64 x 64 where those are fewer than two for each CU
+// (eight experts, 1001 rows, 512 -> 1024 14 us in small and 65 in large tiles; 4096 rows, 1024 -> 1024
+// 75 and 127; one, 4096 rows, 1024 -> 4096 287 and 255).
 enum LinearForm { kRows64, kRows128, kRows256, kFew, kSmall32 };
 LinearForm linear_form(int64_t R, int64_t E, int64_t N, int elt) {
-  const int64_t columns = (N + 255) / 256;
-  if (elt == 4) {
-    const int64_t tiles = (R + E * 127) / 128 * columns;
-    return tiles < 2 * kSplitCUs ? kSmall32 : kRows128;
-  }
-  if (R <= 32 * E) return (R + E * 63) / 64 * columns < kSplitCUs / 2 ? kFew : kRows64;
-  return R <= 128 * E ? kRows128 : kRows256;
+  auto row_tiles = [&](int64_t bm) { return E * ((R + bm * E - 1) / (bm * E)); };  // of equal experts
+  if (elt == 4)
+    return row_tiles(128) * ((N + 255) / 256) < 2 * kSplitCUs ? kSmall32 : kRows128;
+  if (row_tiles(64) * (N / 32) <= 2 * kSplitCUs) return kFew;
+  return R <= 32 * E ? kRows64 : R <= 128 * E ? kRows128 : kRows256;
 }
 }  // namespace
 
