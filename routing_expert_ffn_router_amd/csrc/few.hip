@@ -491,7 +491,7 @@ __device__ inline void wait_loads() {
 constexpr bool kAlong = false, kAcross = true;
 
 // A unit is U * 128 bytes of each of 16 weight rows.  LDS of one stage of the ring, of one wave (along)
-// or of the block (across): weight rows of one unit, tp tokens' rows, scales (a word for each 128
+// or of the block (across): weight rows of one unit, tp = T tokens' rows, scales (a word for each 128
 // bytes of gate or down, and of up).
 template <class W, int U, bool ACROSS>
 __host__ __device__ constexpr int stage_bytes(int tp) {
@@ -552,7 +552,7 @@ __device__ __attribute__((always_inline)) inline void few_items(const FewKern& a
   uint32_t frag[kFrags];
   {
     auto piece = [&](int row, int p) { return (uint32_t)(row * 128 + ((p ^ ((row >> 1) & 7)) << 4)); };
-    const int xr = c & (tp - 1);
+    const int xr = min(c, tp - 1);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       frag[ks] = ring_lds + w_at + piece(c, ks * 4 + g);
@@ -969,7 +969,7 @@ static bool ring_fits(const FewKern& k, int stages) {
 // of 2048 / 768 38 and 41 us; sixteen tokens, 2 of 8 of 4096 / 14336 474 and 482 us.)
 template <class W>
 static hipError_t run_few_tokens(FewKern k, hipStream_t s) {
-  k.tp = k.T <= 1 ? 1 : k.T <= 2 ? 2 : k.T <= 4 ? 4 : k.T <= 8 ? 8 : 16;
+  k.tp = std::max(k.T, 1);
   const bool pairs = (int64_t)k.d * W::kElt % 256 == 0 && (int64_t)k.F * W::kElt % 256 == 0;
   if (k.T > 8) {
     if (pairs && ring_fits<W, 2, kAcross>(k, 4)) return run_few<W, 2, 4, kAcross>(k, s);
