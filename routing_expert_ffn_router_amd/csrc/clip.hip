@@ -7,6 +7,9 @@
 // blocks take in turn.  Squares are summed in 64 bits: a value's square cannot overflow or vanish
 // (an fp32 sum loses 1e20 and 1e-25), at no cost while HBM is the bound.  Each block leaves one
 // sum, and a last launch adds them in one order, so a norm repeats bit for bit.
+//   1.4 G bf16 values (2.8 GB): norm 490 us, 5.7 TB/s; clipping 1060 us, 5.3 TB/s.  320 small tensors: 56 us
+// in six launches, beside about 160 us in which the host checks them and fills the arguments.  (Clipping
+// from the last chunk to the first, which the norm has just read, is no faster: 1555 us either way for both.)
 #include <algorithm>
 
 #include "common.h"

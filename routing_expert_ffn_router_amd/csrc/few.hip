@@ -8,16 +8,29 @@
 // everything else is small.  No rows are packed: the matrix instruction's sixteen columns are the
 // tokens themselves, each expert is multiplied with all of them, and what a token did not choose is
 // not stored (h) or not added (out).  Every block finds the routing for itself from the logits,
-// since its cost is less than another launch's.
+// since its cost is less than another launch's.  So there are two launches: the logits, and the
+// experts' network, whose gate/up and down parts follow each other by tickets and a counter, without a
+// barrier over the grid.
 //
-// A block is eight waves on one CU that take items in turn: gate/up, 8 or 16 columns of an expert's
-// hidden layer; down, 16 or 32 output columns over all chosen experts.  The eight waves split an
-// item's reduction, counted in units of 128 bytes of a weight row.  Weights and the rows they meet
-// come in whole lines, eight rows of 128 bytes a load, into registers, one group of units ahead of
-// the one that is multiplied, across the items' borders; a wave turns them into the matrix
-// instruction's layout through its own part of the LDS, without a barrier.  At an item's end the
-// waves' sums meet in LDS, where one wave, a different one each time, adds them in wave order and
-// finishes the item, while the others go on.
+// A block is eight waves on one CU that take items in turn.  An item is sixteen weight rows (eight of
+// gate with the eight of up of the same columns, or sixteen of down over all chosen experts), or
+// eight times that for the block.  Weights and the token rows that they meet are copied straight to
+// LDS, whole 128-byte lines, into a ring of stages that runs on across the items' borders; nothing
+// of it passes through registers but a fragment before its matrix instruction.  Up to eight tokens,
+// the waves divide the reduction, each with a ring of its own and no barrier before the item's end, where
+// their sums meet in LDS and one wave, a different one each time, adds them in wave order and finishes
+// the item while the others go on.  With more tokens their rows would be half of all that is copied:
+// there the waves divide the columns and share the rows, with a barrier for each stage.
+//
+// Sums are fp32; h is rounded to x's type (the down product takes 16-bit operands, as in the layer for
+// many tokens), the output once more; the selection is by logits summed in 64 bits.
+//
+// Measured (TB/s is of the chosen experts' weights; beside it the layer for many tokens): one token, two
+// of eight experts of 4096 / 14336, bf16, 117 us, 6.0 TB/s (179); four 318 (358); eight 373 (401); sixteen
+// 475 us (456: there all eight experts are read by both and that layer's larger tiles read them
+// slightly better); sixteen tokens, eight of 256 experts of 7168 / 2048, 1308 us, 6.7 TB/s (1697); one token, eight
+// of 128 experts of 2048 / 768, 32 us (59), of which about 15 are the two launches, the routing and the wait
+// between gate/up and down.
 #include <algorithm>
 
 #include "fp8_common.h"
@@ -73,8 +86,9 @@ struct FewKern {
 // ---------------------------------------------------------------------------------------
 // router logits
 // ---------------------------------------------------------------------------------------
-// One block for each expert; a product of two bf16 (fp32) values is exact in 64 bits and so are,
-// for a logit, the sums: the selection is that of the exact logits rounded to fp32.
+// One block for each expert and four tokens.  A product of two bf16 (fp32) values is exact in 64 bits and
+// the sums lose 2^-53 of their largest term or so: the selection is that of the exact logits rounded
+// to fp32.  3 to 7 us.
 template <class T, int TT>
 __global__ void __launch_bounds__(256)
 few_logits_kernel(const T* __restrict__ x, const T* __restrict__ w, const float* __restrict__ b,
@@ -674,7 +688,7 @@ __device__ __attribute__((always_inline)) inline void few_items(const FewKern& a
     if constexpr (!DOWN) return;
     constexpr int kAhead = 8 / U;  // units
     const int piece = lane >> 4;
-    u32x4 seen;
+    uint32_t seen[2];
 #pragma unroll
     for (int n = 0; n < 2; ++n) {
       const int unit = n * (kAhead / 2) + piece / U;
@@ -965,7 +979,7 @@ static bool ring_fits(const FewKern& k, int stages) {
              few_routing_bytes(k.T, k.k, k.E) <= 160 * 1024 - 4096;
 }
 
-// The deepest ring that fits.  (Two pieces of 128 bytes a step against one: one token, 8 of 128 experts
+// The deepest ring that fits; more than eight tokens share their rows.  (Two pieces of 128 bytes a step against one: one token, 8 of 128 experts
 // of 2048 / 768 38 and 41 us; sixteen tokens, 2 of 8 of 4096 / 14336 474 and 482 us.)
 template <class W>
 static hipError_t run_few_tokens(FewKern k, hipStream_t s) {
