@@ -850,6 +850,8 @@ def clip_grad_norm(grads, max_norm: float, workspace, norm, out=None, stream=Non
     _check_apart(table)
     ws, nbytes = _workspace_arg(workspace, gpu)
     norm_ptr, s, lib = _arg(norm, "norm", ty.f32, (1,), gpu), _stream(stream), load_library()
+    # of no gradients: max_norm is refused before the norm is enqueued
+    _check("moe_grad_clip", lib.moe_grad_clip(0, None, max_norm, norm_ptr, s))
     _check("moe_grad_norm", lib.moe_grad_norm(count, table.buffer_info()[0], ws, nbytes, norm_ptr,
                                               s))
     _check("moe_grad_clip", lib.moe_grad_clip(count, table.buffer_info()[0], max_norm, norm_ptr,

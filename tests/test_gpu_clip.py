@@ -169,3 +169,17 @@ def test_refusals_of_the_binding():
         moe.grad_norm(g, None, norm)
     assert all(bool((v == 1).all()) for v in g)
     assert float(_norm([g[0], g[0]])) == pytest.approx(math.sqrt(128))  # read twice: as it says
+
+
+@pytest.mark.parametrize("bad", [-1.0, float("nan"), float("inf"), 1e39])
+def test_a_refused_limit_leaves_everything_as_it_was(bad):
+    grads = [g.cuda() for g in _grads([100, 33], 5)]
+    before = [g.clone() for g in grads]
+    ws = torch.empty(moe.grad_workspace_size(2), dtype=torch.uint8, device="cuda")
+    norm = torch.full((1,), 7.0, device="cuda")
+    for call in (lambda: moe.clip_grad_norm(grads, bad, ws, norm),
+                 lambda: moe.grad_clip(grads, bad, norm)):
+        with pytest.raises(moe.MoeError):
+            call()
+    assert float(norm) == 7.0
+    assert all(torch.equal(a, b) for a, b in zip(grads, before))
