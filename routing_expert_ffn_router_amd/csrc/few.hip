@@ -29,8 +29,8 @@
 // of eight experts of 4096 / 14336, bf16, 117 us, 6.0 TB/s (179); four 318 (358); eight 373 (401); sixteen
 // 475 us (456: there all eight experts are read by both and that layer's larger tiles read them
 // slightly better); sixteen tokens, eight of 256 experts of 7168 / 2048, 1308 us, 6.7 TB/s (1697); one token, eight
-// of 128 experts of 2048 / 768, 32 us (59), of which about 15 are the two launches, the routing and the wait
-// between gate/up and down.
+// of 128 experts of 2048 / 768, 32 us (59), of which the logits take 5 and the routing 4 (16 tokens and 256
+// experts: 7 and 11).
 #include <algorithm>
 
 #include "fp8_common.h"
@@ -979,8 +979,11 @@ static bool ring_fits(const FewKern& k, int stages) {
              few_routing_bytes(k.T, k.k, k.E) <= 160 * 1024 - 4096;
 }
 
-// The deepest ring that fits; more than eight tokens share their rows.  (Two pieces of 128 bytes a step against one: one token, 8 of 128 experts
-// of 2048 / 768 38 and 41 us; sixteen tokens, 2 of 8 of 4096 / 14336 474 and 482 us.)
+// The deepest ring that fits.  Up to eight tokens the waves divide the reduction (4 tokens, 2 of 8 of
+// 4096 / 14336: 318 us, and 362 across the columns; 8 tokens 6.6 and 6.0 TB/s; 5 tokens, 8 of 256 of 7168 /
+// 2048 6.5 either way).  With more, a wave's own copy of the rows would take as much of the LDS as its
+// weights.  (Two pieces of 128 bytes a step against one: one token, 8 of 128 experts of 2048 / 768 38 and 41
+// us; sixteen tokens, 2 of 8 of 4096 / 14336 474 and 482 us.)
 template <class W>
 static hipError_t run_few_tokens(FewKern k, hipStream_t s) {
   k.tp = std::max(k.T, 1);
