@@ -33,6 +33,7 @@
 // experts: 7 and 11).
 #include <algorithm>
 
+#include "few_walk.h"
 #include "fp8_common.h"
 #include "gemm_common.h"
 #include "kernels.h"
@@ -41,7 +42,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kWaves = 8, kThreads = kWaves * kWave, kTokens = 16;
+constexpr int kThreads = kWaves * kWave, kTokens = 16;
 
 typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
 typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
@@ -579,59 +580,14 @@ __device__ __attribute__((always_inline)) inline void few_items(const FewKern& a
     }
   }
 
-  // Along, each wave takes every eighth unit: together they read whole kilobytes of each row.
-  constexpr int kStep = ACROSS ? 1 : kWaves;
-  auto item_units = [&](int q, int* u0) __attribute__((always_inline)) {  // how many this wave has, and the first
-    int from = 0, len = units;
-    if constexpr (DOWN) {  // (at most 2^24 units and 32 chunks)
-      const uint32_t n = (uint32_t)q / (uint32_t)tiles;
-      from = (int)(n * (uint32_t)units / (uint32_t)chunks);
-      len = (int)((n + 1) * (uint32_t)units / (uint32_t)chunks) - from;
-    }
-    if constexpr (!ACROSS) {
-      from += wave;
-      len = max(len - wave + kWaves - 1, 0) / kWaves;
-    }
-    // (in scalar registers: a quotient is not)
-    *u0 = __builtin_amdgcn_readfirstlane(from);
-    return __builtin_amdgcn_readfirstlane(len);
-  };
-  // A place in the stream of units: item q, `left` units to go when the run began, unit k of the rows
-  // of the at-th expert there; a run ends with the item or the expert.
-  struct Place {
-    int q, left, run, at, k;
-  };
-  // from the end of a run to the next one; false: no item has units any more.  done(q): item q ended
-  auto next_run = [&](Place& p, auto&& done) __attribute__((always_inline)) {
-    p.left -= p.run;
-    p.k += p.run * kStep;
-#pragma unroll 1
-    while (p.left == 0) {
-      done(p.q);
-      p.q += stride;
-      if (p.q >= items) return false;
-      int u0;
-      p.left = item_units(p.q, &u0);
-      p.at = __builtin_amdgcn_readfirstlane(
-          (int)(DOWN ? (uint32_t)u0 / (uint32_t)per_k : (uint32_t)p.q / (uint32_t)tiles));
-      p.k = DOWN ? u0 - p.at * per_k : u0;
-    }
-    if constexpr (DOWN) {
-#pragma unroll 1
-      while (p.k >= per_k) {
-        p.k -= per_k;
-        ++p.at;
-      }
-      p.run = min(p.left, (int)((uint32_t)(per_k - p.k + kStep - 1) / kStep));
-    } else {
-      p.run = p.left;
-    }
-    return true;
-  };
+  typedef FewWalk<ACROSS, DOWN> Walk;
+  typedef typename Walk::Place Place;
+  constexpr int kStep = Walk::kStep;
+  const Walk walk = {items, stride, tiles, per_k, units, chunks, wave};
 
   // Loading.  Past the last item the loads go nowhere and give zeros, so that every step issues as
   // many loads and the waits count a constant.
-  const Place start = {first - stride, 0, 0, 0, 0};
+  const Place start = walk.start(first);
   Place l = start;
   int l_todo = 0, l_slot = 0;  // units of the run to go; the stage
   uint32_t l_off = 0;          // 128 bytes for each 128 of the rows
@@ -646,11 +602,12 @@ __device__ __attribute__((always_inline)) inline void few_items(const FewKern& a
   const char *scale0 = nullptr, *scale1 = nullptr;
   uint32_t v0 = kNone, v1 = kNone, vx = kNone;
   auto find = [&]() __attribute__((always_inline)) {
-    const bool live = next_run(l, [](int) {});
+    const bool live = walk.next_run(l, [](int) {});
     l_todo = live ? l.run : 0x7fffffff;
     l_off = live ? (uint32_t)l.k * (U * 128u) : 0u;
-    // (none: offsets past the resources' ends)
-    const int e = __builtin_amdgcn_readfirstlane((int)lds_u16(active_tab + l.at * 2));
+    // (not live: offsets past the resources' ends)
+    const int e =
+        __builtin_amdgcn_readfirstlane((int)lds_u16(active_tab + walk.entry(l, live) * 2));
     const int col0 =
         __builtin_amdgcn_readfirstlane((int)((uint32_t)l.q % (uint32_t)tiles)) * kCols;
     const int64_t to = (int64_t)e * matrix +
@@ -802,7 +759,7 @@ __device__ __attribute__((always_inline)) inline void few_items(const FewKern& a
   for (;;) {
     if (phase == kSteps) {
       if (m_todo == 0) {
-        if (!next_run(m, [&](int q) {
+        if (!walk.next_run(m, [&](int q) {
               if (q >= 0) finish(q, nth++);
             }))
           break;
