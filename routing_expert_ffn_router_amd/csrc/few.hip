@@ -272,7 +272,7 @@ __device__ inline bool few_select(const float* __restrict__ row, const float* __
 __device__ inline Routing few_routing(const FewKern& a, char* smem, bool report) {
   __shared__ uint32_t group_key[kWaves][kWave];
   __shared__ uint64_t masks[1024 / kWave];
-  __shared__ int tally[66 + 1];  // drops, then status
+  __shared__ int tally[66 + 2];  // drops, then status, then tokens that took expert 0 more than once
   const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave;
   const int T = a.T, E = a.E, k = a.k, pairs = T * k, most = few_active_max(T, k, E);
   Routing r;
@@ -282,7 +282,7 @@ __device__ inline Routing few_routing(const FewKern& a, char* smem, bool report)
   uint16_t* sel = r.active + most;
   u32x4* slot4 = reinterpret_cast<u32x4*>(smem);
   for (int e = tid; e < E; e += kThreads) slot4[e] = u32x4{0, 0, 0, 0};
-  if (tid < 67) tally[tid] = 0;
+  if (tid < 68) tally[tid] = 0;
   __syncthreads();
 #pragma unroll 1
   for (int t = wave; t < T; t += kWaves) {
@@ -302,38 +302,61 @@ __device__ inline Routing few_routing(const FewKern& a, char* smem, bool report)
     float sum = ex;
 #pragma unroll
     for (int o = 1; o < kWave; o <<= 1) sum += __shfl_xor(sum, o, kWave);
+    // slots without a finite logit take expert 0: the first of its slots stands in the table
+    const uint64_t zero = __ballot(lane < k && e == 0);
     if (lane < k) {
       sel[t * k + lane] = (uint16_t)e;
       r.gate_of[t * k + lane] = ex / sum;
-      r.slot[e * 16 + t] = (uint8_t)(lane + 1);
+      if (e != 0 || lane == __builtin_ctzll(zero)) r.slot[e * 16 + t] = (uint8_t)(lane + 1);
     }
     if (bad && lane == 0) atomicAdd(&tally[66], 1);
+    if ((zero & (zero - 1)) != 0 && lane == 0) atomicAdd(&tally[67], 1);
   }
   __syncthreads();
-  if (report && a.routed) {
+  const bool again = tally[67] != 0;
+  auto count_to = [&](int32_t* counts) {  // each expert's slots, without those that were dropped
     for (int e = tid; e < E; e += kThreads) {
       int n = 0;
+      if (again && e == 0) {
 #pragma unroll 1
-      for (int t = 0; t < T; ++t) n += r.slot[e * 16 + t] != 0;
-      a.routed[e] = n;
+        for (int i = 0; i < pairs; ++i) n += sel[i] == 0;
+      } else {
+#pragma unroll 1
+        for (int t = 0; t < T; ++t) n += r.slot[e * 16 + t] != 0;
+      }
+      counts[e] = n;
     }
-  }
-  if (a.C < T) {  // some may be dropped: count the earlier assignments to the same expert
+  };
+  if (report && a.routed) count_to(a.routed);
+  // some may be dropped (of expert 0's that stand in, beyond T, without a limit too): count the earlier
+  // assignments to the same expert
+  if (a.C < T || again) {
     int drop = 0;  // this thread's pairs (at most 512 of them in all)
     const int t = tid / k, j = tid - t * k;
     if (tid < pairs) {
       int before = 0;
       const int e = sel[tid];
+      if (again && e == 0) {
 #pragma unroll 1
-      for (int o = 0; o < T; ++o) {
-        const int s = r.slot[e * 16 + o];
-        if (s && (a.slot_major ? s - 1 < j || (s - 1 == j && o < t) : o < t)) ++before;
+        for (int o = 0; o < T; ++o)
+#pragma unroll 1
+          for (int i = 0; i < k; ++i)
+            if (sel[o * k + i] == 0 &&
+                (a.slot_major ? i < j || (i == j && o < t) : o < t || (o == t && i < j)))
+              ++before;
+      } else {
+#pragma unroll 1
+        for (int o = 0; o < T; ++o) {
+          const int s = r.slot[e * 16 + o];
+          if (s && (a.slot_major ? s - 1 < j || (s - 1 == j && o < t) : o < t)) ++before;
+        }
       }
       drop = before >= a.C;
     }
     __syncthreads();
     if (drop) {
-      r.slot[sel[tid] * 16 + t] = 0;
+      // (of several slots the first is dropped last, in either order)
+      if (r.slot[sel[tid] * 16 + t] == j + 1) r.slot[sel[tid] * 16 + t] = 0;
       atomicAdd(&tally[0], 1);
       atomicAdd(&tally[1 + j], 1);
       sel[tid] = 0xffff;
@@ -348,15 +371,17 @@ __device__ inline Routing few_routing(const FewKern& a, char* smem, bool report)
     __syncthreads();
   }
   if (report) {
-    if (a.kept)
-      for (int e = tid; e < E; e += kThreads) {
-        int n = 0;
-#pragma unroll 1
-        for (int t = 0; t < T; ++t) n += r.slot[e * 16 + t] != 0;
-        a.kept[e] = n;
-      }
+    if (a.kept) count_to(a.kept);
     if (a.drops && tid < k + 2) a.drops[tid] = tally[tid];
     if (a.status && tid == 0) *a.status = tally[66];
+  }
+  if (again && tid < T && r.slot[tid] != 0) {  // expert 0's slots of a token count with the first
+    float* gates = r.gate_of + tid * k;
+    float sum = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < k; ++i)
+      if (sel[tid * k + i] == 0) sum += gates[i];
+    gates[r.slot[tid] - 1] = sum;
   }
   // experts with tokens, in order: a mask of each 64 experts
   constexpr int kMasks = 1024 / kWave;
