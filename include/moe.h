@@ -22,8 +22,9 @@
  *     Index tables are int32.
  *   - Pointers are device pointers on the current HIP device unless marked "host".  Tensor
  *     pointers (x, weights, x_perm, y_perm, out) must be 16-byte aligned.
- *   - The caller owns every buffer; the library keeps no state between calls, so calls
- *     with distinct workspaces and outputs may run concurrently on different streams.
+ *   - The caller owns every buffer; the library keeps no state between calls (but for the
+ *     setting of moe_few_wait_polls), so calls with distinct workspaces and outputs may run
+ *     concurrently on different streams.
  *   - Errors: arguments are validated before anything is enqueued and a negative
  *     moe_status is returned on failure (nothing is launched).  A failed launch returns
  *     MOE_ERR_HIP.  T = 0 is valid.
@@ -677,6 +678,12 @@ int moe_layer_fp8(const moe_shape* shape, int scale_type, const void* x, const v
  * bytes.  Host function. */
 size_t moe_few_workspace_size(const moe_shape* shape);
 
+/* The number of looks, of about a microsecond each, after which a block of moe_layer_few gives up
+ * waiting for the others; 2^20 at first.  Sets it for the calls that the process makes from now on
+ * (0: every wait is given up at once) and returns the number before; a negative one only returns it.
+ * The one setting that the library keeps.  Host function. */
+int32_t moe_few_wait_polls(int32_t polls);
+
 /*
  * moe_layer_few -- moe_layer for at most MOE_FEW_MAX_TOKENS tokens, which is bound by reading the
  * chosen experts' weights once: no rows are packed and no row tiles filled.  The same layer as
@@ -684,9 +691,13 @@ size_t moe_few_workspace_size(const moe_shape* shape);
  * rounded once to fp32, so that the selection is the exact logits'; an expert's outputs are not
  * rounded before they are weighted and added (in fp32, by expert).  h is rounded to dtype.
  * MOE_FLAG_PAD_TO_CAPACITY changes nothing: there are no row slots.
+ * Blocks wait for each other's part of h by counters in the workspace.  A wait that lasts longer than
+ * any call does (moe_few_wait_polls) is given up: that takes calls that use one workspace at once,
+ * against the rules.  What depends on it in out is then NaN, and status is negative.
  *   workspace  moe_few_workspace_size() bytes, 256-byte aligned
- *   routed_counts, tokens_per_expert [E], drops [k+2], status [1] int32 out, all nullable, as in
- *              moe_layer
+ *   routed_counts, tokens_per_expert [E], drops [k+2] int32 out, all nullable, as in moe_layer
+ *   status     [1] int32 out, nullable, as in moe_layer; where a wait was given up its sign bit is
+ *              set beside that count
  * Other arguments as in moe_layer.  MOE_ERR_UNSUPPORTED outside moe_few_workspace_size's limits.
  */
 int moe_layer_few(const moe_shape* shape, const void* x, const void* w_router,

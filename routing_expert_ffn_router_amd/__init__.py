@@ -156,6 +156,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_grouped_dgrad": (i32, [_G, _P, _P, _P, _P, sz, _P, _P]),
         "moe_grouped_wgrad": (i32, [_G, _P, _P, _P, _P, sz, _P, _P]),
         "moe_few_workspace_size": (sz, [_S]),
+        "moe_few_wait_polls": (i32, [i32]),
         "moe_layer_few": (i32, [_S, _P, _P, _P, _P, _P, _P, _P, sz, _P, _P, _P, _P, _P, _P]),
         "moe_layer_few_fp8": (i32, [_S, i32, _P, _P, _P, _W, _W, _W, _P, sz, _P, _P, _P, _P, _P,
                                     _P]),
@@ -861,6 +862,14 @@ def clip_grad_norm(grads, max_norm: float, workspace, norm, out=None, stream=Non
 # -------------------------------------------------------------------- a few tokens
 def few_workspace_size(s: MoeShape) -> int:
     return int(load_library().moe_few_workspace_size(ctypes.byref(s)))
+
+
+def few_wait_polls(polls: int = -1) -> int:
+    """moe_few_wait_polls: sets how often a block looks before it gives up waiting for the others,
+    and returns the number before; a negative number only returns it."""
+    if polls >= 1 << 31:
+        raise ValueError(f"{polls} polls")
+    return int(load_library().moe_few_wait_polls(max(polls, -1)))
 
 
 def _few_common(ty: _Types, gpu: int, s: MoeShape, act: tuple, x, w_router, b_router):

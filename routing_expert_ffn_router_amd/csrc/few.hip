@@ -32,6 +32,7 @@
 // of 128 experts of 2048 / 768, 32 us (59), of which the logits take 5 and the routing 4 (16 tokens and 256
 // experts: 7 and 11).
 #include <algorithm>
+#include <atomic>
 
 #include "few_walk.h"
 #include "fp8_common.h"
@@ -81,7 +82,7 @@ struct FewKern {
   float* partial;     // [chunks][T, d]
   int32_t* counters;  // tickets and what is done, zero
   int32_t* tile_done; // [column tiles], zero
-  int T, d, E, k, F, C, n_groups, topk_groups, slot_major, chunks, tickets, tp, lds;
+  int T, d, E, k, F, C, n_groups, topk_groups, slot_major, chunks, tickets, tp, lds, polls;
 };
 
 // ---------------------------------------------------------------------------------------
@@ -94,9 +95,11 @@ template <class T, int TT>
 __global__ void __launch_bounds__(256)
 few_logits_kernel(const T* __restrict__ x, const T* __restrict__ w, const float* __restrict__ b,
                   float* __restrict__ logits, int tokens, int d, int E, int32_t* __restrict__ zero,
-                  int zeros) {
-  if (blockIdx.x == 0 && blockIdx.y == 0)  // the experts' counters
+                  int zeros, int32_t* __restrict__ status) {
+  if (blockIdx.x == 0 && blockIdx.y == 0) {  // the experts' counters
     for (int i = threadIdx.x; i < zeros; i += 256) zero[i] = 0;
+    if (status && threadIdx.x == 0) *status = 0;
+  }
   x += (int64_t)blockIdx.y * TT * d;
   logits += (int64_t)blockIdx.y * TT * E;
   tokens -= blockIdx.y * TT;
@@ -373,7 +376,8 @@ __device__ inline Routing few_routing(const FewKern& a, char* smem, bool report)
   if (report) {
     if (a.kept) count_to(a.kept);
     if (a.drops && tid < k + 2) a.drops[tid] = tally[tid];
-    if (a.status && tid == 0) *a.status = tally[66];
+    // (a block that gave up waiting may have marked it already)
+    if (a.status && tid == 0 && tally[66]) atomicOr(a.status, tally[66]);
   }
   if (again && tid < T && r.slot[tid] != 0) {  // expert 0's slots of a token count with the first
     float* gates = r.gate_of + tid * k;
@@ -429,14 +433,15 @@ __device__ inline float e8m0_value(uint32_t v) {
   return __uint_as_float(v == 0 ? 0x00400000u : v == 255 ? 0x7fc00000u : v << 23);
 }
 
-// Waits until `count` tickets are done, or long enough that something must be wrong with the
-// workspace (another call's, say): then the results are unspecified, but the kernel ends.
-__device__ inline void wait_for(const int32_t* done, int count) {
+// Waits until `count` tickets are done; false: it looked `polls` times in vain, something must be
+// wrong with the workspace (another call's, say), and the kernel ends all the same.
+__device__ inline bool wait_for(const int32_t* done, int count, int polls) {
 #pragma unroll 1
-  for (int i = 0; i < (1 << 20); ++i) {
-    if (__hip_atomic_load(done, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) >= count) break;
+  for (int i = 0; i < polls; ++i) {
+    if (__hip_atomic_load(done, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) >= count) return true;
     __builtin_amdgcn_s_sleep(2);
   }
+  return false;
 }
 
 // What one block writes for another (h, sums of chunks) goes through all caches to where every XCD sees
@@ -489,6 +494,9 @@ __device__ inline uint32_t lds_u32(uint32_t at) {
   return v;
 }
 __device__ inline float lds_f32(uint32_t at) { return __uint_as_float(lds_u32(at)); }
+__device__ inline void lds_set(uint32_t at, uint32_t v) {
+  asm volatile("ds_write_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)" ::"v"(at), "v"(v) : "memory");
+}
 __device__ inline void lds_write(uint32_t at, const f32x4& v) {
   asm volatile("ds_write_b128 %0, %1" ::"v"(at), "v"(v) : "memory");
 }
@@ -548,7 +556,7 @@ __host__ __device__ constexpr int few_columns(bool down, bool across) {
 }
 
 // Items first, first + stride, ... of gate/up or of down.  ready(): called once, when the first
-// weights are under way and before h is read.
+// weights are under way and before h and the gates are read.
 template <class W, int U, int S, bool ACROSS, bool DOWN, class Ready>
 __device__ __attribute__((always_inline)) inline void few_items(const FewKern& a, const Routing& r,
                                                                 char* smem, int items, int first,
@@ -881,6 +889,7 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewKern a) {
     return __hip_atomic_fetch_add(p, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   };
   int mine = 0, mine_down = 0;
+  bool gave_up = false;  // thread 0's
   if (tid == 0) {
     mine = take(take_up);
     mine_down = take(take_down);
@@ -905,7 +914,12 @@ __global__ void __launch_bounds__(kThreads) few_kernel(const FewKern a) {
   }
   for (int t = share(mine_down); t < down_tickets; t = share(mine_down)) {
     few_items<W, U, S, ACROSS, true>(a, r, smem_dyn, down_items, t, down_tickets, [&] {
-      if (tid == 0) wait_for(done_up, up_tickets);
+      if (tid == 0 && !gave_up && !wait_for(done_up, up_tickets, a.polls)) {
+        // without h: NaN for every gate makes NaN of every sum that h goes into
+        gave_up = true;
+        for (int i = 0; i < a.T * a.k; ++i) lds_set(lds_address(r.gate_of + i), 0x7fc00000u);
+        if (a.status) atomicOr(a.status, (int)0x80000000u);
+      }
       asm volatile("s_barrier" ::: "memory");
     });
     if (tid == 0) mine_down = take(take_down);
@@ -922,7 +936,7 @@ static hipError_t run_logits(const FewArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)a.E, (unsigned)std::max<int64_t>(1, (a.T + TT - 1) / TT));
   few_logits_kernel<T, TT><<<grid, 256, 0, s>>>(
       (const T*)a.x, (const T*)a.w_router, a.bias, a.logits, (int)a.T, (int)a.d, (int)a.E,
-      a.counters, kFewCounters + (int)(a.d / 16));
+      a.counters, kFewCounters + (int)(a.d / 16), a.status);
   return hipGetLastError();
 }
 
@@ -980,6 +994,13 @@ static hipError_t run_few_tokens(FewKern k, hipStream_t s) {
   return run_few<W, 1, 3, kAlong>(k, s);
 }
 
+// (2^20 looks of about a microsecond: a second)
+static std::atomic<int32_t> wait_polls{1 << 20};
+
+int32_t few_wait_polls(int32_t polls) {
+  return polls < 0 ? wait_polls.load() : wait_polls.exchange(polls);
+}
+
 hipError_t launch_few(const FewArgs& a, hipStream_t s) {
   const bool one = a.T <= 1;
   const hipError_t e = a.dtype == 1 ? one ? run_logits<bf16, 1>(a, s) : run_logits<bf16, 4>(a, s)
@@ -1010,6 +1031,7 @@ hipError_t launch_few(const FewArgs& a, hipStream_t s) {
   k.slot_major = a.slot_major;
   k.partial = a.partial;
   k.counters = a.counters;
+  k.polls = wait_polls.load();
   k.tile_done = a.counters + kFewCounters;
   if (a.scale_type == kScaleF32) return run_few_tokens<W8<4>>(k, s);
   if (a.scale_type == kScaleE8M0) return run_few_tokens<W8<1>>(k, s);

@@ -251,6 +251,7 @@ struct FewArgs {
   bool slot_major;
 };
 hipError_t launch_few(const FewArgs& a, hipStream_t s);
+int32_t few_wait_polls(int32_t polls);  // moe_few_wait_polls
 
 struct GradTensor {  // moe_grad
   const void* grad;

@@ -1045,6 +1045,8 @@ int few_layer(const moe_shape* s, int scale_type, const void* x, const void* w_r
 
 extern "C" {
 
+int32_t moe_few_wait_polls(int32_t polls) { return moe::few_wait_polls(polls); }
+
 size_t moe_few_workspace_size(const moe_shape* s) {
   if (check_few_shape(s) != MOE_OK) return 0;
   return (size_t)few_layout(s).total;
