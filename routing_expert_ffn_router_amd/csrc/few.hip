@@ -858,10 +858,18 @@ __device__ __attribute__((always_inline)) inline void few_items(const FewKern& a
           mma_chunk(v, f[ks], f[2 + ks], X());
         }
       }
+      // the block's scale, then the gate: their product may be below fp32's normal numbers where the
+      // scaled sum is not
       float factor = gate;
       if constexpr (ES > 0) {
-        const float s = lds_f32(ring_lds + m_slot + s_at + u * 8 + (DOWN || g < 2 ? 0 : 4));
-        factor *= ES == 4 ? s : e8m0_value(__float_as_uint(s) & 255u);
+        float s = lds_f32(ring_lds + m_slot + s_at + u * 8 + (DOWN || g < 2 ? 0 : 4));
+        if constexpr (ES == 1) s = e8m0_value(__float_as_uint(s) & 255u);
+        if constexpr (DOWN) {
+#pragma unroll
+          for (int b = 0; b < 4; ++b) v[b] *= s;
+        } else {
+          factor = s;
+        }
       }
 #pragma unroll
       for (int b = 0; b < 4; ++b)
