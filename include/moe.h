@@ -543,6 +543,11 @@ typedef enum {
  * serves both); 0 for an invalid shape.  Host function. */
 size_t moe_linear_workspace_size(const moe_group_shape* shape);
 
+/* How moe_grouped_linear cuts a shape, for profiles and tests: tiles[0] rows by tiles[1] columns of
+ * a tile, and tiles[2], the most pieces along the reduction that a tile of the last partial round
+ * is cut into (1: none is cut).  A tile holds rows of one expert.  Host function. */
+int moe_linear_tiles(const moe_group_shape* shape, int64_t tiles[3]);
+
 /*
  * moe_grouped_linear -- linear layer grouped by expert, for the rows r of expert e:
  *   z[r, n] = (sum over k of x[r, k] * w[e, n, k]) + bias[e, n],   y[r, n] = act(z[r, n]) + residual[r, n]

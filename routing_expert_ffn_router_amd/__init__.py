@@ -161,6 +161,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_layer_few_fp8": (i32, [_S, i32, _P, _P, _P, _W, _W, _W, _P, sz, _P, _P, _P, _P, _P,
                                     _P]),
         "moe_linear_workspace_size": (sz, [_G]),
+        "moe_linear_tiles": (i32, [_G, ctypes.POINTER(i64)]),
         "moe_grouped_linear": (i32, [_G, i32, _P, _P, _P, _P, _P, _P, sz, _P, _P, _P]),
         "moe_grouped_linear_grad": (i32, [_G, i32, _P, _P, _P, _P, sz, _P, _P, _P]),
         "moe_grad_workspace_size": (sz, [i64]),
@@ -737,6 +738,14 @@ class MoELayerFp8:
 # -------------------------------------------------------------------- linear layers, clipping
 def linear_workspace_size(g: MoeGroupShape) -> int:
     return int(load_library().moe_linear_workspace_size(ctypes.byref(g)))
+
+
+def linear_tiles(g: MoeGroupShape) -> tuple:
+    """moe_linear_tiles: (rows, columns) of a tile of grouped_linear and the most pieces that one of
+    the last round is cut into."""
+    tiles = (ctypes.c_int64 * 3)()
+    _check("moe_linear_tiles", load_library().moe_linear_tiles(ctypes.byref(g), tiles))
+    return tuple(tiles)
 
 
 def grouped_linear(g: MoeGroupShape, activation: int, x, expert_offsets, w, bias, residual,

@@ -210,6 +210,7 @@ struct LinearArgs {
   int64_t R, E, N, K;
 };
 GroupPlan linear_plan(int64_t R, int64_t E, int64_t N, int elt);
+int64_t linear_columns(int64_t R, int64_t E, int64_t N, int elt);  // of a tile
 GroupSplit linear_split(int64_t R, int64_t E, int64_t N, int64_t K, int elt);
 hipError_t launch_linear(const LinearArgs& a, hipStream_t s);
 

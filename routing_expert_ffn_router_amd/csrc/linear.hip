@@ -392,6 +392,11 @@ GroupPlan linear_plan(int64_t R, int64_t E, int64_t N, int elt) {
   return p;
 }
 
+int64_t linear_columns(int64_t R, int64_t E, int64_t N, int elt) {
+  const LinearForm f = linear_form(R, E, N, elt);
+  return f == kFew ? 32 : f == kSmall32 ? 64 : 256;
+}
+
 GroupSplit linear_split(int64_t R, int64_t E, int64_t N, int64_t K, int elt) {
   const LinearForm f = linear_form(R, E, N, elt);
   if (f == kFew || f == kSmall32) return GroupSplit{1, 0};

@@ -895,6 +895,17 @@ size_t moe_linear_workspace_size(const moe_group_shape* g) {
   return (size_t)linear_workspace(g);
 }
 
+int moe_linear_tiles(const moe_group_shape* g, int64_t* tiles) {
+  const int rc = check_group(g);
+  if (rc != MOE_OK) return rc;
+  if (!tiles) return MOE_ERR_INVALID_ARG;
+  const int elt = elt_bytes(g->dtype);
+  tiles[0] = moe::linear_plan(g->rows, g->E, g->N, elt).bm;
+  tiles[1] = moe::linear_columns(g->rows, g->E, g->N, elt);
+  tiles[2] = moe::linear_split(g->rows, g->E, g->N, g->K, elt).s_max;
+  return MOE_OK;
+}
+
 int moe_grouped_linear(const moe_group_shape* g, int act, const void* x,
                        const int32_t* expert_offsets, const void* w, const float* bias,
                        const void* residual, void* ws, size_t ws_bytes, void* z, void* y,
@@ -908,7 +919,8 @@ int moe_grouped_linear(const moe_group_shape* g, int act, const void* x,
     return MOE_ERR_ALIGNMENT;
   moe::LinearArgs a = {};
   int32_t* table = nullptr;
-  rc = group_table(g, moe::linear_plan(g->rows, g->E, g->N, elt_bytes(g->dtype)), expert_offsets, ws, &table, st);
+  rc = group_table(g, moe::linear_plan(g->rows, g->E, g->N, elt_bytes(g->dtype)), expert_offsets,
+                   ws, &table, st);
   if (rc != MOE_OK) return rc;
   a.dtype = g->dtype;
   a.act = act;
