@@ -45,9 +45,6 @@ namespace {
 
 constexpr int kThreads = kWaves * kWave, kTokens = 16;
 
-typedef __attribute__((address_space(3))) u32x4 lds_u32x4;
-typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
-
 // Weights' kinds.
 struct W16 {  // bf16
   typedef bf16 X;
@@ -503,13 +500,7 @@ __device__ inline void lds_write(uint32_t at, const f32x4& v) {
 // N pieces
 template <int N>
 __device__ inline void lds_read(u32x4 (&v)[N], const uint32_t (&at)[N]) {
-  static_assert(N == 2 || N == 4 || N == 6, "pieces");
-  if constexpr (N == 2)
-    asm volatile(
-        "ds_read_b128 %0, %2\n\tds_read_b128 %1, %3\n\ts_waitcnt lgkmcnt(0)"
-        : "=&v"(v[0]), "=&v"(v[1])
-        : "v"(at[0]), "v"(at[1])
-        : "memory");
+  static_assert(N == 4 || N == 6, "pieces");
   if constexpr (N == 4)
     asm volatile(
         "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_b128 %2, %6\n\t"
@@ -997,9 +988,13 @@ static hipError_t run_few_tokens(FewKern k, hipStream_t s) {
     return run_few<W, 1, 6, kAcross>(k, s);
   }
   if (pairs && ring_fits<W, 2, kAlong>(k, 3)) return run_few<W, 2, 3, kAlong>(k, s);
-  if (ring_fits<W, 1, kAlong>(k, 5)) return run_few<W, 1, 5, kAlong>(k, s);
-  if (ring_fits<W, 1, kAlong>(k, 4)) return run_few<W, 1, 4, kAlong>(k, s);
-  return run_few<W, 1, 3, kAlong>(k, s);
+  // (five stages fit beside any tables, but for 8-bit weights, whose rows take two lines a unit)
+  if constexpr (W::kScale > 0) {
+    if (!ring_fits<W, 1, kAlong>(k, 5))
+      return ring_fits<W, 1, kAlong>(k, 4) ? run_few<W, 1, 4, kAlong>(k, s)
+                                           : run_few<W, 1, 3, kAlong>(k, s);
+  }
+  return run_few<W, 1, 5, kAlong>(k, s);
 }
 
 // (2^20 looks of about a microsecond: a second)
