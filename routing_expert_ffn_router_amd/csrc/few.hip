@@ -25,12 +25,18 @@
 // Sums are fp32; h is rounded to x's type (the down product takes 16-bit operands, as in the layer for
 // many tokens), the output once more; the selection is by logits summed in 64 bits.
 //
-// Measured (TB/s is of the chosen experts' weights; beside it the layer for many tokens): one token, two
-// of eight experts of 4096 / 14336, bf16, 117 us, 6.0 TB/s (179); four 318 (358); eight 373 (401); sixteen
-// 475 us (456: there all eight experts are read by both and that layer's larger tiles read them
-// slightly better); sixteen tokens, eight of 256 experts of 7168 / 2048, 1308 us, 6.7 TB/s (1697); one token, eight
-// of 128 experts of 2048 / 768, 32 us (59), of which the logits take 5 and the routing 4 (16 tokens and 256
-// experts: 7 and 11).
+// A block that waits in vain (two calls in one workspace) makes its gates NaN and goes on, so that the
+// kernel ends and what it could not compute shows.
+//
+// Measured on one card (the number of experts read, TB/s of their weights, and the layer for many
+// tokens): bf16, two of eight experts of 4096 / 14336, one token 118 us (2, 6.0 TB/s; 195), four 318 (6,
+// 6.6; 350), eight 374 (7, 6.6; 399), nine 416 (7; 399) and sixteen 475 (8; 464: that layer's
+// 64-row tiles read few, large experts slightly better); eight of 256 of 7168 / 2048, one token
+// 122 (8, 5.8; 177), sixteen 1391 (106, 6.7; 1832); eight of 128 of 2048 / 768, one token 33 (8, 2.3; 59),
+// of which the logits take 5 and the routing 4 (sixteen tokens and 256 experts: 7 and 11).
+// e4m3 with E8M0 scales, eight of 256 of 7168 / 2048: one token 86 (8, 4.1; 118), three 191 (22; 210), four
+// 267 (30; 247), sixteen 842 (105; 739: the rows, in 16 bits, are two lines of LDS for each line of
+// weights, and an LDS instruction meets 1.9 cycles of bank conflicts).
 #include <algorithm>
 #include <atomic>
 
@@ -974,11 +980,13 @@ static bool ring_fits(const FewKern& k, int stages) {
              few_routing_bytes(k.T, k.k, k.E) <= 160 * 1024 - 4096;
 }
 
-// The deepest ring that fits.  Up to eight tokens the waves divide the reduction (4 tokens, 2 of 8 of
-// 4096 / 14336: 318 us, and 362 across the columns; 8 tokens 6.6 and 6.0 TB/s; 5 tokens, 8 of 256 of 7168 /
-// 2048 6.5 either way).  With more, a wave's own copy of the rows would take as much of the LDS as its
-// weights.  (Two pieces of 128 bytes a step against one: one token, 8 of 128 experts of 2048 / 768 38 and 41
-// us; sixteen tokens, 2 of 8 of 4096 / 14336 474 and 482 us.)
+// The deepest ring that fits.  Up to eight tokens the waves divide the reduction, with more, a wave's
+// own copy of the rows would take as much of the LDS as its weights (us along and across, bf16: two of
+// eight of 4096 / 14336, one token 118 and 137, four 319 and 361, eight 374 and 417; eight of 128 of
+// 2048 / 768, one 34 and 45, eight 101 and 120; eight of 256 of 7168 / 2048, eight 797 and 787).  Two
+// pieces of 128 bytes a step against one: one token, eight of 256 of 7168 / 2048 121 and 123 us, eight of
+// 128 of 2048 / 768 33.7 and 33.8, six of 64 of 2048 / 1408 37.2 and 36.6; sixteen, two of eight of
+// 4096 / 14336 422 and 426.
 template <class W>
 static hipError_t run_few_tokens(FewKern k, hipStream_t s) {
   k.tp = std::max(k.T, 1);

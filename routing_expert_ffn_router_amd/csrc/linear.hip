@@ -2,8 +2,8 @@
 // rows r of expert e, bf16 and fp32, with everything behind the product in its epilogue.
 //
 // Both operands are rows contiguous along the reduction, which go through LDS in stages of 128 bytes
-// of each row (64 bf16 values, 32 fp32), BM activation rows and 256 weight rows, by direct buffer ->
-// LDS loads; the 16-byte piece c of row r lies in slot c ^ ((r >> 1) & 7), which keeps a fragment's
+// of each row (64 bf16 values, 32 fp32), BM activation rows and BN weight rows (256, or 32 and 64 where
+// tiles are few), by direct buffer -> LDS loads; the 16-byte piece c of row r lies in slot c ^ ((r >> 1) & 7), which keeps a fragment's
 // reads free of bank conflicts.  A stage's weight fragments are read into registers first and their
 // LDS is released and loaded again, two steps ahead, while the activations' stream through
 // registers.  Sums are fp32 (fp32 operands: fp32 MFMA).  A block fills its CU's LDS and works through
@@ -14,7 +14,9 @@
 // grouped products; the launch that adds their sums applies the epilogue.
 //   Large bf16 products are bound by the matrix cores: 8192 rows, 4096 -> 14336, 709 us alone (1357
 // TFLOP/s; the library's product 702) and 785 with bias, gelu and z kept, whose stores and slopes the
-// next tile's loads do not cover; few rows by HBM: 33, 2048 -> 7168, 9.9 us for 29 MB of weights.
+// next tile's loads do not cover.  Few rows are bound by latency: 33, 2048 -> 7168, 10 us for 29 MB of
+// weights, 2.9 TB/s, since each block goes through 32 dependent steps of two barriers, and only half of
+// its waves issue loads.
 #include <algorithm>
 
 #include "act.h"
