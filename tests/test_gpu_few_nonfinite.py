@@ -125,3 +125,22 @@ def test_groups_without_enough_finite_logits(capacity, flags):
     c["w_router"][[1, 3, 5, 7]] = float("nan")
     c["x"][6, 0] = float("nan")
     _check(c, capacity, flags, (4, 2))
+
+
+@pytest.mark.parametrize("capacity,flags", [(0, 0), (1, moe.MOE_FLAG_SLOT_MAJOR)])
+@pytest.mark.parametrize("lost", [[1, 2, 3, 4], [0, 1, 2, 3, 4], [1, 3]])
+def test_one_token(lost, capacity, flags):
+    """One place and several slots of expert 0: the first of them is kept."""
+    c = _case(1, 5, 4, seed=21 + len(lost))
+    c["w_router"][lost] = float("nan")
+    ok, bad = _check(c, capacity, flags)
+    assert bool(bad.all()) and bool(ok.all()) == (0 not in lost)
+
+
+@pytest.mark.parametrize("T", [2, 16])
+def test_most_slots_and_experts(T):
+    c = _case(T, 1024, 512 // 16, seed=T, F=128)
+    c["w_router"][20:] = float("nan")
+    c["x"][1, 5] = float("nan")
+    for capacity, flags in ((0, 0), (3, 0), (T, moe.MOE_FLAG_SLOT_MAJOR)):
+        _check(c, capacity, flags)
